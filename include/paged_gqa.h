@@ -317,6 +317,33 @@ int paged_gqa_workspace_size_host(pgd_pool_t pool, int B, int q_len, int Hq, int
                                   int num_splits, size_t *bytes);
 
 /*
+ * Attention of a ragged batch of query tokens over the pages: prompts, chunks of
+ * prompts behind a cached prefix, and cross attention to the cached states of an
+ * encoder, of another length than the queries.
+ *   q, out       [total, Hq, D] bfloat16 rows, q rows `q_stride` elements apart (heads
+ *                contiguous, 16-byte aligned), out contiguous and apart from q
+ *   cu_seqlens   [B + 1] int32: sequence b owns rows cu_seqlens[b] .. cu_seqlens[b+1] - 1
+ *                (ascending, cu_seqlens[B] <= total; none is fine).  Rows past
+ *                cu_seqlens[B] are left as they were
+ *   seq_lens     [B] int32, cached tokens per sequence
+ *   causal       1: the n_b queries of a sequence are its last n_b cached tokens, already
+ *                written; query i sits at p = Lb - n_b + i and attends to [lo, p], lo =
+ *                max(0, p - window + 1) when window > 0, else 0 (p < 0: nothing).
+ *                0: every query attends to all Lb cached tokens (window must be 0);
+ *                n_b and Lb are independent
+ * A query that attends to nothing gets zeros.  Blocks that lie wholly before every
+ * query's window are never read.  Cached keys and values are expected to be finite where a
+ * query of the sequence may attend to them; slots past Lb may hold anything.
+ * bfloat16 and 8-bit pools (PGD_ERR_UNSUPPORTED for float32).  No workspace.  Sequences
+ * whose cu_seqlens or length is impossible latch PGD_ERR_SEQ_LEN, block ids out of range
+ * PGD_ERR_BLOCK_ID; the rows that would have read them are written as NaN.
+ */
+int paged_gqa_attend(pgd_pool_t pool, const void *q, int64_t q_stride, int total, int Hq,
+                     const int32_t *cu_seqlens, int B, const int32_t *block_table,
+                     int max_blocks, const int32_t *seq_lens, int causal, int window,
+                     float scale, void *out, void *stream);
+
+/*
  * Diagnostic of the failure path: launch one thread that waits, with the
  * bounded wait the pipeline kernels use and a limit of limit_us microseconds
  * (1 .. 1e6), on a barrier nothing arrives on.  The wait gives up, latches

@@ -1,6 +1,7 @@
 /*
  * paged_kv_manager.h -- the KV write path of libpaged_gqa.so: a host block
- * manager for the paged cache and the device kernels that store new tokens and
+ * manager for the paged cache and the device kernels that store new tokens
+ * (quantising, with the norm and rotation of a projection), read them back and
  * copy blocks.
  *
  * Sources: blocks are allocated only when a sequence needs a new one and are
@@ -110,6 +111,85 @@ int paged_kv_copy_blocks(pgd_pool_t pool, const int32_t *src, const int32_t *dst
  */
 int paged_kv_append(pgd_pool_t pool, const void *k_new, const void *v_new,
                     const int32_t *slot_mapping, int n, void *stream);
+
+/*
+ * Ragged batches.  The three calls below take the new tokens of B sequences as
+ * packed rows: sequence b owns rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (device
+ * int32 [B + 1], ascending, cu_seqlens[B] <= total), and they are its last n_b =
+ * cu_seqlens[b+1] - cu_seqlens[b] cached tokens: row i of it is the token at
+ * position seq_lens[b] - n_b + i, found through block_table [B, max_blocks].  n_b may
+ * be 0.  `total` is the rows the packed tensors have room for; rows past
+ * cu_seqlens[B] are neither read as tokens nor written (a padded batch).  Rows are
+ * [Hkv, D] (queries [Hq, D]) contiguous, `*_stride` elements apart (a view of a
+ * packed projection is fine), 16-byte aligned, stride too.  Activations are float32
+ * for float32 pools and bfloat16 for all others.  total = 0 or B = 0 does nothing.
+ *
+ * A sequence with an impossible length (cu_seqlens descending or past total, seq_lens
+ * outside [0, max_blocks * block_size], more rows than cached tokens, a position past
+ * the rotation table) latches PGD_ERR_SEQ_LEN: none of its tokens is stored and its
+ * output rows are NaN.  A block id outside [0, num_blocks) latches PGD_ERR_BLOCK_ID:
+ * the tokens of that block are not stored, or read back as NaN.
+ */
+
+/*
+ * Device: store K and V rows in the pages, quantised as they are written.
+ *   float32 and bfloat16 pages: copies.
+ *   8-bit pages, scale per KV head: code = x / k_scale[h], rounded to the nearest code
+ *     (ties to even) and saturated (e4m3 +-448, int8 +-127); the scales are read only.
+ *   8-bit pages, scale per block and KV head: the call also sets the scale of every
+ *     block it writes to the largest of max|x| / 448 (127 for int8; the product with the
+ *     rounded reciprocal) over the rows it
+ *     stores there and, where the block already holds earlier tokens of the sequence
+ *     (the first row is not at slot 0), the block's scale before the call.  If that
+ *     grows the scale, the earlier tokens' codes are rounded again at the new scale (at
+ *     most half a code step each time).  A block written from slot 0 on takes its scale
+ *     from this call alone.  A largest magnitude whose scale would be below 2^-126 gives
+ *     scale 0 and codes 0.  The handle's scale arrays are written.
+ * Infinities and NaN take no part in a block's scale; an infinity saturates (in a
+ * block of scale 0 it counts as a NaN), a NaN is stored as the NaN code of e4m3 and
+ * as 0 in int8.
+ * Slots of a call must be distinct: blocks shared by several sequences are copied
+ * first (paged_kv_copy_blocks), also partly filled ones that this call adds to.
+ */
+int paged_kv_write(pgd_pool_t pool, const void *k, int64_t k_stride, const void *v,
+                   int64_t v_stride, int total, const int32_t *cu_seqlens, int B,
+                   const int32_t *block_table, int max_blocks, const int32_t *seq_lens,
+                   void *stream);
+
+/*
+ * Device: read the last n_b cached tokens of every sequence back as packed rows,
+ * k_out and v_out [total, Hkv, D] contiguous in the activations' type; 8-bit pages
+ * are dequantised (code * scale, rounded once).  A range [s, e) of a sequence is read
+ * with seq_lens = e and n = e - s.
+ */
+int paged_kv_read(pgd_pool_t pool, void *k_out, void *v_out, int total,
+                  const int32_t *cu_seqlens, int B, const int32_t *block_table, int max_blocks,
+                  const int32_t *seq_lens, void *stream);
+
+/*
+ * Device: the norm of queries and keys for each head, their rotation by position, and
+ * the write of K and V, in one pass.
+ *   norm      y = x / sqrt(mean(x^2) + eps) * weight over the D elements of a head, for
+ *             queries with q_weight and keys with k_weight ([D], weight_dtype PGD_F32 or
+ *             PGD_BF16); a null weight: no norm of that side
+ *   rotation  of the first rope_dim elements of every query and key head by the angles of
+ *             the token's position p: rope is [rope_len, 2, rope_dim / 2] float32, cosines
+ *             then sines; pairs (a, b) = elements (j, j + rope_dim / 2), or (2j, 2j + 1)
+ *             with interleaved = 1, become (a cos - b sin, b cos + a sin).  rope_dim: a
+ *             multiple of 16, at most D.  rope null: no rotation
+ *   q, q_out  [total, Hq, D] rows; q_out may be q itself, or other columns of one packed
+ *             row, but may not overlap q in any other way
+ * Everything is computed in float32 and rounded once: to q_out's type, or to the pages'
+ * (8-bit codes and block scales come from the float32 values, by the rules of
+ * paged_kv_write).  Values are stored as paged_kv_write stores them.
+ */
+int paged_qk_norm_rope_write(pgd_pool_t pool, const void *q, int64_t q_stride, void *q_out,
+                             int64_t q_out_stride, int Hq, const void *k, int64_t k_stride,
+                             const void *v, int64_t v_stride, int total, const void *q_weight,
+                             const void *k_weight, int weight_dtype, float eps,
+                             const float *rope, int rope_len, int rope_dim, int interleaved,
+                             const int32_t *cu_seqlens, int B, const int32_t *block_table,
+                             int max_blocks, const int32_t *seq_lens, void *stream);
 
 #ifdef __cplusplus
 }

@@ -12,7 +12,9 @@ import torch
 
 from . import _lib
 from ._lib import PagedGQAError, STATUS_NAMES, strerror  # noqa: F401
-from .kv_cache import KVBlockManager, paged_kv_append, paged_kv_copy_blocks  # noqa: F401
+from .kv_cache import (KVBlockManager, paged_gqa_attend, paged_kv_append,  # noqa: F401
+                       paged_kv_copy_blocks, paged_kv_read, paged_kv_write,
+                       paged_qk_norm_rope_write, rope_table)
 
 __all__ = [
     "PagedKVPool", "PagedGQAError", "paged_kv_pool_create", "paged_kv_pool_destroy",
@@ -21,6 +23,8 @@ __all__ = [
     "paged_gqa_decode_noalloc", "paged_gqa_noalloc_scratch_bytes",
     "paged_gqa_decode_host", "paged_gqa_workspace_size_host", "paged_gqa_plan",
     "strerror", "decode", "KVBlockManager", "paged_kv_append", "paged_kv_copy_blocks",
+    "paged_kv_write", "paged_kv_read", "paged_qk_norm_rope_write", "rope_table",
+    "paged_gqa_attend",
 ]
 
 _DTYPES = {torch.float32: _lib.PGD_F32, torch.bfloat16: _lib.PGD_BF16}
@@ -74,6 +78,7 @@ class PagedKVPool:
         self.k_pool, self.v_pool = k_pool, v_pool
         self.num_blocks, self.block_size, self.num_kv_heads, self.head_dim = k_pool.shape
         self.dtype = k_pool.dtype
+        self.device = k_pool.device
         self.q_dtype = torch.bfloat16 if fp8 else k_pool.dtype
         self.k_scale, self.v_scale = k_scale, v_scale
         self.scale_per_block = False

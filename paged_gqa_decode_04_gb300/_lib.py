@@ -104,6 +104,18 @@ def load(path=LIB_PATH):
     lib.pgd_kvm_ref_count.argtypes = [vp, i64, pint]
     lib.paged_kv_copy_blocks.argtypes = [vp, vp, vp, i32, vp]
     lib.paged_kv_append.argtypes = [vp, vp, vp, vp, i32, vp]
+    # ragged batches (both headers)
+    rag = [i32, vp, i32, vp, i32, vp]   # total, cu_seqlens, B, block_table, max_blocks, seq_lens
+    lib.paged_kv_write.argtypes = [vp, vp, i64, vp, i64] + rag + [vp]
+    lib.paged_kv_read.argtypes = [vp, vp, vp] + rag + [vp]
+    lib.paged_qk_norm_rope_write.argtypes = (
+        [vp, vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, vp, vp, i32, ctypes.c_float, vp, i32,
+         i32, i32] + rag[1:] + [vp])
+    lib.paged_gqa_attend.argtypes = ([vp, vp, i64, i32, i32] + rag[1:] +
+                                     [i32, i32, ctypes.c_float, vp, vp])
+    for name in ("paged_kv_write", "paged_kv_read", "paged_qk_norm_rope_write",
+                 "paged_gqa_attend"):
+        getattr(lib, name).restype = i32
     for name in ("pgd_kvm_create", "pgd_kvm_destroy", "pgd_kvm_add_sequence", "pgd_kvm_fork",
                  "pgd_kvm_free_sequence", "pgd_kvm_append_slots", "pgd_kvm_block_tables",
                  "pgd_kvm_num_free", "pgd_kvm_ref_count", "paged_kv_copy_blocks",

@@ -23,7 +23,8 @@ SOURCES = ["api.cpp", "block_manager.cpp", "decode_simple.cu", "decode_tma_d64.c
            "decode_tma_i8.cu", "decode_tma_i8_share.cu", "decode_tma_i8_sep.cu",
            "decode_tma_fp8pb.cu", "decode_tma_fp8pb_share.cu", "decode_tma_fp8pb_sep.cu",
            "decode_tma_i8pb.cu", "decode_tma_i8pb_share.cu", "decode_tma_i8pb_sep.cu",
-           "kv_write.cu", "merge.cu", "noalloc.cu", "selftest.cu"]
+           "kv_write.cu", "kv_quant.cu", "kv_read.cu", "attend.cu", "merge.cu", "noalloc.cu",
+           "selftest.cu"]
 
 
 def nvcc():

@@ -1,0 +1,159 @@
+// paged_kv_read: the last n_b cached tokens of every sequence of a ragged batch as
+// packed rows, 8-bit pages dequantised (y = code * scale in float32, rounded once).
+//
+// What bounds it: bytes, every page row read once and every output row written once.
+// A token's row of all KV heads is contiguous on both sides, so a warp takes 4
+// consecutive tokens' K and V rows and has 8 loads of 16 bytes a lane in flight; the
+// sequence is searched and checked once a warp.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "page_ops.h"
+#include "paged_kv_manager.h"
+#include "ragged.cuh"
+
+namespace pgd {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kTokens = 4;  // tokens of a warp
+
+struct ReadArgs {
+    Ragged r;
+    const void* k_pool;
+    const void* v_pool;
+    const float* k_scale;
+    const float* v_scale;
+    int scale_per_block;
+    int hkv, d;
+    void* k_out;
+    void* v_out;
+};
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 16 bytes of a page row as output: 16 codes to 16 bfloat16, else a copy.
+template <int PAGE>
+__device__ __forceinline__ void emit(void* out, int64_t vec, uint4 x, float scale) {
+    if (PAGE != PGD_FP8_E4M3 && PAGE != PGD_INT8) {
+        static_cast<uint4*>(out)[vec] = x;
+        return;
+    }
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t two = w[i / 2] >> (16 * (i % 2));
+        float2 f;
+        if (PAGE == PGD_INT8)
+            f = make_float2(float(int8_t(two)), float(int8_t(two >> 8)));
+        else
+            f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(two),
+                                                                  __NV_E4M3)));
+        o[i] = bf16x2(f.x * scale, f.y * scale);
+    }
+    uint4* p = static_cast<uint4*>(out) + 2 * vec;
+    p[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+template <int PAGE>
+__global__ void __launch_bounds__(kWarps * 32) read_kernel(const ReadArgs a) {
+    constexpr bool q8 = PAGE == PGD_FP8_E4M3 || PAGE == PGD_INT8;
+    constexpr int elt = PAGE == PGD_F32 ? 4 : PAGE == PGD_BF16 ? 2 : 1;
+    constexpr uint32_t nan2 = PAGE == PGD_F32 ? 0x7fc00000u : 0x7fc07fc0u;
+    if (blockIdx.x == 0) check_all(a.r, true);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTokens;
+    if (t0 >= a.r.total) return;
+    const int row_vec = a.hkv * a.d * elt / 16;  // 16-byte vectors of a page row
+    int64_t slot[kTokens];  // pool row of token t0 + i, -1: NaN row, -2: not written
+    int64_t blk[kTokens];
+    int b = find_seq(a.r, t0, 1, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        slot[i] = -2;
+        blk[i] = 0;
+        const int64_t t = t0 + i;
+        if (t >= a.r.total) continue;
+        if (i && b < a.r.B && t >= __ldg(a.r.cu + b + 1)) b = find_seq(a.r, t, 1, 0, 0);
+        if (b >= a.r.B) continue;
+        const Seq s = load_seq(a.r, b);
+        if (t < s.row0) continue;
+        slot[i] = -1;
+        if (!s.ok || s.n > s.len || t >= s.row0 + s.n) continue;
+        const int pos = s.len - s.n + int(t - s.row0);
+        blk[i] = block_of(a.r, b, pos / a.r.block_size);
+        if (blk[i] >= 0) slot[i] = blk[i] * a.r.block_size + pos % a.r.block_size;
+        blk[i] = max(blk[i], (int64_t)0);
+    }
+    const uint4* kp = static_cast<const uint4*>(a.k_pool);
+    const uint4* vp = static_cast<const uint4*>(a.v_pool);
+    for (int j = lane; j < row_vec; j += 32) {
+        uint4 x[2 * kTokens];
+        float sc[2 * kTokens];
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) {
+            x[2 * i] = x[2 * i + 1] = make_uint4(nan2, nan2, nan2, nan2);
+            sc[2 * i] = sc[2 * i + 1] = NAN;
+            if (slot[i] >= 0) {
+                x[2 * i] = __ldg(kp + slot[i] * row_vec + j);
+                x[2 * i + 1] = __ldg(vp + slot[i] * row_vec + j);
+                if (q8) {
+                    const int64_t h = j * 16 / a.d + (a.scale_per_block ? blk[i] * a.hkv : 0);
+                    sc[2 * i] = __ldg(a.k_scale + h);
+                    sc[2 * i + 1] = __ldg(a.v_scale + h);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) {
+            if (slot[i] == -2) continue;
+            emit<PAGE>(a.k_out, (t0 + i) * row_vec + j, x[2 * i], sc[2 * i]);
+            emit<PAGE>(a.v_out, (t0 + i) * row_vec + j, x[2 * i + 1], sc[2 * i + 1]);
+        }
+    }
+}
+
+}  // namespace
+}  // namespace pgd
+
+using namespace pgd;
+
+extern "C" int paged_kv_read(pgd_pool_t pool, void* k_out, void* v_out, int total,
+                             const int32_t* cu_seqlens, int B, const int32_t* block_table,
+                             int max_blocks, const int32_t* seq_lens, void* stream) {
+    if (!pool) return PGD_ERR_ARG;
+    const Pool& p = pool_desc(pool);
+    int rc = check_ragged(p, total, cu_seqlens, B, block_table, max_blocks, seq_lens);
+    if (rc != PGD_OK || B == 0 || total == 0) return rc;
+    const int64_t width = (int64_t)p.hkv * p.d;
+    rc = check_rows(k_out, width, width, act_bytes(p));
+    if (rc == PGD_OK) rc = check_rows(v_out, width, width, act_bytes(p));
+    if (rc != PGD_OK) return rc;
+    const char* ko = static_cast<char*>(k_out);
+    const char* vo = static_cast<char*>(v_out);
+    const int64_t bytes = width * act_bytes(p) * total;
+    if (ko < vo + bytes && vo < ko + bytes) return PGD_ERR_ARG;  // the outputs overlap
+    const int cap = max_blocks * p.block_size;
+    const ReadArgs a = {{cu_seqlens, block_table, seq_lens, B, total, max_blocks, p.block_size,
+                         p.num_blocks, cap, p.err},
+                        p.k, p.v, p.k_scale, p.v_scale, p.scale_per_block, p.hkv, p.d, k_out,
+                        v_out};
+    OnDevice dev(p.device);
+    if (!dev.ok) return PGD_ERR_CUDA;
+    const unsigned ctas = unsigned(((int64_t)total + kWarps * kTokens - 1) / (kWarps * kTokens));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p.dtype == PGD_F32)
+        read_kernel<PGD_F32><<<ctas, kWarps * 32, 0, s>>>(a);
+    else if (p.dtype == PGD_BF16)
+        read_kernel<PGD_BF16><<<ctas, kWarps * 32, 0, s>>>(a);
+    else if (p.dtype == PGD_FP8_E4M3)
+        read_kernel<PGD_FP8_E4M3><<<ctas, kWarps * 32, 0, s>>>(a);
+    else
+        read_kernel<PGD_INT8><<<ctas, kWarps * 32, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? PGD_OK : PGD_ERR_CUDA;
+}
