@@ -7,11 +7,13 @@
 
 #include <new>
 
+#include "page_maps.h"
 #include "paged_kv_manager.h"
 #include "pgd_internal.h"
 
 struct pgd_pool_s {
     pgd::Pool p;
+    pgd::PageMaps maps;
 };
 
 namespace pgd {
@@ -87,6 +89,24 @@ bool encode_pool_map(CUtensorMap* map, const void* base, int64_t num_blocks, int
     return r == CUDA_SUCCESS;
 }
 
+// 4-D view of a pool of 128-byte rows, (row, slot, row of the token, block), with a box
+// of one row of a token for the slots of one block, 128 slots at most.
+bool encode_row_map(CUtensorMap* map, const void* base, int64_t num_blocks, int bs, int hkv,
+                    int d, bool q8) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t elems = q8 ? 128 : 64;
+    const cuuint64_t token = (cuuint64_t)hkv * d * (q8 ? 1 : 2);  // bytes of a token's row
+    cuuint64_t dims[4] = {elems, (cuuint64_t)bs, token / 128, (cuuint64_t)num_blocks};
+    cuuint64_t strides[3] = {token, 128, token * bs};
+    cuuint32_t box[4] = {(cuuint32_t)elems, (cuuint32_t)(bs < 128 ? bs : 128), 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int resolve_parts(const Pool& p, int num_splits) {
     return num_splits > 0 ? num_splits : p.num_sms;
 }
@@ -94,6 +114,7 @@ int resolve_parts(const Pool& p, int num_splits) {
 }  // namespace
 
 const Pool& pool_desc(pgd_pool_t h) { return h->p; }
+const PageMaps& page_maps(pgd_pool_t h) { return h->maps; }
 
 static int choose_hg_for(int dtype, int hkv, int rows) {
     if (dtype == PGD_F32) return 1;
@@ -261,6 +282,14 @@ static int pool_create(pgd_pool_t* out, const void* k_pool, const void* v_pool,
                 return PGD_ERR_CUDA;
             }
             p.tmap_ok[i] = true;
+        }
+        if (!encode_row_map(&h->maps.k, k_pool, num_blocks, block_size, num_kv_heads, head_dim,
+                            fp8) ||
+            !encode_row_map(&h->maps.v, v_pool, num_blocks, block_size, num_kv_heads, head_dim,
+                            fp8)) {
+            cudaFree(p.err);
+            delete h;
+            return PGD_ERR_CUDA;
         }
     }
     *out = h;

@@ -4,11 +4,16 @@
 //
 //     out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale <q, k_t> - m), m = max_t,
 //
-// in one pass over the tokens with a running maximum and sum in float32.  One warp per
-// (query token, query head); a lane holds D / 32 elements.
+// in one pass over the tokens with a running maximum and sum in float32.  bfloat16 pools
+// take the tensor-core kernel (attend_tc.cuh), 8-bit pools one warp per (query token,
+// query head), a lane holding D / 32 elements.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
+
+#include "attend_tc.cuh"
+#include "page_maps.h"
 #include "page_ops.h"
 #include "ragged.cuh"
 
@@ -111,6 +116,39 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simple_kernel(const Attend
             __float2bfloat16(inv == 0.f ? 0.f : o[i] * inv);
 }
 
+// CTAs that share the keys of a block of rows: as many as the GPU has room for while
+// each has two tiles of the longest sequence the table can hold.
+int choose_cluster(const Pool& p, int64_t units, int64_t max_tokens) {
+    int c = 1;
+    while (c < 8 && units * c * 2 <= p.num_sms && max_tokens >= (int64_t)c * 4 * attend::kTile)
+        c *= 2;
+    return c;
+}
+
+template <int D>
+cudaError_t launch_tc(const attend::Args& a, const Pool& p, const PageMaps& maps, cudaStream_t s) {
+    using namespace attend;
+    static std::atomic<uint64_t> ready{0};  // devices whose function attributes are set
+    if (!(ready.load() >> p.device & 1)) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(uint64_t(1) << p.device);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = a.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(unsigned(a.pieces) * a.hkv * a.cluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Layout<D>::kBytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, attend_kernel<D>, a, maps.k, maps.v);
+}
+
 }  // namespace
 }  // namespace pgd
 
@@ -140,6 +178,35 @@ extern "C" int paged_gqa_attend(pgd_pool_t pool, const void* q, int64_t q_stride
             return PGD_ERR_ARG;  // out aliases q
     }
     const int cap = max_blocks * p.block_size;
+    const int group = Hq / p.hkv;
+    if ((int64_t)total * group > INT32_MAX / 2) return PGD_ERR_SHAPE;
+    const int64_t pieces = max_pieces(total, B, group, attend::kRowShift, 1);
+    if (pieces * p.hkv * 8 > INT32_MAX) return PGD_ERR_SHAPE;
+    OnDevice dev(p.device);
+    if (!dev.ok) return PGD_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p.dtype == PGD_BF16) {
+        attend::Args t = {};
+        t.r = {cu_seqlens, block_table, seq_lens, B, total, max_blocks, p.block_size,
+               p.num_blocks, cap, p.err};
+        t.hq = Hq;
+        t.hkv = p.hkv;
+        t.group = group;
+        t.q = static_cast<const __nv_bfloat16*>(q);
+        t.q_stride = q_stride;
+        t.out = static_cast<__nv_bfloat16*>(out);
+        t.causal = causal;
+        t.window = window;
+        // a scale below zero turns the queries' sign, one of zero leaves no query
+        t.scale_log2 = scale != 0.f ? fabsf(scale) * 1.4426950408889634f : 1.f;
+        t.q_and = scale != 0.f ? 0xffffffffu : 0u;
+        t.q_xor = scale < 0.f ? 0x80008000u : 0u;
+        t.pieces = int(pieces);
+        t.cluster = choose_cluster(p, pieces * p.hkv, cap);
+        const cudaError_t e = p.d == 64 ? launch_tc<64>(t, p, page_maps(pool), s)
+                                        : launch_tc<128>(t, p, page_maps(pool), s);
+        return e == cudaSuccess ? PGD_OK : PGD_ERR_CUDA;
+    }
     const AttendArgs a = {{cu_seqlens, block_table, seq_lens, B, total, max_blocks, p.block_size,
                            p.num_blocks, cap, p.err},
                           p.k, p.v, p.k_scale, p.v_scale, p.scale_per_block, Hq, p.hkv,
@@ -148,14 +215,7 @@ extern "C" int paged_gqa_attend(pgd_pool_t pool, const void* q, int64_t q_stride
                           scale * 1.4426950408889634f};
     const int64_t ctas = ((int64_t)total * Hq + kWarps - 1) / kWarps;
     if (ctas > INT32_MAX) return PGD_ERR_SHAPE;
-    OnDevice dev(p.device);
-    if (!dev.ok) return PGD_ERR_CUDA;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (p.dtype == PGD_BF16 && p.d == 64)
-        attend_simple_kernel<PGD_BF16, 64><<<(unsigned)ctas, kWarps * 32, 0, s>>>(a);
-    else if (p.dtype == PGD_BF16)
-        attend_simple_kernel<PGD_BF16, 128><<<(unsigned)ctas, kWarps * 32, 0, s>>>(a);
-    else if (p.dtype == PGD_FP8_E4M3)
+    if (p.dtype == PGD_FP8_E4M3)
         attend_simple_kernel<PGD_FP8_E4M3, 128><<<(unsigned)ctas, kWarps * 32, 0, s>>>(a);
     else
         attend_simple_kernel<PGD_INT8, 128><<<(unsigned)ctas, kWarps * 32, 0, s>>>(a);
