@@ -13,17 +13,25 @@
 // (no shuffles): while one block's weights are computed, the tensor cores run the other's
 // products.
 //
-// Keys.  Tiles of 128 tokens.  A producer warp walks the block table and fetches each page
-// of the tile with one TMA copy for every 64 elements of the head, so that pages land as
+// Keys.  Tiles of 128 tokens.  Producer warps walk the block table and fetch each page of
+// the tile with one TMA copy for every 64 elements of the head, so that pages land as
 // one tile in the swizzled layout both products read: K with its head dimension contiguous,
-// V with its tokens as rows (the transposed operand).  Pages no query of the CTA sees are
-// not fetched, and V rows outside the visible range are zeroed, so that nothing in an
-// unused slot is multiplied.
+// V with its tokens as rows (the transposed operand).  A warp issues its lanes' copies one
+// after the other, 54 cycles each (measured), and a tile of 16-token pages takes 16 for K
+// and 16 for V: one warp needs 2830 cycles for what the products take 2048 for, four need
+// 1650.  (Copies of 16 bytes by the threads of four warps, cp.async: 4850.)  Pages no query
+// of the CTA sees are not fetched, and V rows outside the visible range are zeroed, so that
+// nothing in an unused slot is multiplied.
 //
-// Warps: 0-3 and 4-7 the softmax of the two blocks, 8 the producer, 9 issues products.
-// Weights take the place of the scores they came from in TMEM.  The order of products,
-// P0 V(j), q0 K(j+1), P1 V(j), q1 K(j+1), keeps the tensor cores busy as long as a block's
-// softmax takes no longer than two products of the other.  The accumulator is rescaled
+// Warps: 0-3 and 4-7 the softmax of the two blocks, 8-11 the producers, 12 and 13 issue the
+// products of one block each; 14 and 15 only round the group up to four warps, the unit
+// registers are handed over in.  Weights take the place of the scores they came from in
+// TMEM, in halves, so that the first half's product starts early.  A block's products go P V(j),
+// q K(j+1), P V(j+1), .., in turns with the other's: its softmax runs during the other's
+// turn.  The issuing warp of the next turn has waited for its tiles and weights before the
+// turn is handed over; one warp that issued both blocks' products left the tensor cores
+// idle a third of the time, and two without turns fell into step, softmax with softmax.
+// The accumulator is rescaled
 // only when a row's maximum has grown by more than 2^8: until then weights are relative to
 // an older maximum, at most 256, which costs no precision in either float type.
 //
@@ -35,6 +43,8 @@
 #pragma once
 
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "page_ops.h"
 #include "ragged.cuh"
@@ -48,7 +58,11 @@ using namespace umma;
 constexpr int kTile = 128;      // tokens of a key tile
 constexpr int kBlock = 128;     // rows of a block
 constexpr int kRowShift = 8;    // log2 of the rows of a CTA
-constexpr int kThreads = 320;
+constexpr int kThreads = 512;
+// Registers a thread: launched with 128, then the 256 threads of the softmax take 200, the
+// 128 producers keep 64 and the last 128 keep 48, which is the launch's 65536 again.
+constexpr int kSoftmaxRegs = 200, kProducerRegs = 64, kIssuerRegs = 48;
+constexpr int kProducers = 4;   // warps that issue copies
 constexpr float kGrow = 8.f;    // base-2 growth of a maximum that is let pass
 
 struct Args {
@@ -73,7 +87,7 @@ struct Layout {
     static constexpr int kQ = kBlock * D * 2;              // bytes of a block of queries
     static constexpr int kRing = 2 * kQ;
     static constexpr int kBars = kRing + kSlots * kSlot;
-    static constexpr int kBytes = kBars + 256 + 1024;      // and room to align to 1024
+    static constexpr int kBytes = kBars + 288 + 1024;      // and room to align to 1024
 };
 
 // The keys a block of rows sees: tiles [t0, t1), and which of them every row sees whole.
@@ -103,10 +117,28 @@ __device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int first, 
     return p;
 }
 
+// Token and head of the group of row r, r + step, r + 2 step, ..: one division for all.
+struct Rows {
+    int64_t token;
+    uint32_t head, group, dt, dh;
+    __device__ __forceinline__ Rows(uint32_t r, uint32_t g, uint32_t step)
+        : token(r / g), head(r % g), group(g), dt(step / g), dh(step % g) {}
+    __device__ __forceinline__ void next() {
+        token += dt;
+        head += dh;
+        if (head >= group) head -= group, ++token;
+    }
+};
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float m;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
 }
 __device__ __forceinline__ uint64_t pair(float a, float b) {
     uint64_t p;
@@ -140,12 +172,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
     const uint32_t bars = base + L::kBars;
-    const uint32_t bar_q = bars, bar_s = bars + 16, bar_p = bars + 32, bar_o = bars + 48;
-    const uint32_t bar_patch = bars + 64, bar_full = bars + 72;
-    const uint32_t bar_empty = bar_full + 8 * L::kSlots, bar_end = bars + 208;
-    volatile int* const gave_up = reinterpret_cast<int*>(smem + L::kBars + 240);
-    volatile int* const bad = reinterpret_cast<int*>(smem + L::kBars + 244);
-    uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(smem + L::kBars + 248);
+    const uint32_t bar_q = bars, bar_s = bars + 16, bar_p = bars + 32, bar_o = bars + 64;
+    const uint32_t bar_turn = bars + 80, bar_patch = bars + 96, bar_full = bars + 128;
+    const uint32_t bar_empty = bar_full + 8 * L::kSlots;
+    volatile int* const gave_up = reinterpret_cast<int*>(smem + L::kBars + 272);
+    volatile int* const bad = reinterpret_cast<int*>(smem + L::kBars + 276);
+    uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(smem + L::kBars + 280);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int share = a.cluster > 1 ? (int)cluster_rank() : 0;
@@ -187,22 +219,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            bar_init(bar_q + 8 * i, kBlock);
+            bar_init(bar_q + 8 * i, 4);  // warps of a block
             bar_init(bar_s + 8 * i, 1);
-            bar_init(bar_p + 8 * i, kBlock);
+            bar_init(bar_p + 16 * i, 4);
+            bar_init(bar_p + 16 * i + 8, 4);
             bar_init(bar_o + 8 * i, 1);
+            bar_init(bar_turn + 8 * i, 1);
         }
-        bar_init(bar_patch, 1);
-        bar_init(bar_end, 1);
+        for (int i = 0; i < kProducers; ++i) bar_init(bar_patch + 8 * i, 1);
         for (int i = 0; i < L::kSlots; ++i) {
-            bar_init(bar_full + 8 * i, 1);
-            bar_init(bar_empty + 8 * i, 1);
+            bar_init(bar_full + 8 * i, kProducers);
+            bar_init(bar_empty + 8 * i, 2);
         }
         *gave_up = 0;
         *bad = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) tmem_alloc(smem_addr(tmem_at), 512);
+    if (warp == 12) tmem_alloc(smem_addr(tmem_at), 512);
     fence_before();
     __syncthreads();
     fence_after();
@@ -214,29 +247,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 8) {
         // ---------------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const Span p = blk ? sp[1] : sp[0];
         if (p.t1 > p.t0) {
             // the block's queries into shared memory, swizzled
-            constexpr int kVecs = D / 8;
-            const __nv_bfloat16* q = a.q + (int64_t)s.row0 * a.q_stride + (int64_t)head * a.group * D;
-#pragma unroll 8
-            for (int i = my_row; i < kBlock * kVecs; i += kBlock) {
-                const int r = i / kVecs, c = i % kVecs;
-                const uint32_t R = row0 + blk * kBlock + r;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (blk * kBlock + r < rows) {
-                    x = __ldg(reinterpret_cast<const uint4*>(
-                        q + (int64_t)(R / group) * a.q_stride + R % group * D + c * 8));
-                    x.x = (x.x & a.q_and) ^ a.q_xor;
-                    x.y = (x.y & a.q_and) ^ a.q_xor;
-                    x.z = (x.z & a.q_and) ^ a.q_xor;
-                    x.w = (x.w & a.q_and) ^ a.q_xor;
-                }
+            constexpr int kVecs = D / 8, kStep = kBlock / kVecs;  // 16-byte pieces; rows at once
+            const int c = my_row % kVecs;
+            const __nv_bfloat16* q =
+                a.q + (int64_t)s.row0 * a.q_stride + (int64_t)head * a.group * D + c * 8;
+            Rows at(row0 + blk * kBlock + my_row / kVecs, group, kStep);
+            uint4 x[kVecs];
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i, at.next()) {  // all loads, then all stores
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (blk * kBlock + my_row / kVecs + i * kStep < rows)
+                    x[i] = __ldg(reinterpret_cast<const uint4*>(q + at.token * a.q_stride +
+                                                                at.head * D));
+            }
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const int r = my_row / kVecs + i * kStep;
                 *reinterpret_cast<uint4*>(smem + blk * L::kQ + c / 8 * (kBlock * 128) + r * 128 +
-                                          ((c ^ r) & 7) * 16) = x;
+                                          ((c ^ r) & 7) * 16) =
+                    make_uint4((x[i].x & a.q_and) ^ a.q_xor, (x[i].y & a.q_and) ^ a.q_xor,
+                               (x[i].z & a.q_and) ^ a.q_xor, (x[i].w & a.q_and) ^ a.q_xor);
             }
             fence_smem_async();
-            bar_arrive(bar_q + 8 * blk);
+            warp_arrive(bar_q + 8 * blk);
 
             const uint32_t R = row0 + blk * kBlock + my_row;
             int my_lo = 0, my_hi = 0;
@@ -248,225 +285,296 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t lanes = uint32_t(warp % 4 * 32) << 16;
             const uint32_t ts = tmem + lanes + blk * kTile;
             const uint32_t to = tmem + lanes + 2 * kTile + blk * D;
-            const float c = a.scale_log2;
-            uint32_t phase = 0;
-            for (int j = p.t0; j < p.t1; ++j, phase ^= 1) {
-                if (!__all_sync(0xffffffffu, bar_wait(bar_s + 8 * blk, phase, gave_up))) break;
-                fence_after();
+            const float scale = a.scale_log2;
+            // One tile of scores; `edge`: some row does not see all of it.
+            auto tile = [&](int j, auto edge) {
                 uint32_t x[kTile];
 #pragma unroll
                 for (int i = 0; i < kTile; i += 32) tmem_ld32(ts + i, x + i);
                 wait_ld();
 #pragma unroll
                 for (int i = 0; i < kTile; i += 32) keep32(x + i);
-                const int t = j * kTile;
-                if (t < p.lo_all || t + kTile > p.hi_all) {
-                    const int from = my_lo - t, to_ = my_hi - t;
+                if (decltype(edge)::value) {
+                    const int from = my_lo - j * kTile, until = my_hi - j * kTile;
 #pragma unroll
                     for (int i = 0; i < kTile; ++i)
-                        if (i < from || i >= to_) x[i] = 0xff800000u;  // -infinity
+                        if (i < from || i >= until) x[i] = 0xff800000u;  // -infinity
                 }
-                float top[4];
+                uint32_t w[kTile / 4];
+                uint64_t sum[2];
+                float top[8];
+                // weights of elements [64 h, 64 h + 64) relative to the maximum m, 16 at a
+                // time, and along with the first half the largest of all 128 scores: the
+                // exponentials set the pace, and the rest is issued in between
+                auto weigh = [&](int h) {
+                    const float off = m == -INFINITY ? 0.f : -m;
+                    const uint64_t cc = pair(scale, scale), mm = pair(off, off);
+                    float e[2][16];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) top[i] = __uint_as_float(x[i]);
+                    for (int g = 0; g <= 4; ++g) {
+                        const int at = h * (kTile / 2) + g * 16;
+                        if (g < 4) {
 #pragma unroll
-                for (int i = 4; i < kTile; ++i)
-                    top[i % 4] = fmaxf(top[i % 4], __uint_as_float(x[i]));
-                const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-                float keep = 1.f;
-                if (now > m + kGrow || m == -INFINITY) {
-                    keep = m == -INFINITY ? 0.f : ex2(m - now);
-                    l *= keep;
-                    m = now;
-                }
-                if (j > p.t0 && __any_sync(0xffffffffu, keep != 1.f)) {
-                    // the block's last products are done: its scores came after them
+                            for (int i = 0; i < 16; i += 2)
+                                unpair(fma2(pair(__uint_as_float(x[at + i]),
+                                                 __uint_as_float(x[at + i + 1])),
+                                            cc, mm),
+                                       e[g & 1][i], e[g & 1][i + 1]);
 #pragma unroll
-                    for (int i = 0; i < D; i += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(to + i, o);
-                        wait_ld();
-                        keep32(o);
+                            for (int i = 0; i < 16; ++i) {
+                                e[g & 1][i] = ex2(e[g & 1][i]);
+                                if (h == 0) {
+                                    const float u = __uint_as_float(x[g * 32 + 2 * i]);
+                                    const float v = __uint_as_float(x[g * 32 + 2 * i + 1]);
+                                    top[i % 8] = g == 0 && i < 8 ? fmaxf(u, v)
+                                                                 : max3(top[i % 8], u, v);
+                                }
+                            }
+                        }
+                        if (g > 0) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                        tmem_st32(to + i, o);
+                            for (int i = 0; i < 16; i += 2) {
+                                const float e0 = e[(g - 1) & 1][i], e1 = e[(g - 1) & 1][i + 1];
+                                sum[i / 2 % 2] = add2(sum[i / 2 % 2], pair(e0, e1));
+                                w[(g - 1) * 8 + i / 2] = bf16x2(e0, e1);
+                            }
+                        }
                     }
-                }
-                const float off = m == -INFINITY ? 0.f : -m;
-                const uint64_t cc = pair(c, c), mm = pair(off, off);
-                uint64_t sum[2] = {0, 0};
+                };
+                // The first half's weights are relative to the old maximum while the new one is
+                // found; they are computed again in the tiles where that has grown too far.
+                bool grown;
+                do {
+                    sum[0] = sum[1] = 0;
+                    weigh(0);
+                    const float now = fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]),
+                                            max3(top[5], top[6], top[7])) * scale;
+                    const bool over = now > m + kGrow;
+                    grown = __any_sync(0xffffffffu, over);
+                    if (grown) {
+                        float keep = 1.f;
+                        if (over) {
+                            keep = m == -INFINITY ? 0.f : ex2(m - now);
+                            l *= keep;
+                            m = now;
+                        }
+                        if (j > p.t0) {
+                            // the block's last products are done: its scores came after them
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[kTile / 4];
+                            for (int i = 0; i < D; i += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(to + i, o);
+                                wait_ld();
+                                keep32(o);
 #pragma unroll
-                    for (int i = 0; i < kTile / 2; i += 2) {
-                        const int at = h * (kTile / 2) + i;
-                        float e0, e1;
-                        unpair(fma2(pair(__uint_as_float(x[at]), __uint_as_float(x[at + 1])), cc,
-                                    mm),
-                               e0, e1);
-                        e0 = ex2(e0);
-                        e1 = ex2(e1);
-                        sum[i / 2 % 2] = add2(sum[i / 2 % 2], pair(e0, e1));
-                        w[i / 2] = bf16x2(e0, e1);
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                                tmem_st32(to + i, o);
+                            }
+                        }
                     }
-                    tmem_st32(ts + h * (kTile / 4), w);
-                }
+                } while (grown);
+                // the first half's product runs while the second half is computed
+                tmem_st32(ts, w);
                 wait_st();
                 fence_before();
-                bar_arrive(bar_p + 8 * blk);
+                warp_arrive(bar_p + 16 * blk);
+                weigh(1);
+                tmem_st32(ts + kTile / 4, w);
+                wait_st();
+                fence_before();
+                warp_arrive(bar_p + 16 * blk + 8);
                 float s0, s1;
                 unpair(add2(sum[0], sum[1]), s0, s1);
                 l += s0 + s1;
+            };
+            uint32_t phase = 0;
+            for (int j = p.t0; j < p.t1; ++j, phase ^= 1) {
+                if (!warp_wait(bar_s + 8 * blk, phase, gave_up)) break;
+                fence_after();
+                if (j * kTile < p.lo_all || (j + 1) * kTile > p.hi_all)
+                    tile(j, std::true_type());
+                else
+                    tile(j, std::false_type());
             }
-            bar_wait(bar_o + 8 * blk, 0, gave_up);
+            warp_wait(bar_o + 8 * blk, 0, gave_up);
         }
-    } else if (warp == 8) {
-        // --------------------------------------------------------------- producer
-        const int bs = a.r.block_size;
+    } else if (warp < 12) {
+        // -------------------------------------------------------------- producers
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+        // Copy k of a tile (page k / kHalves, column k % kHalves) is issued by warp k % 4,
+        // lane k / 4: the lanes of one warp take turns, 54 cycles each.
+        const int bs = a.r.block_size, me = warp - 8;
         const int box = min(bs, kTile);               // slots of a copy
-        const int pages = kTile / box;                // copies of a tile and column
-        const uint32_t box_bytes = box * 128;
-        const int my_page = lane / L::kHalves, my_half = lane % L::kHalves;
-        const bool mine = my_page < pages;
-        const int64_t table_row = (int64_t)b * a.r.max_blocks;
-        // block id of this lane's page of tile j; -1 where no query sees it
-        auto id_of = [&](int j) -> int {
-            const int t = j * kTile + my_page * box;
-            if (!mine || j >= T1 || t >= hi || t + box <= lo) return -1;
-            return __ldg(a.r.table + table_row + t / bs);
-        };
+        const int copies = kTile / box * L::kHalves;  // of a tile
+        const int k = lane * kProducers + me, my_page = k / L::kHalves, my_half = k % L::kHalves;
+        const bool mine = k < copies;
+        const int32_t* table = a.r.table + (int64_t)b * a.r.max_blocks;
         auto seen = [&](int j) {
             const int t = j * kTile + my_page * box;
-            return mine && t < hi && t + box > lo;
+            return mine && j < T1 && t < hi && t + box > lo;
         };
-        int id = T0 < T1 ? id_of(T0) : -1;
-        uint32_t n = 0, patches = 0;                  // tiles into the ring so far
-        bool stop = false;
-        for (int j = T0; j < T1 && !stop; ++j) {
+        auto id_of = [&](int j) {
+            return seen(j) ? __ldg(table + (j * kTile + my_page * box) / bs) : -1;
+        };
+        const uint32_t at = my_half * (kTile * 128) + my_page * box * 128;
+        int id = id_of(T0);
+        uint32_t slot = 0, turn = 0, patches = 0, n = 0;  // n: tiles into the ring so far
+        bool live = true;
+        for (int j = T0; j < T1 && live; ++j) {
             const int next = id_of(j + 1);
             const bool ok = id >= 0 && id < a.r.num_blocks;
             if (seen(j) && !ok) {
                 latch(a.r.err, PGD_ERR_BLOCK_ID);
                 *bad = 1;
             }
-            const uint32_t copies = __popc(__ballot_sync(0xffffffffu, ok));
+            const unsigned which = __ballot_sync(0xffffffffu, ok);
+            const uint32_t bytes = __popc(which) * box * 128;
+            // rows no query sees, or that have no page, among this warp's copies
             const bool patch = j * kTile < lo || (j + 1) * kTile > hi ||
-                               copies < uint32_t(pages * L::kHalves);
-            for (int side = 0; side < 2; ++side, ++n) {
-                const uint32_t slot = n % L::kSlots, use = n / L::kSlots;
-                if (use > 0 &&
-                    !__all_sync(0xffffffffu,
-                                bar_wait(bar_empty + 8 * slot, (use - 1) & 1, gave_up))) {
-                    stop = true;
-                    break;
-                }
+                               __any_sync(0xffffffffu, mine && !ok);
+            const int row = (j * kTile + my_page * box) % bs;
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                if (live) live = warp_wait(bar_empty + 8 * slot, turn ^ 1, gave_up);
+                if (!live) break;
                 const bool hold = side == 1 && patch;
-                const uint32_t bar = hold ? bar_patch : bar_full + 8 * slot;
-                const uint32_t dst = base + L::kRing + slot * L::kSlot;
+                const uint32_t full = bar_full + 8 * slot;
+                const uint32_t bar = hold ? bar_patch + 8 * me : full;
                 if (lane == 0) {
-                    if (copies)
-                        bar_arrive_tx(bar, copies * box_bytes);
+                    if (bytes)
+                        bar_arrive_tx(bar, bytes);
                     else
                         bar_arrive(bar);
                 }
                 __syncwarp();
                 if (ok)
-                    tma_load_4d(dst + my_half * (kTile * 128) + my_page * box_bytes,
-                                side ? &map_v : &map_k, bar, 0, (j * kTile + my_page * box) % bs,
-                                head * L::kHalves + my_half, id);
+                    tma_load_4d(base + L::kRing + slot * L::kSlot + at, side ? &map_v : &map_k, bar,
+                                0, row, head * L::kHalves + my_half, id);
                 if (hold) {
-                    // zero the rows no query sees, then hand the tile over
-                    if (!__all_sync(0xffffffffu, bar_wait(bar_patch, patches & 1, gave_up))) {
-                        stop = true;
-                        break;
-                    }
-                    ++patches;
-                    const unsigned there = __ballot_sync(0xffffffffu, ok);
-                    for (int r = 0; r < kTile; ++r) {
-                        const int t = j * kTile + r;
-                        const bool keep = t >= lo && t < hi &&
-                                          (there >> (r / box * L::kHalves) & 1);
-                        if (!keep && lane < L::kHalves * 8)
-                            *reinterpret_cast<uint4*>(smem + L::kRing + slot * L::kSlot +
-                                                      lane / 8 * (kTile * 128) + r * 128 +
-                                                      lane % 8 * 16) = make_uint4(0, 0, 0, 0);
+                    // V: zero those rows once the copies are there, then hand the tile over
+                    live = warp_wait(bar_patch + 8 * me, patches++ & 1, gave_up);
+                    if (!live) break;
+                    for (int c = me; c < copies; c += kProducers) {
+                        const int first = c / L::kHalves * box;
+                        uint8_t* const col = smem + L::kRing + slot * L::kSlot +
+                                             c % L::kHalves * (kTile * 128) + lane % 8 * 16;
+                        for (int r = first + lane / 8; r < first + box; r += 4) {
+                            const int t = j * kTile + r;
+                            if (t < lo || t >= hi || !(which >> (c / kProducers) & 1))
+                                *reinterpret_cast<uint4*>(col + r * 128) = make_uint4(0, 0, 0, 0);
+                        }
                     }
                     fence_smem_async();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(bar_full + 8 * slot);
+                    if (lane == 0) bar_arrive(full);
                 }
+                if (++slot == L::kSlots) slot = 0, turn ^= 1;
+                ++n;
             }
             id = next;
         }
-        if (stop) {  // no copy may land after the CTA has ended
-            const uint32_t from = n > L::kSlots ? n - L::kSlots : 0;
-            for (uint32_t i = from; i < n; ++i) {
-                volatile int never = 0;
+        if (!live) {  // no copy of this warp may land after the CTA has ended
+            volatile int never = 0;
+            if (patches) bar_wait(bar_patch + 8 * me, (patches - 1) & 1, &never);
+            for (uint32_t i = n > L::kSlots ? n - L::kSlots : 0; i < n; ++i)
                 bar_wait(bar_full + 8 * (i % L::kSlots), i / L::kSlots & 1, &never);
-            }
         }
-    } else if (lane == 0 && T1 > T0) {
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssuerRegs));
+    }
+    if ((warp == 12 || warp == 13) && T1 > T0) {
         // --------------------------------------------------------------- products
         constexpr uint32_t kQK = instruction(kBlock, kTile, 1, 0);
         constexpr uint32_t kPV = instruction(kBlock, D, 1, 1);
-        uint32_t n = 0;                               // tiles of the ring taken so far
-        auto ready = [&](uint32_t i) {
-            return bar_wait(bar_full + 8 * (i % L::kSlots), i / L::kSlots & 1, gave_up);
+        constexpr uint32_t kHi = operand_hi(1024);
+        const int i = warp - 12;  // the block whose products this warp issues
+        const int t0 = i ? sp[1].t0 : sp[0].t0, t1 = i ? sp[1].t1 : sp[0].t1;
+        const uint32_t acc = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t acc_s = acc + i * kTile, acc_o = acc + 2 * kTile + i * D;
+        const uint32_t q_lo = operand_lo(base, 16) + i * (L::kQ / 16);
+        const uint32_t k_lo = operand_lo(base + L::kRing, 16);
+        const uint32_t v_lo = operand_lo(base + L::kRing, kTile * 128);
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            return warp_wait(bar, parity, gave_up);
         };
-        auto tile = [&](uint32_t i) { return base + L::kRing + i % L::kSlots * L::kSlot; };
-        auto scores = [&](int i, uint32_t k) {
+        auto scores = [&](uint32_t slot, bool turn) {
             fence_after();
+            if (elected()) {
 #pragma unroll
-            for (int e = 0; e < D / 16; ++e) {
-                const uint32_t at = e / 4 * (kTile * 128) + e % 4 * 32;
-                mma_ss(tmem + i * kTile, operand(base + i * L::kQ + at, 16, 1024),
-                       operand(k + at, 16, 1024), kQK, e > 0);
+                for (int e = 0; e < D / 16; ++e) {
+                    const uint32_t at = (e / 4 * (kTile * 128) + e % 4 * 32) / 16;
+                    mma_ss(acc_s, q_lo + at, k_lo + slot * (L::kSlot / 16) + at, kHi, kQK, e > 0);
+                }
+                // the commits wait for the queue of products, so the turn goes first
+                if (turn) bar_arrive(bar_turn + 8 * (1 - i));
+                mma_commit(bar_s + 8 * i);
+                mma_commit(bar_empty + 8 * slot);
             }
-            mma_commit(bar_s + 8 * i);
         };
-        auto values = [&](int i, uint32_t v, bool add) {
+        auto values = [&](int half, uint32_t slot, bool add) {
             fence_after();
+            if (elected()) {
 #pragma unroll
-            for (int e = 0; e < kTile / 16; ++e)
-                mma_ts(tmem + 2 * kTile + i * D, tmem + i * kTile + e * 8,
-                       operand(v + e * 2048, kTile * 128, 1024), kPV, add || e > 0);
-        };
-        uint32_t done[2] = {0, 0};                    // tiles whose weights were taken
-        bool live = ready(0);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (live && T0 >= sp[i].t0 && T0 < sp[i].t1) {
-                live = bar_wait(bar_q + 8 * i, 0, gave_up);
-                if (live) scores(i, tile(0));
+                for (int k = 0; k < kTile / 32; ++k) {
+                    const int e = half * (kTile / 32) + k;
+                    mma_ts(acc_o, acc_s + e * 8, v_lo + slot * (L::kSlot / 16) + e * 128, kHi, kPV,
+                           add || e > 0);
+                }
+                if (half) mma_commit(bar_empty + 8 * slot);
             }
-        if (live) mma_commit(bar_empty + 8 * 0);
-        n = 1;
-        for (int j = T0; j < T1 && live; ++j, n += 2) {
-            const bool more = j + 1 < T1;
-            live = ready(n) && (!more || ready(n + 1));
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (live && j >= sp[i].t0 && j < sp[i].t1)
-                    live = bar_wait(bar_p + 8 * i, done[i]++ & 1, gave_up);
+        };
+        auto pass = [&](uint32_t slot) {  // a tile this block does not see
+            warp_arrive(bar_empty + 8 * slot);
+        };
+        // tiles lie in the ring as K(T0), V(T0), K(T0 + 1), ..: `at` is the next one's slot
+        uint32_t at = 0, turn = 0, weights = 0;
+        auto step = [&]() {
+            if (++at == L::kSlots) at = 0, turn ^= 1;
+        };
+        bool live = wait(bar_full, 0);
+        if (live && T0 == t0 && t0 < t1) live = wait(bar_q + 8 * i, 0);
+        if (live) {
+            if (T0 == t0 && t0 < t1)
+                scores(0, false);
+            else
+                pass(0);
+        }
+        step();
+        for (int j = T0; j < T1 && live; ++j) {
+            const uint32_t v_at = at, v_turn = turn;
+            step();
+            // all that can be waited for is there before the turn is taken
+            const bool now = j >= t0 && j < t1, next = j + 1 >= t0 && j + 1 < t1;
+            live = wait(bar_full + 8 * v_at, v_turn);
+            if (live && j + 1 < T1) live = wait(bar_full + 8 * at, turn);
+            if (live && j + 1 == t0 && next) live = wait(bar_q + 8 * i, 0);
+            if (live && now) live = wait(bar_p + 16 * i, weights);
+            if (live && (i || j > T0)) live = wait(bar_turn + 8 * i, (j - T0 + 1 - i) & 1);
+            if (!live) break;
+            if (now) {
+                values(0, v_at, j > t0);
+                live = wait(bar_p + 16 * i + 8, weights);
                 if (!live) break;
-                if (j >= sp[i].t0 && j < sp[i].t1) {
-                    values(i, tile(n), j > sp[i].t0);
-                    if (j + 1 == sp[i].t1) mma_commit(bar_o + 8 * i);
-                }
-                if (i == 1) mma_commit(bar_empty + 8 * (n % L::kSlots));
-                if (more && j + 1 >= sp[i].t0 && j + 1 < sp[i].t1) {
-                    if (j + 1 == sp[i].t0) live = bar_wait(bar_q + 8 * i, 0, gave_up);
-                    if (live) scores(i, tile(n + 1));
-                }
-                if (i == 1 && more) mma_commit(bar_empty + 8 * ((n + 1) % L::kSlots));
+                values(1, v_at, true);
+                weights ^= 1;
+            } else {
+                pass(v_at);
             }
+            if (j + 1 < T1 && next) {
+                scores(at, true);
+            } else {
+                if (j + 1 < T1) pass(at);
+                warp_arrive(bar_turn + 8 * (1 - i));
+            }
+            step();
         }
         // every product and its arrivals are over before their memory is given up
+        if (elected()) {
+            mma_commit(bar_o + 8 * i);
+        }
         volatile int never = 0;
-        mma_commit(bar_end);
-        bar_wait(bar_end, 0, &never);
+        bar_wait(bar_o + 8 * i, 0, &never);
     }
     __syncwarp();
     fence_before();
@@ -506,15 +614,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();
-            constexpr int kVecs = D / 8;
-            for (int i = lane; i < 32 * kVecs; i += 32) {
-                const int r = warp * 32 + i / kVecs, c = i % kVecs;
-                if (r >= rows) continue;
-                const uint32_t R = row0 + r;
-                const uint4 x = *reinterpret_cast<const uint4*>(
-                    smem + r * (D * 2) + ((c ^ r) & (kVecs - 1)) * 16);
-                *reinterpret_cast<uint4*>(
-                    a.out + (out_at + (int64_t)(R / group) * a.hq + R % group) * D + c * 8) = x;
+            constexpr int kVecs = D / 8, kStep = 32 / kVecs;
+            const int c = lane % kVecs;
+            Rows at(row0 + warp * 32 + lane / kVecs, group, kStep);
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i, at.next()) {
+                const int r = warp * 32 + lane / kVecs + i * kStep;
+                if (r < rows)
+                    *reinterpret_cast<uint4*>(
+                        a.out + (out_at + at.token * a.hq + at.head) * D + c * 8) =
+                        *reinterpret_cast<const uint4*>(smem + r * (D * 2) +
+                                                        ((c ^ r) & (kVecs - 1)) * 16);
             }
         }
     } else {
@@ -546,11 +656,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (threadIdx.x == 0) reinterpret_cast<int*>(stat)[512] = failed;
         cluster_sync();
+        if (warp < 8) {
         bool any_failed = false;
         for (int k = 0; k < a.cluster; ++k)
             any_failed |= __float_as_int(peer_ld4(peer_addr(base + 2048, k)).x) != 0;
         constexpr int kVecs = D / 4;  // four columns a thread
-        for (int i = threadIdx.x + share * kThreads; i < rows * kVecs; i += a.cluster * kThreads) {
+        for (int i = threadIdx.x + share * 256; i < rows * kVecs; i += a.cluster * 256) {
             const int r = i / kVecs, c = i % kVecs;
             float top = -INFINITY;
             float2 st[8];
@@ -580,10 +691,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       c * 4) =
                 make_uint2(bf16x2(o[0] * inv, o[1] * inv), bf16x2(o[2] * inv, o[3] * inv));
         }
+        }
         cluster_sync();  // shared memory stays until every CTA has read it
     }
     __syncthreads();
-    if (warp == 9) tmem_free(tmem, 512);
+    if (warp == 12) tmem_free(tmem, 512);
 }
 
 }  // namespace attend

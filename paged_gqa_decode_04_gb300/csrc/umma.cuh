@@ -52,6 +52,31 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     return true;
 }
 
+// The same for a whole warp.  Every lane asks and the loop goes by their vote, so that the
+// warp never diverges: one lane asking for all (measured: some 300 cycles a wait) is slower.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+    uint64_t t0 = 0;
+    for (int i = 0;; ++i) {
+        if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+        if (i % 32 != 31) continue;
+        uint64_t t;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        if (t0 == 0) t0 = t;
+        if (__any_sync(0xffffffffu, *gave_up || t - t0 > 2000000000ull)) {
+            *gave_up = 1;
+            return false;
+        }
+    }
+}
+// One arrival for the warp, after what all its lanes did.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+    __syncwarp();
+    asm volatile(
+        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n"
+        " @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar)
+        : "memory");
+}
+
 // Writes of this thread to shared memory become visible to the tensor cores and TMA.
 __device__ __forceinline__ void fence_smem_async() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -131,11 +156,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
 
 // ----------------------------------------------------------------------- products
 // Shared-memory operand with 128-byte rows in the 128-byte swizzle, 1024-byte atoms of
-// 8 rows.  lead: bytes between 64-element blocks of the contiguous dimension when that
-// dimension is M or N (ignored when it is K); stride: bytes between atoms along the other.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride) {
-    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 |
-           (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// 8 rows.  The low word holds the address, and the bytes between 64-element blocks of the
+// contiguous dimension when that is M or N (`lead`; ignored when it is K); the high word
+// the bytes between atoms along the other dimension.  An operand that starts `d` bytes on
+// has d / 16 more in its low word.
+__device__ __forceinline__ uint32_t operand_lo(uint32_t addr, uint32_t lead) {
+    return (addr & 0x3ffff) >> 4 | (lead >> 4) << 16;
+}
+__host__ __device__ constexpr uint32_t operand_hi(uint32_t stride) {
+    return stride >> 4 | 1u << 14 | 2u << 29;
 }
 
 // Instruction descriptor: 16-bit operands of one type (bf16 1, f16 0), float32
@@ -145,21 +174,33 @@ __host__ __device__ constexpr uint32_t instruction(int m, int n, int bf16, int b
            uint32_t(n >> 3) << 17 | uint32_t(m >> 4) << 24;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool add) {
+// Both are issued by one thread.  The instruction takes its operands from uniform
+// registers: a warp that runs its loop together, with only the products behind elected(),
+// computes them there once; a single diverged thread moves each one over (measured: about
+// 95 cycles a product instead of 64).
+__device__ __forceinline__ bool elected() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                       uint32_t idesc, bool add) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.u32 p, %5, 0;\n"
+        " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
 // A from TMEM (two 16-bit elements a column).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi,
+                                       uint32_t idesc, bool add) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.u32 p, %5, 0;\n"
+        " mov.b64 b, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
 // Arrive on `bar` when every product issued by this thread so far is done.
