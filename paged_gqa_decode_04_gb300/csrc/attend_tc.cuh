@@ -288,63 +288,64 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float scale = a.scale_log2;
             // One tile of scores; `edge`: some row does not see all of it.
             auto tile = [&](int j, auto edge) {
-                uint32_t x[kTile];
-#pragma unroll
-                for (int i = 0; i < kTile; i += 32) tmem_ld32(ts + i, x + i);
-                wait_ld();
-#pragma unroll
-                for (int i = 0; i < kTile; i += 32) keep32(x + i);
-                if (decltype(edge)::value) {
-                    const int from = my_lo - j * kTile, until = my_hi - j * kTile;
-#pragma unroll
-                    for (int i = 0; i < kTile; ++i)
-                        if (i < from || i >= until) x[i] = 0xff800000u;  // -infinity
-                }
-                uint32_t w[kTile / 4];
+                uint32_t x[kTile], w[kTile / 4];
                 uint64_t sum[2];
                 float top[8];
-                // weights of elements [64 h, 64 h + 64) relative to the maximum m, 16 at a
-                // time, and along with the first half the largest of all 128 scores: the
-                // exponentials set the pace, and the rest is issued in between
+                // weights of elements [64 h, 64 h + 64) relative to the maximum m, in the
+                // scores' registers and 8 at a time; along with the first half the largest of
+                // all 128 scores: the exponentials set the pace, the rest is issued in between
                 auto weigh = [&](int h) {
                     const float off = m == -INFINITY ? 0.f : -m;
                     const uint64_t cc = pair(scale, scale), mm = pair(off, off);
-                    float e[2][16];
 #pragma unroll
-                    for (int g = 0; g <= 4; ++g) {
-                        const int at = h * (kTile / 2) + g * 16;
-                        if (g < 4) {
+                    for (int g = 0; g <= 8; ++g) {
+                        const int at = h * (kTile / 2) + g * 8;
+                        if (g < 8) {
+                            if (h == 0) {
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2)
+                                for (int i = 0; i < 8; ++i) {
+                                    const float u = __uint_as_float(x[g * 8 + i]);
+                                    const float v = __uint_as_float(x[kTile / 2 + g * 8 + i]);
+                                    top[i] = g == 0 ? fmaxf(u, v) : max3(top[i], u, v);
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) {
+                                float e0, e1;
                                 unpair(fma2(pair(__uint_as_float(x[at + i]),
                                                  __uint_as_float(x[at + i + 1])),
                                             cc, mm),
-                                       e[g & 1][i], e[g & 1][i + 1]);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                e[g & 1][i] = ex2(e[g & 1][i]);
-                                if (h == 0) {
-                                    const float u = __uint_as_float(x[g * 32 + 2 * i]);
-                                    const float v = __uint_as_float(x[g * 32 + 2 * i + 1]);
-                                    top[i % 8] = g == 0 && i < 8 ? fmaxf(u, v)
-                                                                 : max3(top[i % 8], u, v);
-                                }
+                                       e0, e1);
+                                x[at + i] = __float_as_uint(ex2(e0));
+                                x[at + i + 1] = __float_as_uint(ex2(e1));
                             }
                         }
                         if (g > 0) {
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const float e0 = e[(g - 1) & 1][i], e1 = e[(g - 1) & 1][i + 1];
-                                sum[i / 2 % 2] = add2(sum[i / 2 % 2], pair(e0, e1));
-                                w[(g - 1) * 8 + i / 2] = bf16x2(e0, e1);
+                            for (int i = -8; i < 0; i += 2) {
+                                const float e0 = __uint_as_float(x[at + i]);
+                                const float e1 = __uint_as_float(x[at + i + 1]);
+                                sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(e0, e1));
+                                w[g * 4 + i / 2] = bf16x2(e0, e1);
                             }
                         }
                     }
                 };
                 // The first half's weights are relative to the old maximum while the new one is
-                // found; they are computed again in the tiles where that has grown too far.
+                // found; the tile is read again where that has grown too far.
                 bool grown;
                 do {
+#pragma unroll
+                    for (int i = 0; i < kTile; i += 32) tmem_ld32(ts + i, x + i);
+                    wait_ld();
+#pragma unroll
+                    for (int i = 0; i < kTile; i += 32) keep32(x + i);
+                    if (decltype(edge)::value) {
+                        const int from = my_lo - j * kTile, until = my_hi - j * kTile;
+#pragma unroll
+                        for (int i = 0; i < kTile; ++i)
+                            if (i < from || i >= until) x[i] = 0xff800000u;  // -infinity
+                    }
                     sum[0] = sum[1] = 0;
                     weigh(0);
                     const float now = fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]),
