@@ -334,7 +334,8 @@ int paged_gqa_workspace_size_host(pgd_pool_t pool, int B, int q_len, int Hq, int
  * A query that attends to nothing gets zeros.  Blocks that lie wholly before every
  * query's window are never read.  Cached keys and values are expected to be finite where a
  * query of the sequence may attend to them; slots past Lb may hold anything.
- * bfloat16 and 8-bit pools (PGD_ERR_UNSUPPORTED for float32).  No workspace.  Sequences
+ * bfloat16 and 8-bit pools (PGD_ERR_UNSUPPORTED for float32; with 8-bit pages queries
+ * stay below 65504 in magnitude and scales are not negative).  No workspace.  Sequences
  * whose cu_seqlens or length is impossible latch PGD_ERR_SEQ_LEN, block ids out of range
  * PGD_ERR_BLOCK_ID; the rows that would have read them are written as NaN.
  */

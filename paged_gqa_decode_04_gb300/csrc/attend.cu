@@ -4,12 +4,8 @@
 //
 //     out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale <q, k_t> - m), m = max_t,
 //
-// in one pass over the tokens with a running maximum and sum in float32.  bfloat16 pools
-// take the tensor-core kernel (attend_tc.cuh), 8-bit pools one warp per (query token,
-// query head), a lane holding D / 32 elements.
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
+// in one pass over the tokens with a running maximum and sum in float32, on the tensor
+// cores: attend_tc.cuh.  This file checks the arguments and chooses the launch.
 #include <atomic>
 
 #include "attend_tc.cuh"
@@ -19,102 +15,6 @@
 
 namespace pgd {
 namespace {
-
-constexpr int kWarps = 8;
-
-struct AttendArgs {
-    Ragged r;
-    const void* k_pool;
-    const void* v_pool;
-    const float* k_scale;
-    const float* v_scale;
-    int scale_per_block;
-    int hq, hkv;
-    const __nv_bfloat16* q;
-    int64_t q_stride;
-    __nv_bfloat16* out;
-    int causal;
-    int window;
-    float scale_log2;
-};
-
-// D / 32 consecutive elements of a page row, element e of the pool.
-template <int PAGE, int N>
-__device__ __forceinline__ void page_values(const void* pool, int64_t e, float (&x)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (PAGE == PGD_BF16)
-            x[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(pool)[e + i]);
-        else if (PAGE == PGD_INT8)
-            x[i] = float(static_cast<const int8_t*>(pool)[e + i]);
-        else
-            x[i] = float(static_cast<const __nv_fp8_e4m3*>(pool)[e + i]);
-    }
-}
-
-template <int PAGE, int D>
-__global__ void __launch_bounds__(kWarps * 32) attend_simple_kernel(const AttendArgs a) {
-    constexpr int N = D / 32;
-    constexpr bool q8 = PAGE != PGD_BF16;
-    if (blockIdx.x == 0) check_all(a.r, false);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
-    const int64_t t = unit / a.hq;
-    const int h = int(unit % a.hq), kv = h / (a.hq / a.hkv);
-    if (t >= a.r.total) return;
-    const int b = find_seq(a.r, t, 1, 0, 0);
-    if (b >= a.r.B) return;
-    const Seq s = load_seq(a.r, b);
-    if (t < s.row0 || (s.ok && t >= s.row0 + s.n)) return;
-    const int pos = s.len - s.n + int(t - s.row0);  // the query's position
-    int lo = 0, hi = s.len;
-    if (a.causal) {
-        hi = pos + 1;
-        if (a.window > 0) lo = max(0, pos - a.window + 1);
-    }
-    float q[N], o[N], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        q[i] = __bfloat162float(a.q[t * a.q_stride + h * D + lane * N + i]);
-        o[i] = 0.f;
-    }
-    bool bad = !s.ok;
-    for (int u = lo; u < hi && !bad; ++u) {
-        const int64_t blk = block_of(a.r, b, u / a.r.block_size);
-        if (blk < 0) {
-            bad = true;
-            break;
-        }
-        const int64_t e = ((blk * a.r.block_size + u % a.r.block_size) * a.hkv + kv) * D + lane * N;
-        float x[N];
-        page_values<PAGE, N>(a.k_pool, e, x);
-        float z = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) z = fmaf(q[i], x[i], z);
-#pragma unroll
-        for (int k = 1; k < 32; k *= 2) z += __shfl_xor_sync(0xffffffffu, z, k);
-        float vs = 1.f;
-        z *= a.scale_log2;
-        if (q8) {
-            const int64_t si = kv + (a.scale_per_block ? blk * a.hkv : 0);
-            z *= a.k_scale[si];
-            vs = a.v_scale[si];
-        }
-        const float top = fmaxf(m, z);
-        const float keep = top == -INFINITY ? 1.f : exp2f(m - top);
-        const float p = top == -INFINITY ? 0.f : exp2f(z - top);
-        m = top;
-        l = l * keep + p;
-        page_values<PAGE, N>(a.v_pool, e, x);
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = fmaf(p * vs, x[i], o[i] * keep);
-    }
-    const float inv = bad ? NAN : l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        a.out[(t * a.hq + h) * D + lane * N + i] =
-            __float2bfloat16(inv == 0.f ? 0.f : o[i] * inv);
-}
 
 // CTAs that share the keys of a piece of rows (a cluster).  One CTA fits on an SM, so
 // `units` pieces take ceil(units c / SMs) rounds of 1 / c of the work each; c is raised
@@ -132,13 +32,13 @@ int choose_cluster(const Pool& p, int64_t units, int64_t max_tokens) {
     return best;
 }
 
-template <int D>
-cudaError_t launch_tc(const attend::Args& a, const Pool& p, const PageMaps& maps, cudaStream_t s) {
+template <int D, int PAGE, bool PB>
+cudaError_t launch(const attend::Args& a, const Pool& p, const PageMaps& maps, cudaStream_t s) {
     using namespace attend;
     static std::atomic<uint64_t> ready{0};  // devices whose function attributes are set
     if (!(ready.load() >> p.device & 1)) {
         const cudaError_t e = cudaFuncSetAttribute(
-            attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
+            attend_kernel<D, PAGE, PB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D, PAGE>::kBytes);
         if (e != cudaSuccess) return e;
         ready.fetch_or(uint64_t(1) << p.device);
     }
@@ -149,11 +49,11 @@ cudaError_t launch_tc(const attend::Args& a, const Pool& p, const PageMaps& maps
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(unsigned(a.pieces) * a.hkv * a.cluster);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Layout<D>::kBytes;
+    cfg.dynamicSmemBytes = Layout<D, PAGE>::kBytes;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = a.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attend_kernel<D>, a, maps.k, maps.v);
+    return cudaLaunchKernelEx(&cfg, attend_kernel<D, PAGE, PB>, a, maps.k, maps.v);
 }
 
 }  // namespace
@@ -192,39 +92,35 @@ extern "C" int paged_gqa_attend(pgd_pool_t pool, const void* q, int64_t q_stride
     OnDevice dev(p.device);
     if (!dev.ok) return PGD_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (p.dtype == PGD_BF16) {
-        attend::Args t = {};
-        t.r = {cu_seqlens, block_table, seq_lens, B, total, max_blocks, p.block_size,
-               p.num_blocks, cap, p.err};
-        t.hq = Hq;
-        t.hkv = p.hkv;
-        t.group = group;
-        t.q = static_cast<const __nv_bfloat16*>(q);
-        t.q_stride = q_stride;
-        t.out = static_cast<__nv_bfloat16*>(out);
-        t.causal = causal;
-        t.window = window;
-        // a scale below zero turns the queries' sign, one of zero leaves no query
-        t.scale_log2 = scale != 0.f ? fabsf(scale) * 1.4426950408889634f : 1.f;
-        t.q_and = scale != 0.f ? 0xffffffffu : 0u;
-        t.q_xor = scale < 0.f ? 0x80008000u : 0u;
-        t.pieces = int(pieces);
-        t.cluster = choose_cluster(p, pieces * p.hkv, cap);
-        const cudaError_t e = p.d == 64 ? launch_tc<64>(t, p, page_maps(pool), s)
-                                        : launch_tc<128>(t, p, page_maps(pool), s);
-        return e == cudaSuccess ? PGD_OK : PGD_ERR_CUDA;
-    }
-    const AttendArgs a = {{cu_seqlens, block_table, seq_lens, B, total, max_blocks, p.block_size,
-                           p.num_blocks, cap, p.err},
-                          p.k, p.v, p.k_scale, p.v_scale, p.scale_per_block, Hq, p.hkv,
-                          static_cast<const __nv_bfloat16*>(q), q_stride,
-                          static_cast<__nv_bfloat16*>(out), causal, window,
-                          scale * 1.4426950408889634f};
-    const int64_t ctas = ((int64_t)total * Hq + kWarps - 1) / kWarps;
-    if (ctas > INT32_MAX) return PGD_ERR_SHAPE;
-    if (p.dtype == PGD_FP8_E4M3)
-        attend_simple_kernel<PGD_FP8_E4M3, 128><<<(unsigned)ctas, kWarps * 32, 0, s>>>(a);
+    attend::Args t = {};
+    t.r = {cu_seqlens, block_table, seq_lens, B, total, max_blocks, p.block_size,
+           p.num_blocks, cap, p.err};
+    t.hq = Hq;
+    t.hkv = p.hkv;
+    t.group = group;
+    t.q = static_cast<const __nv_bfloat16*>(q);
+    t.q_stride = q_stride;
+    t.out = static_cast<__nv_bfloat16*>(out);
+    t.causal = causal;
+    t.window = window;
+    // a scale below zero turns the queries' sign, one of zero leaves no query
+    t.scale_log2 = scale != 0.f ? fabsf(scale) * 1.4426950408889634f : 1.f;
+    t.q_and = scale != 0.f ? 0xffffffffu : 0u;
+    t.q_xor = scale < 0.f ? 0x80008000u : 0u;
+    t.pieces = int(pieces);
+    t.cluster = choose_cluster(p, pieces * p.hkv, cap);
+    t.k_scale = p.k_scale;
+    t.v_scale = p.v_scale;
+    const PageMaps& maps = page_maps(pool);
+    cudaError_t e;
+    if (p.dtype == PGD_BF16)
+        e = p.d == 64 ? launch<64, PGD_BF16, false>(t, p, maps, s)
+                      : launch<128, PGD_BF16, false>(t, p, maps, s);
+    else if (p.dtype == PGD_FP8_E4M3)
+        e = p.scale_per_block ? launch<128, PGD_FP8_E4M3, true>(t, p, maps, s)
+                              : launch<128, PGD_FP8_E4M3, false>(t, p, maps, s);
     else
-        attend_simple_kernel<PGD_INT8, 128><<<(unsigned)ctas, kWarps * 32, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? PGD_OK : PGD_ERR_CUDA;
+        e = p.scale_per_block ? launch<128, PGD_INT8, true>(t, p, maps, s)
+                              : launch<128, PGD_INT8, false>(t, p, maps, s);
+    return e == cudaSuccess ? PGD_OK : PGD_ERR_CUDA;
 }

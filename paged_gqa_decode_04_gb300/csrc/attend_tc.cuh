@@ -43,6 +43,8 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include <type_traits>
 
@@ -62,7 +64,6 @@ constexpr int kThreads = 512;
 // Registers a thread: launched with 128, then the 256 threads of the softmax take 200, the
 // 128 producers keep 64 and the last 128 keep 48, which is the launch's 65536 again.
 constexpr int kSoftmaxRegs = 200, kProducerRegs = 64, kIssuerRegs = 48;
-constexpr int kProducers = 4;   // warps that issue copies
 constexpr float kGrow = 8.f;    // base-2 growth of a maximum that is let pass
 
 struct Args {
@@ -77,17 +78,30 @@ struct Args {
     uint32_t q_and, q_xor;  // applied to pairs of query elements (a scale below or of zero)
     int pieces;             // row pieces of the grid (each with every KV head)
     int cluster;            // CTAs sharing a piece's keys
+    const float* k_scale;   // 8-bit pages: [hkv], or [num_blocks][hkv]
+    const float* v_scale;
 };
 
-template <int D>
+template <int D, int PAGE>
 struct Layout {
-    static constexpr int kHalves = D / 64;                 // 128-byte columns of a head
+    static constexpr bool kQ8 = PAGE != PGD_BF16;
+    static constexpr int kHalves = D / 64;                 // 128-byte columns of a 16-bit tile
     static constexpr int kSlot = kTile * D * 2;            // bytes of a K or V tile
-    static constexpr int kSlots = D == 128 ? 5 : 8;
+    static constexpr int kSlots = kQ8 ? 4 : D == 128 ? 5 : 8;
     static constexpr int kQ = kBlock * D * 2;              // bytes of a block of queries
     static constexpr int kRing = 2 * kQ;
-    static constexpr int kBars = kRing + kSlots * kSlot;
+    // 8-bit pages: tiles as they are stored, and the scales of the tiles in flight (a tile
+    // is at most 1 + kRawSlots / 2 + kSlots / 2 ahead of the softmax)
+    static constexpr int kRawSlot = kTile * 128;
+    static constexpr int kRawSlots = 2;
+    static constexpr int kRaw = kRing + kSlots * kSlot;
+    static constexpr int kScaleTiles = 8;
+    static constexpr int kScales = kRaw + (kQ8 ? kRawSlots * kRawSlot : 0);
+    static constexpr int kBars = kScales + (kQ8 ? kScaleTiles * 128 : 0);
     static constexpr int kBytes = kBars + 288 + 1024;      // and room to align to 1024
+    // warps that issue copies, and the tiles' 128-byte columns they fetch one by one
+    static constexpr int kProducers = kQ8 ? 2 : 4;
+    static constexpr int kColumns = kQ8 ? 1 : kHalves;
 };
 
 // The keys a block of rows sees: tiles [t0, t1), and which of them every row sees whole.
@@ -140,6 +154,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
     return m;
 }
+__device__ __forceinline__ float max8(const uint32_t* x) {
+    const float a = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+    const float b = max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
+    return max3(a, b, fmaxf(__uint_as_float(x[6]), __uint_as_float(x[7])));
+}
 __device__ __forceinline__ uint64_t pair(float a, float b) {
     uint64_t p;
     asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
@@ -163,17 +182,58 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int D>
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The type of the products' operands: bfloat16, or f16 over 8-bit pages, in which both
+// codes are exact.
+template <int PAGE>
+__device__ __forceinline__ uint32_t operand2(float lo, float hi) {
+    return PAGE == PGD_BF16 ? bf16x2(lo, hi) : f16x2(lo, hi);
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Four codes to two pairs of f16.
+template <int PAGE>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
+    if (PAGE == PGD_INT8) {
+        // a code with its sign bit turned is code + 128; under the high byte 0x64 it is the
+        // f16 1024 + code + 128
+        const __half2 off = __half2half2(__float2half(1152.f));
+        w ^= 0x80808080u;
+        const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140);
+        const uint32_t hi = __byte_perm(w, 0x64646464u, 0x4342);
+        const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&lo), off);
+        const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&hi), off);
+        a = *reinterpret_cast<const uint32_t*>(&x);
+        b = *reinterpret_cast<const uint32_t*>(&y);
+    } else {
+        const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w), __NV_E4M3);
+        const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w >> 16), __NV_E4M3);
+        a = x.x | uint32_t(x.y) << 16;
+        b = y.x | uint32_t(y.y) << 16;
+    }
+}
+
+template <int D, int PAGE, bool PB>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
-    using L = Layout<D>;
+    using L = Layout<D, PAGE>;
+    constexpr bool kQ8 = L::kQ8;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
     const uint32_t bars = base + L::kBars;
     const uint32_t bar_q = bars, bar_s = bars + 16, bar_p = bars + 32, bar_o = bars + 64;
+    // bar_patch: one of each producer (bfloat16), bar_raw: full and empty raw slots (8-bit)
     const uint32_t bar_turn = bars + 80, bar_patch = bars + 96, bar_full = bars + 128;
+    const uint32_t bar_raw = bar_patch, bar_raw_empty = bar_raw + 8 * L::kRawSlots;
     const uint32_t bar_empty = bar_full + 8 * L::kSlots;
     volatile int* const gave_up = reinterpret_cast<int*>(smem + L::kBars + 272);
     volatile int* const bad = reinterpret_cast<int*>(smem + L::kBars + 276);
@@ -226,9 +286,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(bar_o + 8 * i, 1);
             bar_init(bar_turn + 8 * i, 1);
         }
-        for (int i = 0; i < kProducers; ++i) bar_init(bar_patch + 8 * i, 1);
+        if (kQ8) {
+            for (int i = 0; i < L::kRawSlots; ++i) {
+                bar_init(bar_raw + 8 * i, L::kProducers);
+                bar_init(bar_raw_empty + 8 * i, 4);
+            }
+        } else {
+            for (int i = 0; i < L::kProducers; ++i) bar_init(bar_patch + 8 * i, 1);
+        }
         for (int i = 0; i < L::kSlots; ++i) {
-            bar_init(bar_full + 8 * i, kProducers);
+            bar_init(bar_full + 8 * i, 4);  // producer or widening warps
             bar_init(bar_empty + 8 * i, 2);
         }
         *gave_up = 0;
@@ -242,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_at;
 
     float m = -INFINITY, l = 0.f;  // of the thread's row, in the units of exp2
+    float vgain = 0.f;             // of the accumulator, with a V scale per block
     const int blk = warp / 4;      // block of rows of a softmax warp
     const int my_row = threadIdx.x % kBlock;
 
@@ -267,10 +335,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
                 const int r = my_row / kVecs + i * kStep;
+                auto operand = [&](uint32_t two) {
+                    two = (two & a.q_and) ^ a.q_xor;
+                    return kQ8 ? f16x2(__uint_as_float(two << 16),
+                                       __uint_as_float(two & 0xffff0000u))
+                               : two;
+                };
                 *reinterpret_cast<uint4*>(smem + blk * L::kQ + c / 8 * (kBlock * 128) + r * 128 +
                                           ((c ^ r) & 7) * 16) =
-                    make_uint4((x[i].x & a.q_and) ^ a.q_xor, (x[i].y & a.q_and) ^ a.q_xor,
-                               (x[i].z & a.q_and) ^ a.q_xor, (x[i].w & a.q_and) ^ a.q_xor);
+                    make_uint4(operand(x[i].x), operand(x[i].y), operand(x[i].z),
+                               operand(x[i].w));
             }
             fence_smem_async();
             warp_arrive(bar_q + 8 * blk);
@@ -285,23 +359,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t lanes = uint32_t(warp % 4 * 32) << 16;
             const uint32_t ts = tmem + lanes + blk * kTile;
             const uint32_t to = tmem + lanes + 2 * kTile + blk * D;
-            const float scale = a.scale_log2;
+            // a scale of 0 still has to leave masked scores at -infinity
+            const float scale =
+                kQ8 && !PB ? fmaxf(a.scale_log2 * __ldg(a.k_scale + head), 1e-30f) : a.scale_log2;
+            auto rescale = [&](float keep) {  // the block's accumulator
+#pragma unroll
+                for (int i = 0; i < D; i += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(to + i, o);
+                    wait_ld();
+                    keep32(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                    tmem_st32(to + i, o);
+                }
+            };
             // One tile of scores; `edge`: some row does not see all of it.
             auto tile = [&](int j, auto edge) {
                 uint32_t x[kTile], w[kTile / 4];
                 uint64_t sum[2];
                 float top[8];
+                // scales of each 8 tokens: K's on the scores, V's (times vgain) on the weights
+                const float* const ks =
+                    reinterpret_cast<const float*>(smem + L::kScales + (j - T0) % 8 * 128);
+                const float* const vs = ks + kTile / 8;
+                if (PB) {
+                    // vgain, a power of two, keeps weight times scale within f16: it starts from
+                    // the first tile's largest scale and falls when one grows past 16 times that
+                    float most = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kTile / 8; ++i) most = fmaxf(most, vs[i]);
+                    if (most * vgain > 16.f || vgain == 0.f) {
+                        const int e = min(max((__float_as_int(most) >> 23) & 255, 2), 252);
+                        const float gain = __int_as_float((254 - e) << 23);
+                        if (j > p.t0) rescale(gain / vgain);
+                        vgain = gain;
+                    }
+                }
                 // weights of elements [64 h, 64 h + 64) relative to the maximum m, in the
                 // scores' registers and 8 at a time; along with the first half the largest of
                 // all 128 scores: the exponentials set the pace, the rest is issued in between
                 auto weigh = [&](int h) {
                     const float off = m == -INFINITY ? 0.f : -m;
-                    const uint64_t cc = pair(scale, scale), mm = pair(off, off);
+                    const uint64_t mm = pair(off, off);
 #pragma unroll
                     for (int g = 0; g <= 8; ++g) {
                         const int at = h * (kTile / 2) + g * 8;
+                        const float by = PB && g < 8 ? scale * ks[h * 8 + g] : scale;
+                        const uint64_t cc = pair(by, by);
                         if (g < 8) {
-                            if (h == 0) {
+                            if (h == 0 && PB) {
+                                float u = max8(x + g * 8) * ks[g];
+                                float v = max8(x + kTile / 2 + g * 8) * ks[8 + g];
+                                top[0] = g == 0 ? fmaxf(u, v) : max3(top[0], u, v);
+                            } else if (h == 0) {
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
                                     const float u = __uint_as_float(x[g * 8 + i]);
@@ -321,12 +433,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                         if (g > 0) {
+                            const float gain = PB ? vs[h * 8 + g - 1] * vgain : 1.f;
 #pragma unroll
                             for (int i = -8; i < 0; i += 2) {
-                                const float e0 = __uint_as_float(x[at + i]);
-                                const float e1 = __uint_as_float(x[at + i + 1]);
+                                float e0 = __uint_as_float(x[at + i]);
+                                float e1 = __uint_as_float(x[at + i + 1]);
                                 sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(e0, e1));
-                                w[g * 4 + i / 2] = bf16x2(e0, e1);
+                                if (PB) unpair(mul2(pair(e0, e1), pair(gain, gain)), e0, e1);
+                                w[g * 4 + i / 2] = operand2<PAGE>(e0, e1);
                             }
                         }
                     }
@@ -348,8 +462,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     sum[0] = sum[1] = 0;
                     weigh(0);
-                    const float now = fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]),
-                                            max3(top[5], top[6], top[7])) * scale;
+                    if (!PB)
+                        top[0] = fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]),
+                                       max3(top[5], top[6], top[7]));
+                    const float now = top[0] * scale;
                     const bool over = now > m + kGrow;
                     grown = __any_sync(0xffffffffu, over);
                     if (grown) {
@@ -359,20 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             l *= keep;
                             m = now;
                         }
-                        if (j > p.t0) {
-                            // the block's last products are done: its scores came after them
-#pragma unroll
-                            for (int i = 0; i < D; i += 32) {
-                                uint32_t o[32];
-                                tmem_ld32(to + i, o);
-                                wait_ld();
-                                keep32(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                                tmem_st32(to + i, o);
-                            }
-                        }
+                        // the block's last products are done: its scores came after them
+                        if (j > p.t0) rescale(keep);
                     }
                 } while (grown);
                 // the first half's product runs while the second half is computed
@@ -400,7 +504,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             warp_wait(bar_o + 8 * blk, 0, gave_up);
         }
-    } else if (warp < 12) {
+    } else if (kQ8 && warp < 12) {
+        // ---------------------------------------------------------- widening (8-bit pages)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+        // A warp reads 64 of the 128 codes of 8 rows at a time and stores them as f16.  Its
+        // lanes take rows r and r ^ 5 in pairs, so that neither the reads (in 16-byte pieces
+        // swizzled by r) nor the writes (every other piece, swizzled alike) share a bank.
+        const int c = lane % 4, r8 = lane / 8 ^ (lane / 4 % 2 * 5);
+        uint32_t slot = 0, turn = 0, raw = 0, raw_turn = 0;
+        bool live = true;
+        for (int j = T0; j < T1 && live; ++j) {
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                if (live) live = warp_wait(bar_raw + 8 * raw, raw_turn, gave_up);
+                if (live) live = warp_wait(bar_empty + 8 * slot, turn ^ 1, gave_up);
+                if (!live) break;
+                const uint8_t* const src = smem + L::kRaw + raw * L::kRawSlot;
+                uint8_t* const dst = smem + L::kRing + slot * L::kSlot;
+                uint4 x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int u = (warp - 8) * 8 + i, r = u / 2 * 8 + r8, h = u % 2;
+                    x[i] = *reinterpret_cast<const uint4*>(src + r * 128 +
+                                                           (((h * 4 + c) ^ r) & 7) * 16);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int u = (warp - 8) * 8 + i, r = u / 2 * 8 + r8, h = u % 2;
+                    uint32_t y[8];
+                    widen4<PAGE>(x[i].x, y[0], y[1]);
+                    widen4<PAGE>(x[i].y, y[2], y[3]);
+                    widen4<PAGE>(x[i].z, y[4], y[5]);
+                    widen4<PAGE>(x[i].w, y[6], y[7]);
+                    const int t = j * kTile + r;
+                    if (side == 1 && (t < lo || t >= hi)) {  // V rows no query sees
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = 0;
+                    }
+                    uint8_t* const row = dst + h * (kTile * 128) + r * 128;
+                    *reinterpret_cast<uint4*>(row + ((2 * c ^ r) & 7) * 16) =
+                        make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ r) & 7) * 16) =
+                        make_uint4(y[4], y[5], y[6], y[7]);
+                }
+                fence_smem_async();
+                warp_arrive(bar_full + 8 * slot);
+                warp_arrive(bar_raw_empty + 8 * raw);
+                if (++slot == L::kSlots) slot = 0, turn ^= 1;
+                if (++raw == L::kRawSlots) raw = 0, raw_turn ^= 1;
+            }
+        }
+    } else if (!kQ8 && warp < 12) {
         // -------------------------------------------------------------- producers
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
         // Copy k of a tile (page k / kHalves, column k % kHalves) is issued by warp k % 4,
@@ -408,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int bs = a.r.block_size, me = warp - 8;
         const int box = min(bs, kTile);               // slots of a copy
         const int copies = kTile / box * L::kHalves;  // of a tile
-        const int k = lane * kProducers + me, my_page = k / L::kHalves, my_half = k % L::kHalves;
+        const int k = lane * L::kProducers + me, my_page = k / L::kHalves, my_half = k % L::kHalves;
         const bool mine = k < copies;
         const int32_t* table = a.r.table + (int64_t)b * a.r.max_blocks;
         auto seen = [&](int j) {
@@ -456,13 +610,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // V: zero those rows once the copies are there, then hand the tile over
                     live = warp_wait(bar_patch + 8 * me, patches++ & 1, gave_up);
                     if (!live) break;
-                    for (int c = me; c < copies; c += kProducers) {
+                    for (int c = me; c < copies; c += L::kProducers) {
                         const int first = c / L::kHalves * box;
                         uint8_t* const col = smem + L::kRing + slot * L::kSlot +
                                              c % L::kHalves * (kTile * 128) + lane % 8 * 16;
                         for (int r = first + lane / 8; r < first + box; r += 4) {
                             const int t = j * kTile + r;
-                            if (t < lo || t >= hi || !(which >> (c / kProducers) & 1))
+                            if (t < lo || t >= hi || !(which >> (c / L::kProducers) & 1))
                                 *reinterpret_cast<uint4*>(col + r * 128) = make_uint4(0, 0, 0, 0);
                         }
                     }
@@ -484,10 +638,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssuerRegs));
     }
+    if (kQ8 && warp >= 14) {
+        // -------------------------------------------------------- producers (8-bit pages)
+        // One copy a page, issued by warp 14 + page % 2, lane page / 2; the lane also brings
+        // the page's scales, one tile ahead.
+        const int bs = a.r.block_size, me = warp - 14;
+        const int box = min(bs, kTile), pages = kTile / box;
+        const int page = lane * L::kProducers + me;
+        const bool mine = page < pages;
+        const int32_t* table = a.r.table + (int64_t)b * a.r.max_blocks;
+        auto seen = [&](int j) {
+            const int t = j * kTile + page * box;
+            return mine && j < T1 && t < hi && t + box > lo;
+        };
+        auto id_of = [&](int j) {
+            return seen(j) ? __ldg(table + (j * kTile + page * box) / bs) : -1;
+        };
+        auto scale_of = [&](const float* scales, int id, float none) {
+            return PB && id >= 0 && id < a.r.num_blocks
+                       ? __ldg(scales + (int64_t)id * a.hkv + head)
+                       : none;
+        };
+        int id = id_of(T0), after = id_of(T0 + 1);
+        float ks = scale_of(a.k_scale, id, 1.f), vs = scale_of(a.v_scale, id, 0.f);
+        uint32_t raw = 0, turn = 0, n = 0;
+        bool live = true;
+        for (int j = T0; j < T1 && live; ++j) {
+            const int later = id_of(j + 2);
+            const float next_ks = scale_of(a.k_scale, after, 1.f);
+            const float next_vs = scale_of(a.v_scale, after, 0.f);
+            const bool ok = id >= 0 && id < a.r.num_blocks;
+            if (seen(j) && !ok) {
+                latch(a.r.err, PGD_ERR_BLOCK_ID);
+                *bad = 1;
+            }
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * box * 128;
+            const int row = (j * kTile + page * box) % bs;
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                if (live) live = warp_wait(bar_raw_empty + 8 * raw, turn ^ 1, gave_up);
+                if (!live) break;
+                if (PB && side == 0 && mine) {
+                    // the tile kScaleTiles back is done with: its slot in the ring was reused
+                    float* const to = reinterpret_cast<float*>(
+                        smem + L::kScales + (j - T0) % L::kScaleTiles * 128);
+                    for (int g = page * box / 8; g < (page + 1) * box / 8; ++g) {
+                        to[g] = ks < 1e-30f ? 1e-30f : ks;
+                        to[kTile / 8 + g] = vs;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (bytes)
+                        bar_arrive_tx(bar_raw + 8 * raw, bytes);
+                    else
+                        bar_arrive(bar_raw + 8 * raw);
+                }
+                __syncwarp();
+                if (ok)
+                    tma_load_4d(base + L::kRaw + raw * L::kRawSlot + page * box * 128,
+                                side ? &map_v : &map_k, bar_raw + 8 * raw, 0, row, head, id);
+                if (++raw == L::kRawSlots) raw = 0, turn ^= 1;
+                ++n;
+            }
+            id = after;
+            after = later;
+            ks = next_ks;
+            vs = next_vs;
+        }
+        if (!live) {  // no copy of this warp may land after the CTA has ended
+            volatile int never = 0;
+            for (uint32_t i = n > L::kRawSlots ? n - L::kRawSlots : 0; i < n; ++i)
+                bar_wait(bar_raw + 8 * (i % L::kRawSlots), i / L::kRawSlots & 1, &never);
+        }
+    }
     if ((warp == 12 || warp == 13) && T1 > T0) {
         // --------------------------------------------------------------- products
-        constexpr uint32_t kQK = instruction(kBlock, kTile, 1, 0);
-        constexpr uint32_t kPV = instruction(kBlock, D, 1, 1);
+        constexpr uint32_t kQK = instruction(kBlock, kTile, !kQ8, 0);
+        constexpr uint32_t kPV = instruction(kBlock, D, !kQ8, 1);
         constexpr uint32_t kHi = operand_hi(1024);
         const int i = warp - 12;  // the block whose products this warp issues
         const int t0 = i ? sp[1].t0 : sp[0].t0, t1 = i ? sp[1].t1 : sp[0].t1;
@@ -586,10 +814,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // -------------------------------------------------------------------- results
     const int64_t out_at = (int64_t)s.row0 * a.hq + (int64_t)head * a.group;  // head vectors
+    // what the accumulator is to be multiplied with beside 1 / l
+    const float by = !kQ8 ? 1.f : PB ? 1.f / vgain : __ldg(a.v_scale + head);
     if (a.cluster == 1) {
         if (warp < 8) {
             const uint32_t to = tmem + (uint32_t(warp % 4 * 32) << 16) + 2 * kTile + blk * D;
-            const float inv = failed ? NAN : l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN;
+            const float inv = failed ? NAN : l > 0.f ? by / l : l == 0.f ? 0.f : NAN;
             const bool have = blk ? sp[1].t1 > sp[1].t0 : sp[0].t1 > sp[0].t0;
             uint8_t* const rowp = smem + (blk * kBlock + my_row) * (D * 2);
 #pragma unroll
@@ -607,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 4; ++k) {
                         const float y0 = __uint_as_float(o[e + 2 * k]) * inv;
                         const float y1 = __uint_as_float(o[e + 2 * k + 1]) * inv;
-                        w[k] = inv == 0.f ? 0u : inv != inv ? 0x7fc07fc0u : bf16x2(y0, y1);
+                        w[k] = l == 0.f && !failed ? 0u : inv != inv ? 0x7fc07fc0u : bf16x2(y0, y1);
                     }
                     const int c = (i + e) / 8;
                     *reinterpret_cast<uint4*>(rowp + ((c ^ my_row) & (D / 8 - 1)) * 16) =
@@ -650,7 +880,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int c = (i + e) / 4;
                         *reinterpret_cast<uint4*>(smem + L::kRing + r * (D * 4) +
                                                   ((c ^ r) & (D / 4 - 1)) * 16) =
-                            make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            make_uint4(__float_as_uint(__uint_as_float(o[e]) * by),
+                                       __float_as_uint(__uint_as_float(o[e + 1]) * by),
+                                       __float_as_uint(__uint_as_float(o[e + 2]) * by),
+                                       __float_as_uint(__uint_as_float(o[e + 3]) * by));
                     }
                 }
             }
