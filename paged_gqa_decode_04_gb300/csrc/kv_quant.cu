@@ -4,25 +4,27 @@
 // (paged_qk_norm_rope_write).  See include/paged_kv_manager.h for the contract.
 //
 // Mathematics of a head vector x of D elements at position p:
-//     y = x * rsqrt(mean(x^2) + eps) * w                        (norm, optional)
-//     (a, b) -> (a cos - b sin, b cos + a sin) for the pairs j < R / 2 of the first R
-//     elements, cos and sin from the caller's table at p        (rotation, optional)
+//     r = rsqrt(mean(x^2) + eps)                                (norm, optional)
+//     y_e = r (x_e w_e cos - x_f w_f sin)   or   r (x_e w_e cos + x_f w_f sin)
+// for the first or second of a rotated pair (e, f), cos and sin from the caller's table at
+// p, and y_e = r x_e w_e outside the rotated part: with w_e cos and -+ w_f sin made once
+// for a token, two products, a sum and r for all its heads.
 //     8-bit pages: code = rn(y / scale), saturated.
 // All of it in float32 and in registers, with one rounding at the end: to the output
 // type, or to the code.
 //
-// What bounds it: bytes.  Every row is read once and written once, about ten operations
-// an element.  So: 16-byte accesses, a lane holds 8 consecutive elements of a head (16
-// lanes a vector at D = 128), the sum of squares and the rotation partner by shuffles,
-// and a warp issues the loads of 16 head vectors before it uses the first.
+// What bounds it: bytes, once the instructions are few.  Every row is read once and written
+// once.  16-byte accesses, a lane holds 8 consecutive elements of a head (16 lanes a vector
+// at D = 128), sums of squares and rotation partners by shuffles, and a warp issues the
+// loads of 16 head vectors before it uses the first.
 //
-// Work of a warp.  K and V: one (chunk of tokens, KV head, K or V).  Where the scale
-// belongs to a block, the chunk is the block: the largest magnitude of its new rows has
-// to be known before the first code, and the rows stay in registers in between; blocks
-// of more than 16 tokens are shared by up to 8 warps of a CTA, which exchange their
-// maxima through shared memory.  Otherwise chunks are 16 tokens.  No two warps write one
-// scale and there are no atomics, so the pages do not depend on timing.  Queries: one
-// (token, 16 heads), whose cosines, sines and weights are loaded once.
+// Work of a warp.  One token's 16 query heads, or 8 KV heads with K and V, whose angles and
+// weights are loaded once.  Where a scale belongs to a block, K and V go by blocks instead:
+// one (block, KV head, K or V), since the largest magnitude of a block's new rows has to be
+// known before its first code; the rows stay in registers in between, and blocks of more
+// than 16 tokens are shared by up to 8 warps of a CTA, which exchange their maxima through
+// shared memory.  No two warps write one scale and there are no atomics, so the pages do
+// not depend on timing.
 #include <cuda_fp8.h>
 
 #include "page_ops.h"
@@ -61,9 +63,11 @@ struct WriteArgs {
     void* v_pool;
     float* k_scale;
     float* v_scale;
-    int chunk_shift;      // log2 of the tokens of a K/V chunk
-    int warps_per_unit;   // warps sharing one (chunk, head, K or V)
-    int64_t kv_ctas;      // CTAs of the K/V part; the query part follows
+    int chunk_shift;      // scale per block: log2 of the block's tokens,
+    int warps_per_unit;   // warps sharing one (block, head, K or V),
+    uint32_t block_ctas;  // and the CTAs of these units; token units follow
+    uint32_t q_groups;    // units of a token: 16 query heads each,
+    uint32_t kv_groups;   // then 8 KV heads each
 };
 
 // ---------------------------------------------------------- 8 elements of a lane
@@ -74,6 +78,12 @@ struct Raw<__nv_bfloat16> {
     uint4 a;
     __device__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
     __device__ void zero() { a = make_uint4(0, 0, 0, 0); }
+    __device__ Raw from(int lane) const {  // the same 8 places of another lane
+        Raw r;
+        r.a = make_uint4(__shfl_sync(0xffffffffu, a.x, lane), __shfl_sync(0xffffffffu, a.y, lane),
+                         __shfl_sync(0xffffffffu, a.z, lane), __shfl_sync(0xffffffffu, a.w, lane));
+        return r;
+    }
     __device__ void get(float (&x)[8]) const {
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -91,6 +101,14 @@ struct Raw<float> {
         b = reinterpret_cast<const float4*>(p)[1];
     }
     __device__ void zero() { a = b = make_float4(0, 0, 0, 0); }
+    __device__ Raw from(int lane) const {
+        Raw r;
+        r.a = make_float4(__shfl_sync(0xffffffffu, a.x, lane), __shfl_sync(0xffffffffu, a.y, lane),
+                          __shfl_sync(0xffffffffu, a.z, lane), __shfl_sync(0xffffffffu, a.w, lane));
+        r.b = make_float4(__shfl_sync(0xffffffffu, b.x, lane), __shfl_sync(0xffffffffu, b.y, lane),
+                          __shfl_sync(0xffffffffu, b.z, lane), __shfl_sync(0xffffffffu, b.w, lane));
+        return r;
+    }
     __device__ void get(float (&x)[8]) const {
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
         x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
@@ -125,16 +143,17 @@ template <int PAGE>
 __device__ __forceinline__ uint2 codes8(const float (&x)[8]) {
     uint32_t w[2];
     if (PAGE == PGD_INT8) {
+        // 1.5 * 2^23 more, a float32 has its integer, rounded to even, in its low bits
+        uint32_t c[8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            w[i] = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float v = x[4 * i + j];
-                const int c = v == v ? __float2int_rn(fminf(fmaxf(v, -127.f), 127.f)) : 0;
-                w[i] |= uint32_t(c & 0xff) << (8 * j);
-            }
+        for (int i = 0; i < 8; ++i) {
+            const float v = x[i] == x[i] ? fminf(fmaxf(x[i], -127.f), 127.f) : 0.f;
+            c[i] = __float_as_uint(v + 12582912.f);
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040),
+                               __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
     } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -166,80 +185,112 @@ __device__ __forceinline__ void values8(uint2 c, float (&x)[8]) {
 }
 
 // ------------------------------------------------------------- norm and rotation
-// The lane's 8 weights (ones without a norm).
+// The lane's 8 weights at d0 (ones without a norm).
 __device__ __forceinline__ void load_weights(const void* w, int f32, int d0, float (&out)[8]) {
+    if (!w) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        out[i] = !w ? 1.f
-                 : f32 ? __ldg(static_cast<const float*>(w) + d0 + i)
-                       : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[d0 + i]);
-}
-
-// The lane's 8 cosines and sines at position p (interleaved: 4 of each).
-__device__ __forceinline__ void load_angles(const Prep& pr, int p, int d0, float (&cs)[8],
-                                            float (&sn)[8]) {
-    const int half = pr.rope_dim / 2;
-    const float* t = pr.rope + (int64_t)p * pr.rope_dim;
-    if (d0 >= pr.rope_dim) {
+        for (int i = 0; i < 8; ++i) out[i] = 1.f;
+    } else if ((reinterpret_cast<uintptr_t>(w) & 15) != 0) {  // a weight inside a larger tensor
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
-    } else if (pr.interleaved) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(t + d0 / 2));
-        const float4 s = __ldg(reinterpret_cast<const float4*>(t + half + d0 / 2));
-        cs[0] = c.x, cs[1] = c.y, cs[2] = c.z, cs[3] = c.w;
-        sn[0] = s.x, sn[1] = s.y, sn[2] = s.z, sn[3] = s.w;
+        for (int i = 0; i < 8; ++i)
+            out[i] = f32 ? __ldg(static_cast<const float*>(w) + d0 + i)
+                         : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[d0 + i]);
+    } else if (f32) {
+        Raw<float> r;
+        r.load(static_cast<const float*>(w) + d0);
+        r.get(out);
     } else {
-        const int j = d0 < half ? d0 : d0 - half;
-        const float4* c = reinterpret_cast<const float4*>(t + j);
-        const float4* s = reinterpret_cast<const float4*>(t + half + j);
-        const float4 c0 = __ldg(c), c1 = __ldg(c + 1), s0 = __ldg(s), s1 = __ldg(s + 1);
-        cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w;
-        cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
-        sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w;
-        sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
+        Raw<__nv_bfloat16> r;
+        r.load(static_cast<const __nv_bfloat16*>(w) + d0);
+        r.get(out);
     }
 }
 
-// Norm and rotate the lane's 8 elements of a head vector; the D / 8 lanes of a vector
-// (and the whole warp) call this together.
-template <int D>
-__device__ __forceinline__ void norm_rotate(const Prep& pr, bool norm, const float (&w)[8],
-                                            const float (&cs)[8], const float (&sn)[8], int d0,
-                                            float (&x)[8]) {
-    if (norm) {
-        float ss = 0.f;
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+// What the lane's 8 elements of a token's heads are multiplied with: themselves and their
+// partners.
+struct Turn {
+    float own[8], other[8];
+    int src;      // the lane of the partners; -1: none here, or (interleaved) in this lane
+    bool norm;
+
+    __device__ __forceinline__ void make(const Prep& pr, const void* weight, int d0, int p) {
+        const int half = pr.rope_dim / 2, lane = threadIdx.x & 31;
+        const float* t = pr.rope + (int64_t)p * pr.rope_dim;
+        norm = weight != nullptr;
+        src = -1;
+        load_weights(weight, pr.weight_f32, d0, own);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-        for (int m = 1; m < D / 8; m *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-        const float r = rsqrtf(ss * (1.f / D) + pr.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-    }
-    if (!pr.rope) return;
-    if (pr.interleaved) {
-        if (d0 < pr.rope_dim) {
+        for (int i = 0; i < 8; ++i) other[i] = 0.f;
+        if (d0 >= pr.rope_dim) return;  // also without a rotation
+        if (pr.interleaved) {
+            const float4 c4 = __ldg(reinterpret_cast<const float4*>(t + d0 / 2));
+            const float4 s4 = __ldg(reinterpret_cast<const float4*>(t + half + d0 / 2));
+            const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float a = x[2 * i], b = x[2 * i + 1];
-                x[2 * i] = a * cs[i] - b * sn[i];
-                x[2 * i + 1] = b * cs[i] + a * sn[i];
+                other[2 * i] = -own[2 * i + 1] * s[i];
+                other[2 * i + 1] = own[2 * i] * s[i];
+                own[2 * i] *= c[i];
+                own[2 * i + 1] *= c[i];
+            }
+        } else {
+            const bool low = d0 < half;
+            float c[8], s[8];
+            src = low ? lane + half / 8 : lane - half / 8;
+            load8(t + (low ? d0 : d0 - half), c);
+            load8(t + half + (low ? d0 : d0 - half), s);
+            load_weights(weight, pr.weight_f32, low ? d0 + half : d0 - half, other);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                own[i] *= c[i];
+                other[i] *= low ? -s[i] : s[i];
             }
         }
-        return;
     }
-    // the partner of element j is j +- rope_dim / 2: the same place in another lane
-    const int half = pr.rope_dim / 2, lane = threadIdx.x & 31;
-    const bool low = d0 < half, in = d0 < pr.rope_dim;
-    const int src = !in ? lane : low ? lane + half / 8 : lane - half / 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float o = __shfl_sync(0xffffffffu, x[i], src);
-        if (in) x[i] = low ? x[i] * cs[i] - o * sn[i] : x[i] * cs[i] + o * sn[i];
-    }
-}
 
-// -------------------------------------------------------------------------- K, V
+    // The lane's 8 elements of a vector, normed and rotated; a whole warp calls it together.
+    template <typename Act, int D>
+    __device__ __forceinline__ void apply(const Prep& pr, const Raw<Act>& raw,
+                                          float (&y)[8]) const {
+        float x[8], z[8];
+        raw.get(x);
+        float r = 1.f;
+        if (norm) {
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+            for (int k = 1; k < D / 8; k *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+            r = rsqrtf(ss * (1.f / D) + pr.eps);
+        }
+        if (!pr.rope) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = x[i] * own[i] * r;
+            return;
+        }
+        if (pr.interleaved) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = x[i ^ 1];
+        } else {
+            raw.from(src >= 0 ? src : (threadIdx.x & 31)).get(z);
+        }
+        const bool in = pr.interleaved ? threadIdx.x % (D / 8) * 8 < pr.rope_dim : src >= 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            y[i] = x[i] * own[i];
+            if (in) y[i] = fmaf(z[i], other[i], y[i]);
+            y[i] *= r;
+        }
+    }
+};
+
 template <int PAGE>
 struct PageType {
     using type = uint8_t;
@@ -253,24 +304,33 @@ struct PageType<PGD_BF16> {
     using type = __nv_bfloat16;
 };
 
-template <typename Act, int PAGE, int D, bool PB, bool PREP>
-__device__ __forceinline__ void write_kv(const WriteArgs& a, float* smax) {
+// ------------------------------------------------- K, V with a scale for each block
+// Largest finite magnitude of 8 elements, joined with `top`.
+__device__ __forceinline__ float finite_max(const float (&x)[8], float top) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float m = fabsf(x[i]);
+        top = fmaxf(top, m < INFINITY ? m : 0.f);
+    }
+    return top;
+}
+
+template <int PAGE, int D, bool PREP>
+__device__ __forceinline__ void write_blocks(const WriteArgs& a, float* smax) {
+    using Act = __nv_bfloat16;
     constexpr int kLanes = D / 8;              // lanes of a head vector
     constexpr int kRows = 32 / kLanes;         // vectors of a warp at once
     constexpr int kIters = kChunk / kRows;
-    using Page = typename PageType<PAGE>::type;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int sub = lane / kLanes, d0 = lane % kLanes * 8;
-    const int W = PB ? a.warps_per_unit : 1;
-    const int64_t unit = (int64_t)blockIdx.x * (kWarps / W) + warp / W;
-    const int part = warp % W;
-    const int per = 2 * a.hkv;
-    const int64_t piece = unit / per;
+    const int W = a.warps_per_unit, part = warp % W;
+    const uint32_t unit = blockIdx.x * (kWarps / W) + warp / W, per = 2 * a.hkv;
+    const uint32_t piece = unit / per;
     const int side = int(unit % per) / a.hkv, h = int(unit % per) % a.hkv;
 
     Seq s;
     s.ok = false;
-    int chunk = 0, lo = 0, hi = 0;  // the chunk's number in the sequence; rows of it to write
+    int chunk = 0, lo = 0, hi = 0;  // the block's number in the sequence; its rows to write
     const int b = find_seq(a.r, piece, 1, a.chunk_shift, 2);
     if (b < a.r.B) {
         s = load_seq(a.r, b);
@@ -285,16 +345,19 @@ __device__ __forceinline__ void write_kv(const WriteArgs& a, float* smax) {
             if (hi <= lo) s.ok = false;
         }
     }
-    const Act* src = static_cast<const Act*>(side ? a.v : a.k);
+    const int64_t blk = s.ok ? block_of(a.r, s.b, chunk) : -1;
+    const int at = s.ok ? chunk << a.chunk_shift : 0;
     const int64_t stride = side ? a.v_stride : a.k_stride;
-    Page* pool = static_cast<Page*>(side ? a.v_pool : a.k_pool);
-    float* scales = side ? a.v_scale : a.k_scale;
-    const int64_t at = (int64_t)chunk << a.chunk_shift;
-    // packed row of the chunk's row j: row0 + (at + j) - (len - n)
-    const int64_t row_of = s.ok ? s.row0 + at - (s.len - s.n) : 0;
+    // this lane's elements of packed row j of the block, and of pool row j
+    const Act* const src = static_cast<const Act*>(side ? a.v : a.k) +
+                           (int64_t)(s.ok ? s.row0 + at - (s.len - s.n) : 0) * stride + h * D + d0;
+    const int row = a.hkv * D;
+    uint8_t* const dst = static_cast<uint8_t*>(side ? a.v_pool : a.k_pool) +
+                         (max(blk, (int64_t)0) << a.chunk_shift) * row + h * D + d0;
+    float* const scale = (side ? a.v_scale : a.k_scale) + max(blk, (int64_t)0) * a.hkv + h;
     const bool prep = PREP && side == 0;
-    float w[8];
-    if (prep) load_weights(a.prep.k_weight, a.prep.weight_f32, d0, w);
+    const int rows = 1 << a.chunk_shift;
+    const int passes = (rows + W * kChunk - 1) / (W * kChunk);
 
     Raw<Act> raw[kIters];
     auto load = [&](int j0) {
@@ -302,148 +365,179 @@ __device__ __forceinline__ void write_kv(const WriteArgs& a, float* smax) {
         for (int i = 0; i < kIters; ++i) {
             const int j = j0 + i * kRows + sub;
             raw[i].zero();
-            if (j >= lo && j < hi) raw[i].load(src + (row_of + j) * stride + h * D + d0);
+            if (j >= lo && j < hi) raw[i].load(src + j * stride);
         }
     };
-    // values of row j (all lanes of the warp call this for the same i)
-    auto value = [&](int i, int j, float (&x)[8]) {
-        raw[i].get(x);
-        if (prep) {
-            float cs[8], sn[8];
-            if (a.prep.rope)
-                load_angles(a.prep, j >= lo && j < hi ? int(at) + j : 0, d0, cs, sn);
-            norm_rotate<D>(a.prep, a.prep.k_weight != nullptr, w, cs, sn, d0, x);
-        }
-    };
-    auto slot_of = [&](int64_t blk, int64_t pos) {
-        return ((blk * a.r.block_size + pos % a.r.block_size) * a.hkv + h) * D + d0;
-    };
-
-    if (!PB) {
-        if (!s.ok) return;
-        float inv = 1.f;
-        if (PAGE == PGD_FP8_E4M3 || PAGE == PGD_INT8) inv = inverse(__ldg(scales + h));
-        load(0);
-#pragma unroll
-        for (int i = 0; i < kIters; ++i) {
-            const int j = i * kRows + sub;
-            float x[8];
-            value(i, j, x);
-            if (j < lo || j >= hi) continue;
-            const int64_t pos = at + j;
-            const int64_t blk = block_of(a.r, s.b, int(pos / a.r.block_size));
-            if (blk < 0) continue;
-            if constexpr (PAGE == PGD_FP8_E4M3 || PAGE == PGD_INT8) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= inv;
-                *reinterpret_cast<uint2*>(pool + slot_of(blk, pos)) = codes8<PAGE>(x);
-            } else {
-                store8(pool + slot_of(blk, pos), x);
-            }
-        }
-    } else if constexpr (PAGE == PGD_FP8_E4M3 || PAGE == PGD_INT8) {
-        const int64_t blk = s.ok ? block_of(a.r, s.b, chunk) : -1;
-        const int rows = 1 << a.chunk_shift;
-        const int passes = (rows + W * kChunk - 1) / (W * kChunk);
-        // the old scale first: its latency passes under the rows' loads
-        const float was = blk >= 0 && lo > 0 ? scales[blk * a.hkv + h] : 0.f;
-        float top = 0.f;
-        for (int p = 0; p < passes; ++p) {
-            if (blk < 0) break;
-            const int j0 = (p * W + part) * kChunk;
-            load(j0);
-#pragma unroll
-            for (int i = 0; i < kIters; ++i) {
-                float x[8];
-                value(i, j0 + i * kRows + sub, x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float m = fabsf(x[e]);
-                    top = fmaxf(top, m < INFINITY ? m : 0.f);  // NaN and infinities left out
-                }
-            }
-        }
-#pragma unroll
-        for (int m = 1; m < 32; m *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        if (W > 1) {
-            if (lane == 0) smax[warp] = top;
-            __syncthreads();
-            for (int i = 0; i < W; ++i) top = fmaxf(top, smax[warp / W * W + i]);
-        }
-        if (blk < 0) return;
-        float now = top * (1.f / code_max<PAGE>());
-        if (!(now >= kTiny)) now = 0.f;
-        now = fmaxf(now, was);
-        const float inv = inverse(now);
-        if (part == 0 && lane == 0) scales[blk * a.hkv + h] = now;
-        // rows cached in the block before this call take the larger scale
-        if (now > was && lo > 0) {
-            const float ratio = was * inv;
-            for (int j = part * kRows + sub; j < lo; j += W * kRows) {
-                uint2* c = reinterpret_cast<uint2*>(pool + slot_of(blk, j));
-                float x[8];
-                values8<PAGE>(*c, x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= ratio;
-                *c = codes8<PAGE>(x);
-            }
-        }
-        for (int p = passes - 1; p >= 0; --p) {
-            const int j0 = (p * W + part) * kChunk;
-            if (p != passes - 1) load(j0);
+    float y[PREP ? kIters : 1][8];  // values of the rows held, where they are not the raw ones
+    auto prepare = [&](int j0) {
+        if constexpr (PREP) {
 #pragma unroll
             for (int i = 0; i < kIters; ++i) {
                 const int j = j0 + i * kRows + sub;
-                float x[8];
-                value(i, j, x);
-                if (j < lo || j >= hi) continue;
+                if (prep) {
+                    Turn turn;
+                    turn.make(a.prep, a.prep.k_weight, d0, j >= lo && j < hi ? at + j : 0);
+                    turn.template apply<Act, D>(a.prep, raw[i], y[i]);
+                } else {
+                    raw[i].get(y[i]);
+                }
+            }
+        }
+    };
+    // the old scale first: its latency passes under the rows' loads
+    const float was = blk >= 0 && lo > 0 ? *scale : 0.f;
+    float top = 0.f;
+    for (int p = 0; p < passes && blk >= 0; ++p) {
+        const int j0 = (p * W + part) * kChunk;
+        load(j0);
+        prepare(j0);
+        if constexpr (PREP) {
+#pragma unroll
+            for (int i = 0; i < kIters; ++i) top = finite_max(y[i], top);
+        } else {
+            // bfloat16 magnitudes are ordered like their bits, two of them at once
+            uint32_t most = 0;
+#pragma unroll
+            for (int i = 0; i < kIters; ++i) {
+                most = __vmaxu2(most, raw[i].a.x & 0x7fff7fffu);
+                most = __vmaxu2(most, raw[i].a.y & 0x7fff7fffu);
+                most = __vmaxu2(most, raw[i].a.z & 0x7fff7fffu);
+                most = __vmaxu2(most, raw[i].a.w & 0x7fff7fffu);
+            }
+            const uint32_t larger = max(most & 0xffffu, most >> 16);
+            if (larger < 0x7f80u) {
+                top = fmaxf(top, __uint_as_float(larger << 16));
+            } else {  // an infinity or NaN, which take no part
+#pragma unroll
+                for (int i = 0; i < kIters; ++i) {
+                    float x[8];
+                    raw[i].get(x);
+                    top = finite_max(x, top);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+    if (W > 1) {
+        if (lane == 0) smax[warp] = top;
+        __syncthreads();
+        for (int i = 0; i < W; ++i) top = fmaxf(top, smax[warp / W * W + i]);
+    }
+    if (blk < 0) return;
+    float now = top * (1.f / code_max<PAGE>());
+    if (!(now >= kTiny)) now = 0.f;
+    now = fmaxf(now, was);
+    const float inv = inverse(now);
+    if (part == 0 && lane == 0) *scale = now;
+    // rows cached in the block before this call take the larger scale
+    if (now > was && lo > 0) {
+        const float ratio = was * inv;
+        for (int j = part * kRows + sub; j < lo; j += W * kRows) {
+            uint2* c = reinterpret_cast<uint2*>(dst + j * row);
+            float x[8];
+            values8<PAGE>(*c, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= ratio;
+            *c = codes8<PAGE>(x);
+        }
+    }
+    for (int p = passes - 1; p >= 0; --p) {
+        const int j0 = (p * W + part) * kChunk;
+        if (p != passes - 1) {
+            load(j0);
+            prepare(j0);
+        }
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) {
+            const int j = j0 + i * kRows + sub;
+            float x[8];
+            if constexpr (PREP) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = y[i][e] * inv;
+            } else {
+                raw[i].get(x);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] *= inv;
-                *reinterpret_cast<uint2*>(pool + slot_of(blk, j)) = codes8<PAGE>(x);
             }
+            if (j >= lo && j < hi) *reinterpret_cast<uint2*>(dst + j * row) = codes8<PAGE>(x);
         }
     }
 }
 
-// ----------------------------------------------------------------------- queries
-template <typename Act, int D>
-__device__ __forceinline__ void prep_q(const WriteArgs& a) {
+// ------------------------------------------------------------------ heads of a token
+template <typename Act, int PAGE, int D, bool PREP>
+__device__ __forceinline__ void write_tokens(const WriteArgs& a) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIters = kChunk / kRows;
+    constexpr bool q8 = PAGE == PGD_FP8_E4M3 || PAGE == PGD_INT8;
+    using Page = typename PageType<PAGE>::type;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int sub = lane / kLanes, d0 = lane % kLanes * 8;
-    const int groups = (a.hq + kChunk - 1) / kChunk;
-    const int64_t unit = ((int64_t)blockIdx.x - a.kv_ctas) * kWarps + warp;
-    const int64_t t = unit / groups;
-    const int h0 = int(unit % groups) * kChunk;
+    const uint32_t groups = a.q_groups + a.kv_groups;
+    const uint32_t unit = (blockIdx.x - a.block_ctas) * kWarps + warp;
+    const int t = unit / groups, group = unit % groups;
     if (t >= a.r.total) return;
-    const Act* q = static_cast<const Act*>(a.q) + t * a.q_stride + d0;
+    const bool kv = group >= (int)a.q_groups;
+    const int h0 = kv ? (group - a.q_groups) * (kChunk / 2) : group * kChunk;
+    // vector i of the unit: query head h0 + i, or K of KV head h0 + i, i < 8, then V
     Raw<Act> raw[kIters];
+    const Act* const q = static_cast<const Act*>(a.q) + t * a.q_stride + d0;
+    const Act* const k = static_cast<const Act*>(a.k) + t * a.k_stride + d0;
+    const Act* const v = static_cast<const Act*>(a.v) + t * a.v_stride + d0;
 #pragma unroll
     for (int i = 0; i < kIters; ++i) {  // the rows do not wait for the sequence's tables
-        const int h = h0 + i * kRows + sub;
+        const int h = h0 + i % (kv ? kIters / 2 : kIters) * kRows + sub;
         raw[i].zero();
-        if (h < a.hq) raw[i].load(q + h * D);
+        if (h < (kv ? a.hkv : a.hq)) raw[i].load((kv ? i < kIters / 2 ? k : v : q) + h * D);
     }
-    float w[8], cs[8], sn[8];
-    load_weights(a.prep.q_weight, a.prep.weight_f32, d0, w);
     const int b = find_seq(a.r, t, 1, 0, 0);
     if (b >= a.r.B) return;  // a row behind the last sequence
     Seq s = load_seq(a.r, b);
     if (s.n > s.len) s.ok = false;
     if (t < s.row0 || (s.ok && t >= s.row0 + s.n)) return;
-    if (s.ok && a.prep.rope) load_angles(a.prep, s.len - s.n + int(t - s.row0), d0, cs, sn);
-    Act* out = static_cast<Act*>(a.q_out) + t * a.q_out_stride + d0;
+    const int pos = s.ok ? s.len - s.n + (t - s.row0) : 0;
+    Turn turn;
+    if (PREP) turn.make(a.prep, kv ? a.prep.k_weight : a.prep.q_weight, d0, pos);
+    if (!kv) {
+        if constexpr (PREP) {
+            Act* const out = static_cast<Act*>(a.q_out) + t * a.q_out_stride + d0;
+#pragma unroll
+            for (int i = 0; i < kIters; ++i) {
+                const int h = h0 + i * kRows + sub;
+                float y[8];
+                turn.template apply<Act, D>(a.prep, raw[i], y);
+                if (!s.ok) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = NAN;
+                }
+                if (h < a.hq) store8(out + h * D, y);
+            }
+        }
+        return;
+    }
+    if (!s.ok) return;
+    const int64_t blk = block_of(a.r, b, pos / a.r.block_size);
+    if (blk < 0) return;
+    const int64_t to = ((blk * a.r.block_size + pos % a.r.block_size) * a.hkv) * D + d0;
 #pragma unroll
     for (int i = 0; i < kIters; ++i) {
-        const int h = h0 + i * kRows + sub;
-        float x[8];
-        raw[i].get(x);
-        norm_rotate<D>(a.prep, a.prep.q_weight != nullptr, w, cs, sn, d0, x);
-        if (!s.ok) {
+        const bool val = i >= kIters / 2;
+        const int h = h0 + i % (kIters / 2) * kRows + sub;
+        float y[8];
+        if (PREP && !val)
+            turn.template apply<Act, D>(a.prep, raw[i], y);
+        else
+            raw[i].get(y);
+        if (h >= a.hkv) continue;
+        Page* const dst = static_cast<Page*>(val ? a.v_pool : a.k_pool) + to + h * D;
+        if constexpr (q8) {
+            const float inv = inverse(__ldg((val ? a.v_scale : a.k_scale) + h));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = NAN;
+            for (int e = 0; e < 8; ++e) y[e] *= inv;
+            *reinterpret_cast<uint2*>(dst) = codes8<PAGE>(y);
+        } else {
+            store8(dst, y);
         }
-        if (h < a.hq) store8(out + h * D, x);
     }
 }
 
@@ -451,10 +545,11 @@ template <typename Act, int PAGE, int D, bool PB, bool PREP>
 __global__ void __launch_bounds__(kWarps * 32) write_kernel(const WriteArgs a) {
     __shared__ float smax[kWarps];
     if (blockIdx.x == 0) check_all(a.r, true);
-    if (blockIdx.x < a.kv_ctas)
-        write_kv<Act, PAGE, D, PB, PREP>(a, smax);
-    else if (PREP)
-        prep_q<Act, D>(a);
+    if (PB && blockIdx.x < a.block_ctas) {
+        if constexpr (PB) write_blocks<PAGE, D, PREP>(a, smax);
+    } else {
+        write_tokens<Act, PAGE, D, PREP>(a);
+    }
 }
 
 template <typename Act, int PAGE, int D>
@@ -477,20 +572,24 @@ cudaError_t launch(const WriteArgs& a, bool pb, bool prep, int64_t ctas, cudaStr
 
 int run_write(const Pool& p, WriteArgs& a, bool prep, void* stream) {
     const bool pb = is_q8(p.dtype) && p.scale_per_block;
-    a.chunk_shift = 4;
-    a.warps_per_unit = 1;
+    int64_t block_ctas = 0;
     if (pb) {  // block_size is a power of two in 8 .. 256
         a.chunk_shift = 3;
+        a.warps_per_unit = 1;
         while ((1 << a.chunk_shift) < p.block_size) ++a.chunk_shift;
         while (a.warps_per_unit < kWarps && a.warps_per_unit * kChunk < p.block_size)
             a.warps_per_unit *= 2;
+        const int64_t units = max_pieces(a.r.total, a.r.B, 1, a.chunk_shift, 2) * 2 * p.hkv;
+        if (units > INT32_MAX) return PGD_ERR_SHAPE;
+        const int per_cta = kWarps / a.warps_per_unit;
+        block_ctas = (units + per_cta - 1) / per_cta;
     }
-    const int64_t units = max_pieces(a.r.total, a.r.B, 1, a.chunk_shift, 2) * 2 * p.hkv;
-    const int per_cta = kWarps / a.warps_per_unit;
-    a.kv_ctas = (units + per_cta - 1) / per_cta;
-    const int64_t q_units = prep ? (int64_t)a.r.total * ((a.hq + kChunk - 1) / kChunk) : 0;
-    const int64_t ctas = a.kv_ctas + (q_units + kWarps - 1) / kWarps;
-    if (ctas > INT32_MAX) return PGD_ERR_SHAPE;
+    a.block_ctas = uint32_t(block_ctas);
+    a.q_groups = prep ? (a.hq + kChunk - 1) / kChunk : 0;
+    a.kv_groups = pb ? 0 : (a.hkv + kChunk / 2 - 1) / (kChunk / 2);
+    const int64_t units = (int64_t)a.r.total * (a.q_groups + a.kv_groups);
+    const int64_t ctas = block_ctas + (units + kWarps - 1) / kWarps;
+    if (units > INT32_MAX || ctas > INT32_MAX) return PGD_ERR_SHAPE;
     OnDevice dev(p.device);
     if (!dev.ok) return PGD_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
