@@ -213,25 +213,41 @@ __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
     x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
+// Place of the lane's 8 elements in the rotation, and their weights and partners' weights.
+struct Place {
+    int d0;
+    bool in, low;  // inside the rotated part; first of a pair (two halves)
+    int src;       // lane that has the partners (two halves), else this one
+    bool norm;
+    float w[8], wp[8];
+
+    __device__ __forceinline__ Place(const Prep& pr, const void* weight, int d) {
+        const int half = pr.rope_dim / 2, lane = threadIdx.x & 31;
+        d0 = d;
+        in = d < pr.rope_dim;
+        low = d < half;
+        src = !in || pr.interleaved ? lane : low ? lane + half / 8 : lane - half / 8;
+        norm = weight != nullptr;
+        load_weights(weight, pr.weight_f32, d, w);
+        if (in && !pr.interleaved)
+            load_weights(weight, pr.weight_f32, low ? d + half : d - half, wp);
+    }
+};
+
 // What the lane's 8 elements of a token's heads are multiplied with: themselves and their
 // partners.
 struct Turn {
     float own[8], other[8];
-    int src;      // the lane of the partners; -1: none here, or (interleaved) in this lane
-    bool norm;
 
-    __device__ __forceinline__ void make(const Prep& pr, const void* weight, int d0, int p) {
-        const int half = pr.rope_dim / 2, lane = threadIdx.x & 31;
-        const float* t = pr.rope + (int64_t)p * pr.rope_dim;
-        norm = weight != nullptr;
-        src = -1;
-        load_weights(weight, pr.weight_f32, d0, own);
+    __device__ __forceinline__ Turn(const Prep& pr, const Place& at, int p) {
+        const int half = pr.rope_dim / 2;
+        const float* const t = pr.rope + (int64_t)p * pr.rope_dim;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) other[i] = 0.f;
-        if (d0 >= pr.rope_dim) return;  // also without a rotation
+        for (int i = 0; i < 8; ++i) own[i] = at.w[i], other[i] = 0.f;
+        if (!at.in) return;  // also without a rotation
         if (pr.interleaved) {
-            const float4 c4 = __ldg(reinterpret_cast<const float4*>(t + d0 / 2));
-            const float4 s4 = __ldg(reinterpret_cast<const float4*>(t + half + d0 / 2));
+            const float4 c4 = __ldg(reinterpret_cast<const float4*>(t + at.d0 / 2));
+            const float4 s4 = __ldg(reinterpret_cast<const float4*>(t + half + at.d0 / 2));
             const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -241,28 +257,25 @@ struct Turn {
                 own[2 * i + 1] *= c[i];
             }
         } else {
-            const bool low = d0 < half;
             float c[8], s[8];
-            src = low ? lane + half / 8 : lane - half / 8;
-            load8(t + (low ? d0 : d0 - half), c);
-            load8(t + half + (low ? d0 : d0 - half), s);
-            load_weights(weight, pr.weight_f32, low ? d0 + half : d0 - half, other);
+            load8(t + (at.low ? at.d0 : at.d0 - half), c);
+            load8(t + half + (at.low ? at.d0 : at.d0 - half), s);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 own[i] *= c[i];
-                other[i] *= low ? -s[i] : s[i];
+                other[i] = at.low ? -at.wp[i] * s[i] : at.wp[i] * s[i];
             }
         }
     }
 
     // The lane's 8 elements of a vector, normed and rotated; a whole warp calls it together.
     template <typename Act, int D>
-    __device__ __forceinline__ void apply(const Prep& pr, const Raw<Act>& raw,
+    __device__ __forceinline__ void apply(const Prep& pr, const Place& at, const Raw<Act>& raw,
                                           float (&y)[8]) const {
         float x[8], z[8];
         raw.get(x);
         float r = 1.f;
-        if (norm) {
+        if (at.norm) {
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
@@ -270,22 +283,16 @@ struct Turn {
             for (int k = 1; k < D / 8; k *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, k);
             r = rsqrtf(ss * (1.f / D) + pr.eps);
         }
-        if (!pr.rope) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = x[i] * own[i] * r;
-            return;
-        }
         if (pr.interleaved) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) z[i] = x[i ^ 1];
         } else {
-            raw.from(src >= 0 ? src : (threadIdx.x & 31)).get(z);
+            raw.from(at.src).get(z);
         }
-        const bool in = pr.interleaved ? threadIdx.x % (D / 8) * 8 < pr.rope_dim : src >= 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             y[i] = x[i] * own[i];
-            if (in) y[i] = fmaf(z[i], other[i], y[i]);
+            if (at.in) y[i] = fmaf(z[i], other[i], y[i]);
             y[i] *= r;
         }
     }
@@ -315,7 +322,77 @@ __device__ __forceinline__ float finite_max(const float (&x)[8], float top) {
     return top;
 }
 
-template <int PAGE, int D, bool PREP>
+// Block number `piece` of the call: its sequence, its first token, its rows [lo, hi) to
+// write and its place in the pool (-1: none, or out of range).
+struct Block {
+    Seq s;
+    int at, lo, hi;
+    int64_t id;
+
+    __device__ __forceinline__ Block(const WriteArgs& a, uint32_t piece) {
+        s.ok = false;
+        at = lo = hi = 0;
+        id = -1;
+        const int b = find_seq(a.r, piece, 1, a.chunk_shift, 2);
+        if (b >= a.r.B) return;
+        s = load_seq(a.r, b);
+        if (!s.ok || s.n > s.len) return;
+        const int start = s.len - s.n;
+        const int i = (start >> a.chunk_shift) +
+                      int(piece - first_piece(a.r, b, 1, a.chunk_shift, 2));
+        const int64_t first = (int64_t)i << a.chunk_shift;
+        lo = int(max(first, (int64_t)start) - first);
+        hi = first < s.len ? int(min((int64_t)s.len - first, (int64_t)1 << a.chunk_shift)) : 0;
+        if (hi <= lo) return;
+        at = int(first);
+        id = block_of(a.r, b, i);
+    }
+    // packed row of the block's row 0
+    __device__ __forceinline__ int64_t row() const { return s.row0 + at - (s.len - s.n); }
+};
+
+// The scale a block takes from the largest magnitude of its new rows and the scale before.
+template <int PAGE>
+__device__ __forceinline__ float new_scale(float top, float was) {
+    const float now = top * (1.f / code_max<PAGE>());
+    return fmaxf(now >= kTiny ? now : 0.f, was);
+}
+
+// 8 codes at a larger scale: rows cached in a block before this call.
+template <int PAGE>
+__device__ __forceinline__ void requantise(uint8_t* p, float ratio) {
+    float x[8];
+    values8<PAGE>(*reinterpret_cast<uint2*>(p), x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= ratio;
+    *reinterpret_cast<uint2*>(p) = codes8<PAGE>(x);
+}
+
+// Largest finite magnitude of some vectors of a lane.  bfloat16 magnitudes are ordered like
+// their bits, two of them at once.
+template <int N>
+__device__ __forceinline__ float largest(const Raw<__nv_bfloat16> (&raw)[N]) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        most = __vmaxu2(most, raw[i].a.x & 0x7fff7fffu);
+        most = __vmaxu2(most, raw[i].a.y & 0x7fff7fffu);
+        most = __vmaxu2(most, raw[i].a.z & 0x7fff7fffu);
+        most = __vmaxu2(most, raw[i].a.w & 0x7fff7fffu);
+    }
+    most = max(most & 0xffffu, most >> 16);
+    if (most < 0x7f80u) return __uint_as_float(most << 16);
+    float top = 0.f;  // an infinity or NaN, which take no part
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float x[8];
+        raw[i].get(x);
+        top = finite_max(x, top);
+    }
+    return top;
+}
+
+template <int PAGE, int D>
 __device__ __forceinline__ void write_blocks(const WriteArgs& a, float* smax) {
     using Act = __nv_bfloat16;
     constexpr int kLanes = D / 8;              // lanes of a head vector
@@ -325,37 +402,17 @@ __device__ __forceinline__ void write_blocks(const WriteArgs& a, float* smax) {
     const int sub = lane / kLanes, d0 = lane % kLanes * 8;
     const int W = a.warps_per_unit, part = warp % W;
     const uint32_t unit = blockIdx.x * (kWarps / W) + warp / W, per = 2 * a.hkv;
-    const uint32_t piece = unit / per;
     const int side = int(unit % per) / a.hkv, h = int(unit % per) % a.hkv;
-
-    Seq s;
-    s.ok = false;
-    int chunk = 0, lo = 0, hi = 0;  // the block's number in the sequence; its rows to write
-    const int b = find_seq(a.r, piece, 1, a.chunk_shift, 2);
-    if (b < a.r.B) {
-        s = load_seq(a.r, b);
-        if (s.n > s.len) s.ok = false;
-        if (s.ok) {
-            const int start = s.len - s.n;
-            chunk = (start >> a.chunk_shift) +
-                    int(piece - first_piece(a.r, b, 1, a.chunk_shift, 2));
-            const int64_t at = (int64_t)chunk << a.chunk_shift;
-            lo = int(max(at, (int64_t)start) - at);
-            hi = at < s.len ? int(min((int64_t)s.len - at, (int64_t)1 << a.chunk_shift)) : 0;
-            if (hi <= lo) s.ok = false;
-        }
-    }
-    const int64_t blk = s.ok ? block_of(a.r, s.b, chunk) : -1;
-    const int at = s.ok ? chunk << a.chunk_shift : 0;
+    const Block blk(a, unit / per);
+    const int lo = blk.lo, hi = blk.hi;
     const int64_t stride = side ? a.v_stride : a.k_stride;
     // this lane's elements of packed row j of the block, and of pool row j
-    const Act* const src = static_cast<const Act*>(side ? a.v : a.k) +
-                           (int64_t)(s.ok ? s.row0 + at - (s.len - s.n) : 0) * stride + h * D + d0;
+    const Act* const src = static_cast<const Act*>(side ? a.v : a.k) + blk.row() * stride + h * D + d0;
     const int row = a.hkv * D;
+    const int64_t id = max(blk.id, (int64_t)0);
     uint8_t* const dst = static_cast<uint8_t*>(side ? a.v_pool : a.k_pool) +
-                         (max(blk, (int64_t)0) << a.chunk_shift) * row + h * D + d0;
-    float* const scale = (side ? a.v_scale : a.k_scale) + max(blk, (int64_t)0) * a.hkv + h;
-    const bool prep = PREP && side == 0;
+                         (id << a.chunk_shift) * row + h * D + d0;
+    float* const scale = (side ? a.v_scale : a.k_scale) + id * a.hkv + h;
     const int rows = 1 << a.chunk_shift;
     const int passes = (rows + W * kChunk - 1) / (W * kChunk);
 
@@ -368,54 +425,12 @@ __device__ __forceinline__ void write_blocks(const WriteArgs& a, float* smax) {
             if (j >= lo && j < hi) raw[i].load(src + j * stride);
         }
     };
-    float y[PREP ? kIters : 1][8];  // values of the rows held, where they are not the raw ones
-    auto prepare = [&](int j0) {
-        if constexpr (PREP) {
-#pragma unroll
-            for (int i = 0; i < kIters; ++i) {
-                const int j = j0 + i * kRows + sub;
-                if (prep) {
-                    Turn turn;
-                    turn.make(a.prep, a.prep.k_weight, d0, j >= lo && j < hi ? at + j : 0);
-                    turn.template apply<Act, D>(a.prep, raw[i], y[i]);
-                } else {
-                    raw[i].get(y[i]);
-                }
-            }
-        }
-    };
     // the old scale first: its latency passes under the rows' loads
-    const float was = blk >= 0 && lo > 0 ? *scale : 0.f;
+    const float was = blk.id >= 0 && lo > 0 ? *scale : 0.f;
     float top = 0.f;
-    for (int p = 0; p < passes && blk >= 0; ++p) {
-        const int j0 = (p * W + part) * kChunk;
-        load(j0);
-        prepare(j0);
-        if constexpr (PREP) {
-#pragma unroll
-            for (int i = 0; i < kIters; ++i) top = finite_max(y[i], top);
-        } else {
-            // bfloat16 magnitudes are ordered like their bits, two of them at once
-            uint32_t most = 0;
-#pragma unroll
-            for (int i = 0; i < kIters; ++i) {
-                most = __vmaxu2(most, raw[i].a.x & 0x7fff7fffu);
-                most = __vmaxu2(most, raw[i].a.y & 0x7fff7fffu);
-                most = __vmaxu2(most, raw[i].a.z & 0x7fff7fffu);
-                most = __vmaxu2(most, raw[i].a.w & 0x7fff7fffu);
-            }
-            const uint32_t larger = max(most & 0xffffu, most >> 16);
-            if (larger < 0x7f80u) {
-                top = fmaxf(top, __uint_as_float(larger << 16));
-            } else {  // an infinity or NaN, which take no part
-#pragma unroll
-                for (int i = 0; i < kIters; ++i) {
-                    float x[8];
-                    raw[i].get(x);
-                    top = finite_max(x, top);
-                }
-            }
-        }
+    for (int p = 0; p < passes && blk.id >= 0; ++p) {
+        load((p * W + part) * kChunk);
+        top = fmaxf(top, largest(raw));
     }
 #pragma unroll
     for (int m = 1; m < 32; m *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
@@ -424,43 +439,126 @@ __device__ __forceinline__ void write_blocks(const WriteArgs& a, float* smax) {
         __syncthreads();
         for (int i = 0; i < W; ++i) top = fmaxf(top, smax[warp / W * W + i]);
     }
-    if (blk < 0) return;
-    float now = top * (1.f / code_max<PAGE>());
-    if (!(now >= kTiny)) now = 0.f;
-    now = fmaxf(now, was);
-    const float inv = inverse(now);
+    if (blk.id < 0) return;
+    const float now = new_scale<PAGE>(top, was), inv = inverse(now);
     if (part == 0 && lane == 0) *scale = now;
-    // rows cached in the block before this call take the larger scale
-    if (now > was && lo > 0) {
-        const float ratio = was * inv;
-        for (int j = part * kRows + sub; j < lo; j += W * kRows) {
-            uint2* c = reinterpret_cast<uint2*>(dst + j * row);
-            float x[8];
-            values8<PAGE>(*c, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= ratio;
-            *c = codes8<PAGE>(x);
-        }
-    }
+    if (now > was)
+        for (int j = part * kRows + sub; j < lo; j += W * kRows)
+            requantise<PAGE>(dst + j * row, was * inv);
     for (int p = passes - 1; p >= 0; --p) {
         const int j0 = (p * W + part) * kChunk;
-        if (p != passes - 1) {
-            load(j0);
-            prepare(j0);
-        }
+        if (p != passes - 1) load(j0);
 #pragma unroll
         for (int i = 0; i < kIters; ++i) {
             const int j = j0 + i * kRows + sub;
             float x[8];
-            if constexpr (PREP) {
+            raw[i].get(x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = y[i][e] * inv;
-            } else {
-                raw[i].get(x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= inv;
-            }
+            for (int e = 0; e < 8; ++e) x[e] *= inv;
             if (j >= lo && j < hi) *reinterpret_cast<uint2*>(dst + j * row) = codes8<PAGE>(x);
+        }
+    }
+}
+
+// The same with keys normed and rotated first: a CTA takes a block of 8 KV heads, K and V,
+// and a warp one token after the other, so that a token's angles serve all its heads.  Rows
+// are read twice (the second time from L1) instead of held: 8 heads of float32 values would
+// leave room for few warps.  `smax`: the largest magnitudes of [K, V][8 heads].
+template <int PAGE, int D>
+__device__ __forceinline__ void norm_blocks(const WriteArgs& a, float* smax) {
+    using Act = __nv_bfloat16;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kHeads = kChunk / 2;
+    constexpr int kIters = kHeads / kRows;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int sub = lane / kLanes, d0 = lane % kLanes * 8;
+    const uint32_t groups = (a.hkv + kHeads - 1) / kHeads;
+    const int h0 = int(blockIdx.x % groups) * kHeads + sub;  // head of vector i: h0 + i kRows
+    const Block blk(a, blockIdx.x / groups);
+    if (blk.id < 0) return;  // the whole CTA
+    const int lo = blk.lo, hi = blk.hi, row = a.hkv * D;
+    const Act* const k = static_cast<const Act*>(a.k) + blk.row() * a.k_stride + h0 * D + d0;
+    const Act* const v = static_cast<const Act*>(a.v) + blk.row() * a.v_stride + h0 * D + d0;
+    const int64_t pool_at = (blk.id << a.chunk_shift) * row + h0 * D + d0;
+    const Place place(a.prep, a.prep.k_weight, d0);
+
+    Raw<Act> rk[kIters], rv[kIters];
+    auto load = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) {
+            rk[i].zero();
+            rv[i].zero();
+            if (h0 + i * kRows < a.hkv) {
+                rk[i].load(k + j * a.k_stride + i * kRows * D);
+                rv[i].load(v + j * a.v_stride + i * kRows * D);
+            }
+        }
+    };
+    float top[2][kIters] = {}, was[2][kIters] = {};
+    if (threadIdx.x < 2 * kHeads) smax[threadIdx.x] = 0.f;
+    for (int j = lo + warp; j < hi; j += kWarps) {
+        load(j);
+        const Turn turn(a.prep, place, blk.at + j);
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) {
+            float y[8];
+            turn.template apply<Act, D>(a.prep, place, rk[i], y);
+            top[0][i] = finite_max(y, top[0][i]);
+            const Raw<Act> one[1] = {rv[i]};
+            top[1][i] = fmaxf(top[1][i], largest(one));
+        }
+    }
+    __syncthreads();  // smax is zero
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) {
+            const int h = h0 + i * kRows;
+            float t = top[side][i];
+#pragma unroll
+            for (int m = 1; m < kLanes; m *= 2) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, m));
+            // magnitudes are ordered like their bits; a maximum has no order of arrival
+            if (lane % kLanes == 0)
+                atomicMax(reinterpret_cast<int*>(smax) + side * kHeads + i * kRows + sub,
+                          __float_as_int(t));
+            if (lo > 0 && h < a.hkv)
+                was[side][i] = (side ? a.v_scale : a.k_scale)[blk.id * a.hkv + h];
+        }
+    __syncthreads();
+    float inv[2][kIters];
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) {
+            const int h = h0 + i * kRows;
+            uint8_t* const dst =
+                static_cast<uint8_t*>(side ? a.v_pool : a.k_pool) + pool_at + i * kRows * D;
+            const float now =
+                new_scale<PAGE>(smax[side * kHeads + i * kRows + sub], was[side][i]);
+            inv[side][i] = inverse(now);
+            if (h >= a.hkv) continue;
+            if (warp == 0 && lane % kLanes == 0)
+                (side ? a.v_scale : a.k_scale)[blk.id * a.hkv + h] = now;
+            if (now > was[side][i])
+                for (int j = warp; j < lo; j += kWarps)
+                    requantise<PAGE>(dst + j * row, was[side][i] * inv[side][i]);
+        }
+    for (int j = lo + warp; j < hi; j += kWarps) {
+        load(j);
+        const Turn turn(a.prep, place, blk.at + j);
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) {
+            float y[8], x[8];
+            turn.template apply<Act, D>(a.prep, place, rk[i], y);
+            rv[i].get(x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                y[e] *= inv[0][i];
+                x[e] *= inv[1][i];
+            }
+            if (h0 + i * kRows >= a.hkv) continue;
+            const int64_t to = pool_at + j * row + i * kRows * D;
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.k_pool) + to) = codes8<PAGE>(y);
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v_pool) + to) = codes8<PAGE>(x);
         }
     }
 }
@@ -496,8 +594,8 @@ __device__ __forceinline__ void write_tokens(const WriteArgs& a) {
     if (s.n > s.len) s.ok = false;
     if (t < s.row0 || (s.ok && t >= s.row0 + s.n)) return;
     const int pos = s.ok ? s.len - s.n + (t - s.row0) : 0;
-    Turn turn;
-    if (PREP) turn.make(a.prep, kv ? a.prep.k_weight : a.prep.q_weight, d0, pos);
+    const Place place(a.prep, !PREP ? nullptr : kv ? a.prep.k_weight : a.prep.q_weight, d0);
+    const Turn turn(a.prep, place, pos);
     if (!kv) {
         if constexpr (PREP) {
             Act* const out = static_cast<Act*>(a.q_out) + t * a.q_out_stride + d0;
@@ -505,7 +603,7 @@ __device__ __forceinline__ void write_tokens(const WriteArgs& a) {
             for (int i = 0; i < kIters; ++i) {
                 const int h = h0 + i * kRows + sub;
                 float y[8];
-                turn.template apply<Act, D>(a.prep, raw[i], y);
+                turn.template apply<Act, D>(a.prep, place, raw[i], y);
                 if (!s.ok) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[e] = NAN;
@@ -525,7 +623,7 @@ __device__ __forceinline__ void write_tokens(const WriteArgs& a) {
         const int h = h0 + i % (kIters / 2) * kRows + sub;
         float y[8];
         if (PREP && !val)
-            turn.template apply<Act, D>(a.prep, raw[i], y);
+            turn.template apply<Act, D>(a.prep, place, raw[i], y);
         else
             raw[i].get(y);
         if (h >= a.hkv) continue;
@@ -541,12 +639,24 @@ __device__ __forceinline__ void write_tokens(const WriteArgs& a) {
     }
 }
 
+// CTAs an SM is to hold, which bounds a thread's registers: 3 (80 registers) where a token's
+// heads are normed and rotated (67k tokens: 285 us, 353 with 2 CTAs, 363 with 4 and spills),
+// 4 for plain writes; one fewer with float32 rows.
+template <typename Act, bool PREP>
+constexpr int ctas_per_sm() {
+    return (PREP ? 3 : 4) - (sizeof(Act) == 4);
+}
+
 template <typename Act, int PAGE, int D, bool PB, bool PREP>
-__global__ void __launch_bounds__(kWarps * 32) write_kernel(const WriteArgs a) {
-    __shared__ float smax[kWarps];
+__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<Act, PREP>())
+    write_kernel(const WriteArgs a) {
+    __shared__ float smax[2 * kWarps];
     if (blockIdx.x == 0) check_all(a.r, true);
     if (PB && blockIdx.x < a.block_ctas) {
-        if constexpr (PB) write_blocks<PAGE, D, PREP>(a, smax);
+        if constexpr (PB && PREP)
+            norm_blocks<PAGE, D>(a, smax);
+        else if constexpr (PB)
+            write_blocks<PAGE, D>(a, smax);
     } else {
         write_tokens<Act, PAGE, D, PREP>(a);
     }
@@ -579,10 +689,11 @@ int run_write(const Pool& p, WriteArgs& a, bool prep, void* stream) {
         while ((1 << a.chunk_shift) < p.block_size) ++a.chunk_shift;
         while (a.warps_per_unit < kWarps && a.warps_per_unit * kChunk < p.block_size)
             a.warps_per_unit *= 2;
-        const int64_t units = max_pieces(a.r.total, a.r.B, 1, a.chunk_shift, 2) * 2 * p.hkv;
+        const int64_t blocks = max_pieces(a.r.total, a.r.B, 1, a.chunk_shift, 2);
+        const int64_t units = blocks * 2 * p.hkv, per_cta = kWarps / a.warps_per_unit;
         if (units > INT32_MAX) return PGD_ERR_SHAPE;
-        const int per_cta = kWarps / a.warps_per_unit;
-        block_ctas = (units + per_cta - 1) / per_cta;
+        block_ctas = prep ? blocks * ((p.hkv + kChunk / 2 - 1) / (kChunk / 2))
+                          : (units + per_cta - 1) / per_cta;
     }
     a.block_ctas = uint32_t(block_ctas);
     a.q_groups = prep ? (a.hq + kChunk - 1) / kChunk : 0;
