@@ -127,45 +127,44 @@ def paged_kv_copy_blocks(pool, src, dst, stream=None):
 
 
 def _check_tables(pool, cu_seqlens, block_table, seq_lens):
-    """The tables of a ragged call: dtypes, shapes and placement."""
+    """The tables of a ragged call: dtypes, shapes and placement.  Returns B."""
+    dev, i32 = pool.device.index, torch.int32
     if cu_seqlens.dim() != 1 or block_table.dim() != 2 or seq_lens.dim() != 1:
         raise ValueError("cu_seqlens must be [B+1], block_table [B,max_blocks], seq_lens [B]")
-    for t in (cu_seqlens, block_table, seq_lens):
-        if t.dtype != torch.int32:
-            raise TypeError("cu_seqlens, block_table and seq_lens must be int32")
+    if not (cu_seqlens.dtype is i32 and block_table.dtype is i32 and seq_lens.dtype is i32):
+        raise TypeError("cu_seqlens, block_table and seq_lens must be int32")
     B = seq_lens.shape[0]
     if cu_seqlens.shape[0] != B + 1 or block_table.shape[0] != B:
         raise ValueError("shape mismatch between cu_seqlens, block_table and seq_lens")
     for t in (cu_seqlens, block_table, seq_lens):
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError("tables must be contiguous CUDA tensors")
-        if t.device != pool.device:
-            raise ValueError("tensors must be on the pool's device")
+        if t.get_device() != dev or not t.is_contiguous():   # -1 for CPU tensors
+            raise ValueError("tables must be contiguous CUDA tensors on the pool's device")
     return B
 
 
 def _check_rows(pool, name, t, heads, total=None):
     """A packed tensor [total, heads, D] whose rows may be apart (a view of a
     projection); returns its row stride in elements."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != pool.head_dim or (
-            total is not None and t.shape[0] != total):
-        raise ValueError("%s must be [total, %s, %d]" % (name, heads, pool.head_dim))
-    if t.dtype != pool.q_dtype:
+    shape, D = t.shape, pool.head_dim
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D or (
+            total is not None and shape[0] != total):
+        raise ValueError("%s must be [total, %s, %d]" % (name, heads, D))
+    if t.dtype is not pool.q_dtype:
         raise TypeError("%s must be %s for this pool" % (name, pool.q_dtype))
-    if not t.is_cuda or t.device != pool.device:
+    if t.get_device() != pool.device.index:
         raise ValueError("%s must be a CUDA tensor on the pool's device" % name)
-    row = heads * pool.head_dim
-    if t.numel() == 0:
-        return row
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != pool.head_dim):
+    if shape[0] == 0 or heads == 0:
+        return heads * D
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != D):
         raise ValueError("%s: the heads of a row must be contiguous" % name)
-    return t.stride(0) if t.shape[0] > 1 else row
+    return s0 if shape[0] > 1 else heads * D
 
 
 def _stream_on(pool, stream):
     """The stream to launch on: by default the current one of the pool's device."""
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream(pool.device).cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(pool.device.index)
     return _stream(stream)
 
 
