@@ -35,9 +35,11 @@
 // only when a row's maximum has grown by more than 2^8: until then weights are relative to
 // an older maximum, at most 256, which costs no precision in either float type.
 //
-// Few rows.  Where the batch has fewer blocks of rows than the GPU has SMs, up to 8 CTAs
-// of a cluster share a block's key tiles and join their sums through each other's shared
-// memory: out = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c.
+// Few rows.  128 rows or fewer go to both blocks, every other tile each, so that one's
+// softmax still hides behind the other's products; and where the batch has fewer pieces of
+// rows than the GPU has SMs, up to 8 CTAs of a cluster share a piece's key tiles.  The parts
+// join their sums through shared memory, each other's in a cluster:
+// out = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k.
 //
 // Every wait is bounded; one that gives up latches PGD_ERR_TIMEOUT and ends the CTA.
 #pragma once
@@ -243,41 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int share = a.cluster > 1 ? (int)cluster_rank() : 0;
     if (blockIdx.x == 0) check_all(a.r, false);
 
-    // the piece of rows: the longest walks first, which for causal rows are the last ones
-    const int64_t unit = blockIdx.x / a.cluster;
-    const int piece = a.pieces - 1 - int(unit % a.pieces);
-    const int head = int(unit / a.pieces);
-    const int b = find_seq(a.r, piece, a.group, kRowShift, 1);
-    if (b >= a.r.B) return;  // the same for the whole cluster
-    const Seq s = load_seq(a.r, b);
-    const uint32_t group = a.group;
-    const int row0 = int(piece - first_piece(a.r, b, a.group, kRowShift, 1)) << kRowShift;
-    // rows of the piece (an impossible sequence's only become NaN)
-    const int n = s.ok ? s.n : min(__ldg(a.r.cu + b + 1), a.r.total) - s.row0;
-    if (row0 < 0 || s.row0 < 0 || n <= 0) return;
-    const int rows = min(n * a.group - row0, 1 << kRowShift);
-    if (rows <= 0) return;
-
-    Span sp[2];
-    sp[0] = span_of(a, s, row0, row0 + min(rows, kBlock) - 1);
-    sp[1] = span_of(a, s, row0 + kBlock, row0 + rows - 1);
-    const bool some0 = sp[0].t1 > sp[0].t0, some1 = sp[1].t1 > sp[1].t0;
-    // tokens and tiles of the CTA
-    const int lo = some0 ? (some1 ? min(sp[0].lo, sp[1].lo) : sp[0].lo) : sp[1].lo;
-    const int hi = max(sp[0].hi, sp[1].hi);
-    int T0 = lo / kTile, T1 = hi > lo ? (hi + kTile - 1) / kTile : T0;
-    if (a.cluster > 1) {  // this CTA's share of the tiles
-        const int tiles = T1 - T0, t = T0;
-        T0 = t + tiles * share / a.cluster;
-        T1 = t + tiles * (share + 1) / a.cluster;
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        sp[i].t0 = max(sp[i].t0, T0);
-        sp[i].t1 = max(sp[i].t0, min(sp[i].t1, T1));
-    }
-
-    if (threadIdx.x == 0) {
+    // one thread sets the barriers up while the other warps look for their sequence
+    if (threadIdx.x == 416) {
         for (int i = 0; i < 2; ++i) {
             bar_init(bar_q + 8 * i, 4);  // warps of a block
             bar_init(bar_s + 8 * i, 1);
@@ -302,6 +271,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         *bad = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+
+    // the piece of rows: the longest walks first, which for causal rows are the last ones
+    const int64_t unit = blockIdx.x / a.cluster;
+    const int piece = a.pieces - 1 - int(unit % a.pieces);
+    const int head = int(unit / a.pieces);
+    const int b = find_seq(a.r, piece, a.group, kRowShift, 1);
+    if (b >= a.r.B) return;  // the same for the whole cluster
+    const Seq s = load_seq(a.r, b);
+    const uint32_t group = a.group;
+    const int row0 = int(piece - first_piece(a.r, b, a.group, kRowShift, 1)) << kRowShift;
+    // rows of the piece (an impossible sequence's only become NaN)
+    const int n = s.ok ? s.n : min(__ldg(a.r.cu + b + 1), a.r.total) - s.row0;
+    if (row0 < 0 || s.row0 < 0 || n <= 0) return;
+    const int rows = min(n * a.group - row0, 1 << kRowShift);
+    if (rows <= 0) return;
+
+    Span sp[2];
+    sp[0] = span_of(a, s, row0, row0 + min(rows, kBlock) - 1);
+    sp[1] = span_of(a, s, row0 + kBlock, row0 + rows - 1);
+    const bool some0 = sp[0].t1 > sp[0].t0, some1 = sp[1].t1 > sp[1].t0;
+    // tokens and tiles of the CTA
+    const int lo = some0 ? (some1 ? min(sp[0].lo, sp[1].lo) : sp[0].lo) : sp[1].lo;
+    const int hi = max(sp[0].hi, sp[1].hi);
+    int T0 = lo / kTile, T1 = hi > lo ? (hi + kTile - 1) / kTile : T0;
+    // 128 rows or fewer: both blocks take them, and every other tile each, where every CTA of
+    // the cluster has two (all of them decide alike)
+    const bool paired = rows <= kBlock && T1 - T0 >= 2 * a.cluster;
+    if (a.cluster > 1) {  // this CTA's share of the tiles
+        const int tiles = T1 - T0, t = T0;
+        T0 = t + tiles * share / a.cluster;
+        T1 = t + tiles * (share + 1) / a.cluster;
+    }
+    if (paired) sp[1] = sp[0];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        sp[i].t0 = max(sp[i].t0, T0);
+        sp[i].t1 = max(sp[i].t0, min(sp[i].t1, T1));
+    }
+
     if (warp == 12) tmem_alloc(smem_addr(tmem_at), 512);
     fence_before();
     __syncthreads();
@@ -312,6 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float vgain = 0.f;             // of the accumulator, with a V scale per block
     const int blk = warp / 4;      // block of rows of a softmax warp
     const int my_row = threadIdx.x % kBlock;
+    const int at_row = (paired ? 0 : blk * kBlock) + my_row;  // in the piece
 
     if (warp < 8) {
         // ---------------------------------------------------------------- softmax
@@ -323,12 +332,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c = my_row % kVecs;
             const __nv_bfloat16* q =
                 a.q + (int64_t)s.row0 * a.q_stride + (int64_t)head * a.group * D + c * 8;
-            Rows at(row0 + blk * kBlock + my_row / kVecs, group, kStep);
+            const int first_row = at_row - my_row + my_row / kVecs;
+            Rows at(row0 + first_row, group, kStep);
             uint4 x[kVecs];
 #pragma unroll
             for (int i = 0; i < kVecs; ++i, at.next()) {  // all loads, then all stores
                 x[i] = make_uint4(0, 0, 0, 0);
-                if (blk * kBlock + my_row / kVecs + i * kStep < rows)
+                if (first_row + i * kStep < rows)
                     x[i] = __ldg(reinterpret_cast<const uint4*>(q + at.token * a.q_stride +
                                                                 at.head * D));
             }
@@ -349,9 +359,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_smem_async();
             warp_arrive(bar_q + 8 * blk);
 
-            const uint32_t R = row0 + blk * kBlock + my_row;
+            const uint32_t R = row0 + at_row;
             int my_lo = 0, my_hi = 0;
-            if (blk * kBlock + my_row < rows) {
+            if (at_row < rows) {
                 const int pos = s.len - s.n + int(R / group);
                 my_hi = a.causal ? pos + 1 : s.len;
                 if (a.window > 0) my_lo = max(0, pos - a.window + 1);
@@ -375,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st32(to + i, o);
                 }
             };
+            const int first = p.t0 + (paired ? blk : 0), by = paired ? 2 : 1;  // its tiles
             // One tile of scores; `edge`: some row does not see all of it.
             auto tile = [&](int j, auto edge) {
                 uint32_t x[kTile], w[kTile / 4];
@@ -393,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (most * vgain > 16.f || vgain == 0.f) {
                         const int e = min(max((__float_as_int(most) >> 23) & 255, 2), 252);
                         const float gain = __int_as_float((254 - e) << 23);
-                        if (j > p.t0) rescale(gain / vgain);
+                        if (j > first) rescale(gain / vgain);
                         vgain = gain;
                     }
                 }
@@ -406,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int g = 0; g <= 8; ++g) {
                         const int at = h * (kTile / 2) + g * 8;
-                        const float by = PB && g < 8 ? scale * ks[h * 8 + g] : scale;
-                        const uint64_t cc = pair(by, by);
+                        const float mul = PB && g < 8 ? scale * ks[h * 8 + g] : scale;
+                        const uint64_t cc = pair(mul, mul);
                         if (g < 8) {
                             if (h == 0 && PB) {
                                 float u = max8(x + g * 8) * ks[g];
@@ -476,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             m = now;
                         }
                         // the block's last products are done: its scores came after them
-                        if (j > p.t0) rescale(keep);
+                        if (j > first) rescale(keep);
                     }
                 } while (grown);
                 // the first half's product runs while the second half is computed
@@ -494,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l += s0 + s1;
             };
             uint32_t phase = 0;
-            for (int j = p.t0; j < p.t1; ++j, phase ^= 1) {
+            for (int j = first; j < p.t1; j += by, phase ^= 1) {
                 if (!warp_wait(bar_s + 8 * blk, phase, gave_up)) break;
                 fence_after();
                 if (j * kTile < p.lo_all || (j + 1) * kTile > p.hi_all)
@@ -719,6 +730,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kHi = operand_hi(1024);
         const int i = warp - 12;  // the block whose products this warp issues
         const int t0 = i ? sp[1].t0 : sp[0].t0, t1 = i ? sp[1].t1 : sp[0].t1;
+        const int first = t0 + (paired ? i : 0);
+        auto sees = [&](int j) { return j >= first && j < t1 && (!paired || !((j - first) & 1)); };
         const uint32_t acc = __shfl_sync(0xffffffffu, tmem, 0);
         const uint32_t acc_s = acc + i * kTile, acc_o = acc + 2 * kTile + i * D;
         const uint32_t q_lo = operand_lo(base, 16) + i * (L::kQ / 16);
@@ -762,9 +775,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (++at == L::kSlots) at = 0, turn ^= 1;
         };
         bool live = wait(bar_full, 0);
-        if (live && T0 == t0 && t0 < t1) live = wait(bar_q + 8 * i, 0);
+        if (live && sees(T0)) live = wait(bar_q + 8 * i, 0);
         if (live) {
-            if (T0 == t0 && t0 < t1)
+            if (sees(T0))
                 scores(0, false);
             else
                 pass(0);
@@ -774,15 +787,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t v_at = at, v_turn = turn;
             step();
             // all that can be waited for is there before the turn is taken
-            const bool now = j >= t0 && j < t1, next = j + 1 >= t0 && j + 1 < t1;
+            const bool now = sees(j), next = sees(j + 1);
             live = wait(bar_full + 8 * v_at, v_turn);
             if (live && j + 1 < T1) live = wait(bar_full + 8 * at, turn);
-            if (live && j + 1 == t0 && next) live = wait(bar_q + 8 * i, 0);
+            if (live && j + 1 == first && next) live = wait(bar_q + 8 * i, 0);
             if (live && now) live = wait(bar_p + 16 * i, weights);
             if (live && (i || j > T0)) live = wait(bar_turn + 8 * i, (j - T0 + 1 - i) & 1);
             if (!live) break;
             if (now) {
-                values(0, v_at, j > t0);
+                values(0, v_at, j > first);
                 live = wait(bar_p + 16 * i + 8, weights);
                 if (!live) break;
                 values(1, v_at, true);
@@ -816,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t out_at = (int64_t)s.row0 * a.hq + (int64_t)head * a.group;  // head vectors
     // what the accumulator is to be multiplied with beside 1 / l
     const float by = !kQ8 ? 1.f : PB ? 1.f / vgain : __ldg(a.v_scale + head);
-    if (a.cluster == 1) {
+    if (a.cluster == 1 && !paired) {
         if (warp < 8) {
             const uint32_t to = tmem + (uint32_t(warp % 4 * 32) << 16) + 2 * kTile + blk * D;
             const float inv = failed ? NAN : l > 0.f ? by / l : l == 0.f ? 0.f : NAN;
@@ -868,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = blk * kBlock + my_row;
             stat[2 * r] = m;
             stat[2 * r + 1] = l;
-            if (have) {
+            if (have && at_row - lane < rows) {
 #pragma unroll
                 for (int i = 0; i < D; i += 32) {
                     uint32_t o[32];
@@ -891,40 +904,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) reinterpret_cast<int*>(stat)[512] = failed;
         cluster_sync();
         if (warp < 8) {
-        bool any_failed = false;
-        for (int k = 0; k < a.cluster; ++k)
-            any_failed |= __float_as_int(peer_ld4(peer_addr(base + 2048, k)).x) != 0;
-        constexpr int kVecs = D / 4;  // four columns a thread
-        for (int i = threadIdx.x + share * 256; i < rows * kVecs; i += a.cluster * 256) {
-            const int r = i / kVecs, c = i % kVecs;
-            float top = -INFINITY;
-            float2 st[8];
+            // part k of a row: CTA k of the cluster, or with paired blocks block k % 2 of CTA k / 2
+            const int parts = paired ? 2 * a.cluster : a.cluster;
+            auto cta_of = [&](int k) { return paired ? k / 2 : k; };
+            auto row_of = [&](int r, int k) { return paired ? r + k % 2 * kBlock : r; };
+            constexpr int kQuads = D / 4;   // four columns a thread
+            constexpr int kAtOnce = 4;      // parts whose sums are on their way together
+            for (int i = threadIdx.x + share * 256; i < rows * kQuads; i += a.cluster * 256) {
+                const int r = i / kQuads, c = i % kQuads;
+                float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f, top = -INFINITY;
+                int any_failed = 0;
+                for (int k0 = 0; k0 < parts; k0 += kAtOnce) {
+                    float2 st[kAtOnce], flag[kAtOnce];
+                    float4 v[kAtOnce];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < a.cluster) {
-                    const float4 v = peer_ld4(peer_addr(base + r / 2 * 16, k));
-                    st[k] = r % 2 ? make_float2(v.z, v.w) : make_float2(v.x, v.y);
-                    top = fmaxf(top, st[k].x);
-                }
-            float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+                    for (int k = 0; k < kAtOnce; ++k) {
+                        const int part = min(k0 + k, parts - 1), rk = row_of(r, part);
+                        st[k] = peer_ld2(peer_addr(base + rk * 8, cta_of(part)));
+                        flag[k] = peer_ld2(peer_addr(base + 2048, cta_of(part)));
+                        v[k] = peer_ld4(peer_addr(
+                            base + L::kRing + rk * (D * 4) + ((c ^ rk) & (kQuads - 1)) * 16,
+                            cta_of(part)));
+                    }
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < a.cluster && st[k].y != 0.f) {
-                    const float w = ex2(st[k].x - top);
-                    const float4 v = peer_ld4(peer_addr(
-                        base + L::kRing + r * (D * 4) + ((c ^ r) & (kVecs - 1)) * 16, k));
-                    sum = fmaf(w, st[k].y, sum);
-                    o[0] = fmaf(w, v.x, o[0]);
-                    o[1] = fmaf(w, v.y, o[1]);
-                    o[2] = fmaf(w, v.z, o[2]);
-                    o[3] = fmaf(w, v.w, o[3]);
+                    for (int k = 0; k < kAtOnce; ++k) {
+                        any_failed |= __float_as_int(flag[k].x);
+                        // a part without a tile of the row left nothing there
+                        if (k0 + k >= parts || st[k].y == 0.f) continue;
+                        const float now = fmaxf(top, st[k].x);
+                        const float keep = ex2(top - now), w = ex2(st[k].x - now);
+                        top = now;
+                        sum = fmaf(w, st[k].y, sum * keep);
+                        o[0] = fmaf(w, v[k].x, o[0] * keep);
+                        o[1] = fmaf(w, v[k].y, o[1] * keep);
+                        o[2] = fmaf(w, v[k].z, o[2] * keep);
+                        o[3] = fmaf(w, v[k].w, o[3] * keep);
+                    }
                 }
-            const float inv = any_failed ? NAN : sum == 0.f ? 0.f : 1.f / sum;
-            const uint32_t R = row0 + r;
-            *reinterpret_cast<uint2*>(a.out + (out_at + (int64_t)(R / group) * a.hq + R % group) * D +
-                                      c * 4) =
-                make_uint2(bf16x2(o[0] * inv, o[1] * inv), bf16x2(o[2] * inv, o[3] * inv));
-        }
+                const float inv = any_failed ? NAN : sum == 0.f ? 0.f : 1.f / sum;
+                const uint32_t R = row0 + r;
+                *reinterpret_cast<uint2*>(
+                    a.out + (out_at + (int64_t)(R / group) * a.hq + R % group) * D + c * 4) =
+                    make_uint2(bf16x2(o[0] * inv, o[1] * inv), bf16x2(o[2] * inv, o[3] * inv));
+            }
         }
         cluster_sync();  // shared memory stays until every CTA has read it
     }
