@@ -38,7 +38,7 @@ cudaError_t launch(const attend::Args& a, const Pool& p, const PageMaps& maps, c
     static std::atomic<uint64_t> ready{0};  // devices whose function attributes are set
     if (!(ready.load() >> p.device & 1)) {
         const cudaError_t e = cudaFuncSetAttribute(
-            attend_kernel<D, PAGE, PB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D, PAGE>::kBytes);
+            attend_kernel<D, PAGE, PB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D, PAGE, PB>::kBytes);
         if (e != cudaSuccess) return e;
         ready.fetch_or(uint64_t(1) << p.device);
     }
@@ -49,7 +49,7 @@ cudaError_t launch(const attend::Args& a, const Pool& p, const PageMaps& maps, c
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(unsigned(a.pieces) * a.hkv * a.cluster);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Layout<D, PAGE>::kBytes;
+    cfg.dynamicSmemBytes = Layout<D, PAGE, PB>::kBytes;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = a.cluster > 1 ? 1 : 0;

@@ -84,22 +84,26 @@ struct Args {
     const float* v_scale;
 };
 
-template <int D, int PAGE>
+template <int D, int PAGE, bool PB>
 struct Layout {
     static constexpr bool kQ8 = PAGE != PGD_BF16;
     static constexpr int kHalves = D / 64;                 // 128-byte columns of a 16-bit tile
     static constexpr int kSlot = kTile * D * 2;            // bytes of a K or V tile
-    static constexpr int kSlots = kQ8 ? 4 : D == 128 ? 5 : 8;
+    static constexpr int kSlots = kQ8 ? PB ? 3 : 4 : D == 128 ? 5 : 8;
     static constexpr int kQ = kBlock * D * 2;              // bytes of a block of queries
     static constexpr int kRing = 2 * kQ;
-    // 8-bit pages: tiles as they are stored, and the scales of the tiles in flight (a tile
-    // is at most 1 + kRawSlots / 2 + kSlots / 2 ahead of the softmax)
+    // 8-bit pages: tiles as they are stored, and the scales of the tiles in flight (a tile is
+    // at most 1 + kRawSlots / 2 + kSlots / 2 ahead of the softmax).  A widened tile's room
+    // holds two more raw ones: with the longer widening of scaled values that is worth it
+    // (490 us, 523 with two, for 2048 tokens behind 8192 at 64 / 8 heads), without it is not
+    // (423 us, 405 with two).
     static constexpr int kRawSlot = kTile * 128;
-    static constexpr int kRawSlots = 2;
+    static constexpr int kRawSlots = PB ? 4 : 2;
     static constexpr int kRaw = kRing + kSlots * kSlot;
     static constexpr int kScaleTiles = 8;
     static constexpr int kScales = kRaw + (kQ8 ? kRawSlots * kRawSlot : 0);
-    static constexpr int kBars = kScales + (kQ8 ? kScaleTiles * 128 : 0);
+    static constexpr int kScaleBytes = 144;                // 16 of K, 16 of V, V's gain
+    static constexpr int kBars = kScales + (kQ8 ? kScaleTiles * kScaleBytes : 0);
     static constexpr int kBytes = kBars + 288 + 1024;      // and room to align to 1024
     // warps that issue copies, and the tiles' 128-byte columns they fetch one by one
     static constexpr int kProducers = kQ8 ? 2 : 4;
@@ -194,12 +198,6 @@ template <int PAGE>
 __device__ __forceinline__ uint32_t operand2(float lo, float hi) {
     return PAGE == PGD_BF16 ? bf16x2(lo, hi) : f16x2(lo, hi);
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // Four codes to two pairs of f16.
 template <int PAGE>
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
@@ -215,10 +213,10 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
         a = *reinterpret_cast<const uint32_t*>(&x);
         b = *reinterpret_cast<const uint32_t*>(&y);
     } else {
-        const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w), __NV_E4M3);
-        const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w >> 16), __NV_E4M3);
-        a = x.x | uint32_t(x.y) << 16;
-        b = y.x | uint32_t(y.y) << 16;
+        asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"
+            " cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+            : "=r"(a), "=r"(b)
+            : "r"(w));
     }
 }
 
@@ -226,7 +224,7 @@ template <int D, int PAGE, bool PB>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
-    using L = Layout<D, PAGE>;
+    using L = Layout<D, PAGE, PB>;
     constexpr bool kQ8 = L::kQ8;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
@@ -235,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t bar_q = bars, bar_s = bars + 16, bar_p = bars + 32, bar_o = bars + 64;
     // bar_patch: one of each producer (bfloat16), bar_raw: full and empty raw slots (8-bit)
     const uint32_t bar_turn = bars + 80, bar_patch = bars + 96, bar_full = bars + 128;
-    const uint32_t bar_raw = bar_patch, bar_raw_empty = bar_raw + 8 * L::kRawSlots;
+    const uint32_t bar_raw = bars + 192, bar_raw_empty = bar_raw + 8 * L::kRawSlots;
     const uint32_t bar_empty = bar_full + 8 * L::kSlots;
     volatile int* const gave_up = reinterpret_cast<int*>(smem + L::kBars + 272);
     volatile int* const bad = reinterpret_cast<int*>(smem + L::kBars + 276);
@@ -391,19 +389,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t x[kTile], w[kTile / 4];
                 uint64_t sum[2];
                 float top[8];
-                // scales of each 8 tokens: K's on the scores, V's (times vgain) on the weights
-                const float* const ks =
-                    reinterpret_cast<const float*>(smem + L::kScales + (j - T0) % 8 * 128);
-                const float* const vs = ks + kTile / 8;
+                // K's scales of each 8 tokens (times the logit multiplier) go on the scores, V's
+                // are in the widened tile, times a gain: the accumulator follows it
+                float ks[PB ? kTile / 8 : 1];
                 if (PB) {
-                    // vgain, a power of two, keeps weight times scale within f16: it starts from
-                    // the first tile's largest scale and falls when one grows past 16 times that
-                    float most = 0.f;
+                    const float* const sc = reinterpret_cast<const float*>(
+                        smem + L::kScales + (j - T0) % L::kScaleTiles * L::kScaleBytes);
 #pragma unroll
-                    for (int i = 0; i < kTile / 8; ++i) most = fmaxf(most, vs[i]);
-                    if (most * vgain > 16.f || vgain == 0.f) {
-                        const int e = min(max((__float_as_int(most) >> 23) & 255, 2), 252);
-                        const float gain = __int_as_float((254 - e) << 23);
+                    for (int i = 0; i < kTile / 8; ++i) ks[i] = sc[i];
+                    const float gain = sc[2 * kTile / 8];
+                    if (gain != vgain) {
                         if (j > first) rescale(gain / vgain);
                         vgain = gain;
                     }
@@ -417,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int g = 0; g <= 8; ++g) {
                         const int at = h * (kTile / 2) + g * 8;
-                        const float mul = PB && g < 8 ? scale * ks[h * 8 + g] : scale;
+                        const float mul = PB && g < 8 ? ks[h * 8 + g] : scale;
                         const uint64_t cc = pair(mul, mul);
                         if (g < 8) {
                             if (h == 0 && PB) {
@@ -444,13 +439,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                         if (g > 0) {
-                            const float gain = PB ? vs[h * 8 + g - 1] * vgain : 1.f;
 #pragma unroll
                             for (int i = -8; i < 0; i += 2) {
-                                float e0 = __uint_as_float(x[at + i]);
-                                float e1 = __uint_as_float(x[at + i + 1]);
+                                const float e0 = __uint_as_float(x[at + i]);
+                                const float e1 = __uint_as_float(x[at + i + 1]);
                                 sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(e0, e1));
-                                if (PB) unpair(mul2(pair(e0, e1), pair(gain, gain)), e0, e1);
                                 w[g * 4 + i / 2] = operand2<PAGE>(e0, e1);
                             }
                         }
@@ -476,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!PB)
                         top[0] = fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]),
                                        max3(top[5], top[6], top[7]));
-                    const float now = top[0] * scale;
+                    const float now = PB ? top[0] : top[0] * scale;
                     const bool over = now > m + kGrow;
                     grown = __any_sync(0xffffffffu, over);
                     if (grown) {
@@ -532,6 +525,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!live) break;
                 const uint8_t* const src = smem + L::kRaw + raw * L::kRawSlot;
                 uint8_t* const dst = smem + L::kRing + slot * L::kSlot;
+                const float* const scales = reinterpret_cast<const float*>(
+                    smem + L::kScales + (j - T0) % L::kScaleTiles * L::kScaleBytes);
+                __half2 by[4];  // V's scale in f16, product in f16: 2^-11 of the value together,
+                                // little beside the output's own 2^-8; K's is kept out, where
+                                // it would move the scores
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (PB && side == 1)
+                        by[i] = __float2half2_rn(scales[kTile / 8 + (warp - 8) * 4 + i] *
+                                                 scales[2 * kTile / 8]);
+                const bool edge = side == 1 && (j * kTile < lo || (j + 1) * kTile > hi);
                 uint4 x[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -547,8 +551,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     widen4<PAGE>(x[i].y, y[2], y[3]);
                     widen4<PAGE>(x[i].z, y[4], y[5]);
                     widen4<PAGE>(x[i].w, y[6], y[7]);
+                    if (PB && side == 1) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const __half2 v = __hmul2(*reinterpret_cast<__half2*>(y + e), by[i / 2]);
+                            y[e] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                    }
                     const int t = j * kTile + r;
-                    if (side == 1 && (t < lo || t >= hi)) {  // V rows no query sees
+                    if (edge && (t < lo || t >= hi)) {  // V rows no query sees
 #pragma unroll
                         for (int e = 0; e < 8; ++e) y[e] = 0;
                     }
@@ -651,35 +662,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (kQ8 && warp >= 14) {
         // -------------------------------------------------------- producers (8-bit pages)
-        // One copy a page, issued by warp 14 + page % 2, lane page / 2; the lane also brings
-        // the page's scales, one tile ahead.
+        // One copy a page, issued by warp 14 + page % 2, lane page / 2.  Warp 14 also brings the
+        // scales, lane by page, one tile ahead, and V's gain: a power of two that puts the
+        // first tile's largest V scale in [1, 2) and falls when one grows past 16 times that,
+        // so that scale times code stays within f16.
         const int bs = a.r.block_size, me = warp - 14;
         const int box = min(bs, kTile), pages = kTile / box;
         const int page = lane * L::kProducers + me;
-        const bool mine = page < pages;
         const int32_t* table = a.r.table + (int64_t)b * a.r.max_blocks;
-        auto seen = [&](int j) {
-            const int t = j * kTile + page * box;
-            return mine && j < T1 && t < hi && t + box > lo;
+        auto seen = [&](int j, int pg) {
+            const int t = j * kTile + pg * box;
+            return pg < pages && j < T1 && t < hi && t + box > lo;
         };
-        auto id_of = [&](int j) {
-            return seen(j) ? __ldg(table + (j * kTile + page * box) / bs) : -1;
+        auto id_of = [&](int j, int pg) {
+            return seen(j, pg) ? __ldg(table + (j * kTile + pg * box) / bs) : -1;
         };
         auto scale_of = [&](const float* scales, int id, float none) {
-            return PB && id >= 0 && id < a.r.num_blocks
-                       ? __ldg(scales + (int64_t)id * a.hkv + head)
-                       : none;
+            return id >= 0 && id < a.r.num_blocks ? __ldg(scales + (int64_t)id * a.hkv + head)
+                                                  : none;
         };
-        int id = id_of(T0), after = id_of(T0 + 1);
-        float ks = scale_of(a.k_scale, id, 1.f), vs = scale_of(a.v_scale, id, 0.f);
+        int id = id_of(T0, page), id_s = -1;
+        float ks = 1.f, vs = 0.f, gain = 0.f;
+        const bool scaling = PB && me == 0;
+        if (scaling) {
+            id_s = id_of(T0, lane);
+            ks = scale_of(a.k_scale, id_s, 1.f);
+            vs = scale_of(a.v_scale, id_s, 0.f);
+            id_s = id_of(T0 + 1, lane);
+        }
         uint32_t raw = 0, turn = 0, n = 0;
         bool live = true;
         for (int j = T0; j < T1 && live; ++j) {
-            const int later = id_of(j + 2);
-            const float next_ks = scale_of(a.k_scale, after, 1.f);
-            const float next_vs = scale_of(a.v_scale, after, 0.f);
+            const int next = id_of(j + 1, page);
+            float next_ks = 1.f, next_vs = 0.f;
+            if (scaling) {
+                next_ks = scale_of(a.k_scale, id_s, 1.f);
+                next_vs = scale_of(a.v_scale, id_s, 0.f);
+                id_s = id_of(j + 2, lane);
+            }
             const bool ok = id >= 0 && id < a.r.num_blocks;
-            if (seen(j) && !ok) {
+            if (seen(j, page) && !ok) {
                 latch(a.r.err, PGD_ERR_BLOCK_ID);
                 *bad = 1;
             }
@@ -689,14 +711,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int side = 0; side < 2; ++side) {
                 if (live) live = warp_wait(bar_raw_empty + 8 * raw, turn ^ 1, gave_up);
                 if (!live) break;
-                if (PB && side == 0 && mine) {
+                if (scaling && side == 0) {
                     // the tile kScaleTiles back is done with: its slot in the ring was reused
                     float* const to = reinterpret_cast<float*>(
-                        smem + L::kScales + (j - T0) % L::kScaleTiles * 128);
-                    for (int g = page * box / 8; g < (page + 1) * box / 8; ++g) {
-                        to[g] = ks < 1e-30f ? 1e-30f : ks;
-                        to[kTile / 8 + g] = vs;
+                        smem + L::kScales + (j - T0) % L::kScaleTiles * L::kScaleBytes);
+                    float most = vs;
+#pragma unroll
+                    for (int m = 1; m < 32; m *= 2)
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
+                    if (most * gain > 16.f || gain == 0.f) {
+                        const int e = min(max((__float_as_int(most) >> 23) & 255, 2), 252);
+                        gain = __int_as_float((254 - e) << 23);
                     }
+                    if (lane < pages)
+                        for (int g = lane * box / 8; g < (lane + 1) * box / 8; ++g) {
+                            to[g] = ks < 1e-30f ? 1e-30f : ks * a.scale_log2;
+                            to[kTile / 8 + g] = vs;
+                        }
+                    if (lane == 0) to[2 * kTile / 8] = gain;
                 }
                 __syncwarp();
                 if (lane == 0) {
@@ -712,8 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++raw == L::kRawSlots) raw = 0, turn ^= 1;
                 ++n;
             }
-            id = after;
-            after = later;
+            id = next;
             ks = next_ks;
             vs = next_vs;
         }
