@@ -2,11 +2,14 @@
 // packed rows, 8-bit pages dequantised (y = code * scale in float32, rounded once).
 //
 // What bounds it: bytes, every page row read once and every output row written once.
-// A token's row of all KV heads is contiguous on both sides, so a warp takes 4
-// consecutive tokens' K and V rows and has 8 loads of 16 bytes a lane in flight; the
-// sequence is searched and checked once a warp.
+// A token's row of all KV heads is contiguous on both sides.  A warp takes 8 consecutive
+// tokens: its lanes find the tokens' pool rows side by side, then K and V of all of them
+// are loaded before the first is stored, 8 codes (16 bytes of other types) a lane, so that
+// every store covers whole sectors.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "page_ops.h"
 #include "paged_kv_manager.h"
@@ -16,7 +19,7 @@ namespace pgd {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kTokens = 4;  // tokens of a warp
+constexpr int kTokens = 8;  // tokens of a warp
 
 struct ReadArgs {
     Ragged r;
@@ -35,85 +38,98 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 16 bytes of a page row as output: 16 codes to 16 bfloat16, else a copy.
+// A lane's piece of a page row, 8 codes or 16 bytes, and its 16 bytes of output.
 template <int PAGE>
-__device__ __forceinline__ void emit(void* out, int64_t vec, uint4 x, float scale) {
-    if (PAGE != PGD_FP8_E4M3 && PAGE != PGD_INT8) {
-        static_cast<uint4*>(out)[vec] = x;
-        return;
-    }
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t o[8];
+struct Piece {
+    static constexpr bool q8 = PAGE == PGD_FP8_E4M3 || PAGE == PGD_INT8;
+    using type = typename std::conditional<q8, uint2, uint4>::type;
+};
+
+template <int PAGE>
+__device__ __forceinline__ uint4 widen(typename Piece<PAGE>::type x, float scale) {
+    if constexpr (!Piece<PAGE>::q8) {
+        return x;
+    } else {
+        const uint32_t w[2] = {x.x, x.y};
+        uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t two = w[i / 2] >> (16 * (i % 2));
-        float2 f;
-        if (PAGE == PGD_INT8)
-            f = make_float2(float(int8_t(two)), float(int8_t(two >> 8)));
-        else
-            f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(two),
-                                                                  __NV_E4M3)));
-        o[i] = bf16x2(f.x * scale, f.y * scale);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t two = w[i / 2] >> (16 * (i % 2));
+            float2 f;
+            if (PAGE == PGD_INT8)
+                f = make_float2(float(int8_t(two)), float(int8_t(two >> 8)));
+            else
+                f = __half22float2(__half2(
+                    __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(two), __NV_E4M3)));
+            o[i] = bf16x2(f.x * scale, f.y * scale);
+        }
+        return make_uint4(o[0], o[1], o[2], o[3]);
     }
-    uint4* p = static_cast<uint4*>(out) + 2 * vec;
-    p[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    p[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 template <int PAGE>
 __global__ void __launch_bounds__(kWarps * 32) read_kernel(const ReadArgs a) {
-    constexpr bool q8 = PAGE == PGD_FP8_E4M3 || PAGE == PGD_INT8;
+    using V = typename Piece<PAGE>::type;
+    constexpr bool q8 = Piece<PAGE>::q8;
     constexpr int elt = PAGE == PGD_F32 ? 4 : PAGE == PGD_BF16 ? 2 : 1;
+    constexpr int kElems = sizeof(V) / elt;  // of a piece
     constexpr uint32_t nan2 = PAGE == PGD_F32 ? 0x7fc00000u : 0x7fc07fc0u;
     if (blockIdx.x == 0) check_all(a.r, true);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTokens;
     if (t0 >= a.r.total) return;
-    const int row_vec = a.hkv * a.d * elt / 16;  // 16-byte vectors of a page row
-    int64_t slot[kTokens];  // pool row of token t0 + i, -1: NaN row, -2: not written
-    int64_t blk[kTokens];
+    const int row_vec = a.hkv * a.d / kElems;  // pieces of a page row
+
+    // token t0 + lane: its pool row, -1: NaN row, -2: not written; its row of scales
+    int64_t my_slot = -2, my_scale = 0;
     int b = find_seq(a.r, t0, 1, 0, 0);
+    const int64_t t = t0 + lane;
+    if (lane < kTokens && t < a.r.total) {
+        while (b < a.r.B && t >= __ldg(a.r.cu + b + 1)) ++b;
+        if (b < a.r.B) {
+            const Seq s = load_seq(a.r, b);
+            if (t >= s.row0) {
+                my_slot = -1;
+                if (s.ok && s.n <= s.len && t < s.row0 + s.n) {
+                    const int pos = s.len - s.n + int(t - s.row0);
+                    const int64_t blk = block_of(a.r, b, pos / a.r.block_size);
+                    if (blk >= 0) my_slot = blk * a.r.block_size + pos % a.r.block_size;
+                    if (a.scale_per_block) my_scale = max(blk, (int64_t)0) * a.hkv;
+                }
+            }
+        }
+    }
+    int64_t slot[kTokens], scale[kTokens];
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
-        slot[i] = -2;
-        blk[i] = 0;
-        const int64_t t = t0 + i;
-        if (t >= a.r.total) continue;
-        if (i && b < a.r.B && t >= __ldg(a.r.cu + b + 1)) b = find_seq(a.r, t, 1, 0, 0);
-        if (b >= a.r.B) continue;
-        const Seq s = load_seq(a.r, b);
-        if (t < s.row0) continue;
-        slot[i] = -1;
-        if (!s.ok || s.n > s.len || t >= s.row0 + s.n) continue;
-        const int pos = s.len - s.n + int(t - s.row0);
-        blk[i] = block_of(a.r, b, pos / a.r.block_size);
-        if (blk[i] >= 0) slot[i] = blk[i] * a.r.block_size + pos % a.r.block_size;
-        blk[i] = max(blk[i], (int64_t)0);
+        slot[i] = __shfl_sync(0xffffffffu, my_slot, i);
+        scale[i] = q8 ? __shfl_sync(0xffffffffu, my_scale, i) : 0;
     }
-    const uint4* kp = static_cast<const uint4*>(a.k_pool);
-    const uint4* vp = static_cast<const uint4*>(a.v_pool);
+    const V* const kp = static_cast<const V*>(a.k_pool);
+    const V* const vp = static_cast<const V*>(a.v_pool);
+    uint4* const ko = static_cast<uint4*>(a.k_out) + t0 * row_vec;
+    uint4* const vo = static_cast<uint4*>(a.v_out) + t0 * row_vec;
     for (int j = lane; j < row_vec; j += 32) {
-        uint4 x[2 * kTokens];
+        const int h = q8 ? j * kElems / a.d : 0;
+        V x[2 * kTokens];
         float sc[2 * kTokens];
 #pragma unroll
         for (int i = 0; i < kTokens; ++i) {
-            x[2 * i] = x[2 * i + 1] = make_uint4(nan2, nan2, nan2, nan2);
-            sc[2 * i] = sc[2 * i + 1] = NAN;
-            if (slot[i] >= 0) {
-                x[2 * i] = __ldg(kp + slot[i] * row_vec + j);
-                x[2 * i + 1] = __ldg(vp + slot[i] * row_vec + j);
-                if (q8) {
-                    const int64_t h = j * 16 / a.d + (a.scale_per_block ? blk[i] * a.hkv : 0);
-                    sc[2 * i] = __ldg(a.k_scale + h);
-                    sc[2 * i + 1] = __ldg(a.v_scale + h);
-                }
+            const int64_t at = max(slot[i], (int64_t)0) * row_vec + j;
+            x[2 * i] = __ldg(kp + at);
+            x[2 * i + 1] = __ldg(vp + at);
+            if (q8) {
+                sc[2 * i] = __ldg(a.k_scale + scale[i] + h);
+                sc[2 * i + 1] = __ldg(a.v_scale + scale[i] + h);
             }
         }
 #pragma unroll
         for (int i = 0; i < kTokens; ++i) {
             if (slot[i] == -2) continue;
-            emit<PAGE>(a.k_out, (t0 + i) * row_vec + j, x[2 * i], sc[2 * i]);
-            emit<PAGE>(a.v_out, (t0 + i) * row_vec + j, x[2 * i + 1], sc[2 * i + 1]);
+            uint4 k = widen<PAGE>(x[2 * i], sc[2 * i]), v = widen<PAGE>(x[2 * i + 1], sc[2 * i + 1]);
+            if (slot[i] == -1) k = v = make_uint4(nan2, nan2, nan2, nan2);
+            ko[i * row_vec + j] = k;
+            vo[i * row_vec + j] = v;
         }
     }
 }

@@ -235,9 +235,9 @@ def _check_weight(pool, name, w):
         return None
     if w.dim() != 1 or w.shape[0] != pool.head_dim or not w.is_contiguous():
         raise ValueError("%s must be a contiguous [%d]" % (name, pool.head_dim))
-    if w.dtype not in (torch.float32, torch.bfloat16):
+    if w.dtype is not torch.float32 and w.dtype is not torch.bfloat16:
         raise TypeError("%s must be float32 or bfloat16" % name)
-    if w.device != pool.device:
+    if w.get_device() != pool.device.index:
         raise ValueError("%s must be on the pool's device" % name)
     return w.data_ptr()
 
@@ -257,15 +257,15 @@ def paged_qk_norm_rope_write(pool, q, k, v, cu_seqlens, block_table, seq_lens, q
     ks = _check_rows(pool, "k", k, pool.num_kv_heads, total)
     vs = _check_rows(pool, "v", v, pool.num_kv_heads, total)
     qw, kw = _check_weight(pool, "q_weight", q_weight), _check_weight(pool, "k_weight", k_weight)
-    if qw and kw and q_weight.dtype != k_weight.dtype:
+    if qw and kw and q_weight.dtype is not k_weight.dtype:
         raise TypeError("q_weight and k_weight must share one dtype")
     given = q_weight if q_weight is not None else k_weight
     w_code = _lib.PGD_F32 if given is not None and given.dtype == torch.float32 else _lib.PGD_BF16
     r_ptr, r_len, r_dim = None, 0, 0
     if rope is not None:
-        if rope.dim() != 3 or rope.shape[1] != 2 or rope.dtype != torch.float32:
+        if rope.dim() != 3 or rope.shape[1] != 2 or rope.dtype is not torch.float32:
             raise ValueError("rope must be float32 [positions, 2, rope_dim / 2]")
-        if not rope.is_contiguous() or rope.device != pool.device:
+        if not rope.is_contiguous() or rope.get_device() != pool.device.index:
             raise ValueError("rope must be contiguous and on the pool's device")
         r_ptr, r_len, r_dim = rope.data_ptr(), rope.shape[0], 2 * rope.shape[2]
     if q_out is None:
