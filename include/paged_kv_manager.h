@@ -178,7 +178,7 @@ int paged_kv_read(pgd_pool_t pool, void *k_out, void *v_out, int total,
  *             with interleaved = 1, become (a cos - b sin, b cos + a sin).  rope_dim: a
  *             multiple of 16, at most D.  rope null: no rotation
  *   q, q_out  [total, Hq, D] rows; q_out may be q itself, or other columns of one packed
- *             row, but may not overlap q in any other way
+ *             row, but may not overlap q, k or v in any other way (PGD_ERR_ARG)
  * Everything is computed in float32 and rounded once: to q_out's type, or to the pages'
  * (8-bit codes and block scales come from the float32 values, by the rules of
  * paged_kv_write).  Values are stored as paged_kv_write stores them.

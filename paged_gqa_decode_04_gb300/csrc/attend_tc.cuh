@@ -130,7 +130,7 @@ __device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int first, 
     }
     if (p.hi > p.lo) {
         p.t0 = p.lo / kTile;
-        p.t1 = (p.hi + kTile - 1) / kTile;
+        p.t1 = (p.hi - 1) / kTile + 1;
     } else {
         p.lo = p.hi = 0;
     }
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // tokens and tiles of the CTA
     const int lo = some0 ? (some1 ? min(sp[0].lo, sp[1].lo) : sp[0].lo) : sp[1].lo;
     const int hi = max(sp[0].hi, sp[1].hi);
-    int T0 = lo / kTile, T1 = hi > lo ? (hi + kTile - 1) / kTile : T0;
+    int T0 = lo / kTile, T1 = hi > lo ? (hi - 1) / kTile + 1 : T0;
     // 128 rows or fewer: both blocks take them, and every other tile each, where every CTA of
     // the cluster has two (all of them decide alike)
     const bool paired = rows <= kBlock && T1 - T0 >= 2 * a.cluster;
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = first; j < p.t1; j += by, phase ^= 1) {
                 if (!warp_wait(bar_s + 8 * blk, phase, gave_up)) break;
                 fence_after();
-                if (j * kTile < p.lo_all || (j + 1) * kTile > p.hi_all)
+                if (j * kTile < p.lo_all || p.hi_all - j * kTile < kTile)
                     tile(j, std::true_type());
                 else
                     tile(j, std::false_type());
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (PB && side == 1)
                         by[i] = __float2half2_rn(scales[kTile / 8 + (warp - 8) * 4 + i] *
                                                  scales[2 * kTile / 8]);
-                const bool edge = side == 1 && (j * kTile < lo || (j + 1) * kTile > hi);
+                const bool edge = side == 1 && (j * kTile < lo || hi - j * kTile < kTile);
                 uint4 x[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const unsigned which = __ballot_sync(0xffffffffu, ok);
             const uint32_t bytes = __popc(which) * box * 128;
             // rows no query sees, or that have no page, among this warp's copies
-            const bool patch = j * kTile < lo || (j + 1) * kTile > hi ||
+            const bool patch = j * kTile < lo || hi - j * kTile < kTile ||
                                __any_sync(0xffffffffu, mine && !ok);
             const int row = (j * kTile + my_page * box) % bs;
 #pragma unroll

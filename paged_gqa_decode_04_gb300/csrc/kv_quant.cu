@@ -743,17 +743,22 @@ int check_kv(const Pool& p, const void* k, int64_t k_stride, const void* v, int6
     return PGD_OK;
 }
 
-// Whether q_out may be written while q is read: the same rows, or rows that never meet.
-bool q_out_fits(const char* q, int64_t q_stride, const char* o, int64_t o_stride, int64_t width,
-                int64_t total) {
-    if (q == o) return q_stride == o_stride || total == 1;
-    const char* q_end = q + (total - 1) * q_stride + width;
-    const char* o_end = o + (total - 1) * o_stride + width;
-    if (q_end <= o || o_end <= q) return true;
-    if (q_stride != o_stride) return false;
-    int64_t off = (o - q) % q_stride;  // columns of one packed row
-    if (off < 0) off += q_stride;
-    return off >= width && off + width <= q_stride;
+// Rows of `width` bytes, `stride` apart, from `p` on.
+struct Span {
+    const char* p;
+    int64_t stride, width;
+};
+
+// Whether no row of one meets a row of the other: apart altogether, or columns of the
+// rows of one packed tensor.
+bool apart(const Span& x, const Span& y, int64_t total) {
+    if (x.p + (total - 1) * x.stride + x.width <= y.p ||
+        y.p + (total - 1) * y.stride + y.width <= x.p)
+        return true;
+    if (x.stride != y.stride) return false;
+    int64_t off = (y.p - x.p) % x.stride;
+    if (off < 0) off += x.stride;
+    return off >= x.width && off + y.width <= x.stride;
 }
 
 }  // namespace
@@ -800,8 +805,12 @@ extern "C" int paged_qk_norm_rope_write(
     rc = check_rows(q, q_stride, width, elt);
     if (rc == PGD_OK) rc = check_rows(q_out, q_out_stride, width, elt);
     if (rc != PGD_OK) return rc;
-    if (!q_out_fits(static_cast<const char*>(q), q_stride * elt, static_cast<char*>(q_out),
-                    q_out_stride * elt, width * elt, total))
+    const Span in = {static_cast<const char*>(q), q_stride * elt, width * elt};
+    const Span out = {static_cast<const char*>(q_out), q_out_stride * elt, width * elt};
+    const Span ks = {static_cast<const char*>(k), k_stride * elt, (int64_t)p.hkv * p.d * elt};
+    const Span vs = {static_cast<const char*>(v), v_stride * elt, ks.width};
+    const bool in_place = in.p == out.p && (in.stride == out.stride || total == 1);
+    if ((!in_place && !apart(in, out, total)) || !apart(ks, out, total) || !apart(vs, out, total))
         return PGD_ERR_ARG;
     const int w_align = weight_dtype == PGD_F32 ? 4 : 2;
     if (!is_aligned(q_weight, w_align) || !is_aligned(k_weight, w_align)) return PGD_ERR_ALIGN;

@@ -36,7 +36,8 @@ inline int act_bytes(const Pool& p) { return p.dtype == PGD_F32 ? 4 : 2; }
 inline int check_ragged(const Pool& p, int total, const int32_t* cu, int B, const int32_t* table,
                         int max_blocks, const int32_t* lens) {
     if (total < 0 || B < 0 || max_blocks < 0) return PGD_ERR_ARG;
-    if ((int64_t)max_blocks * p.block_size > INT32_MAX) return PGD_ERR_SHAPE;
+    // token positions plus a tile stay within 31 bits
+    if ((int64_t)max_blocks * p.block_size > INT32_MAX - 1024) return PGD_ERR_SHAPE;
     if (B == 0 || total == 0) return PGD_OK;
     if (!cu || !table || !lens) return PGD_ERR_ARG;
     if (max_blocks < 1) return PGD_ERR_SHAPE;

@@ -168,6 +168,43 @@ def test_norm_rope_write(pages, scales, d, norm, rope_dim, interleaved):
     check_stored(b, "v", want, {r: y.abs() for r, y in want.items()}, b.dv, b.dvs, 0.0)
 
 
+@pytest.mark.parametrize("bs", [8, 32, 256])
+@pytest.mark.parametrize("pages,hkv", [("e4m3", 9), ("int8", 1)])
+def test_norm_rope_write_blocks(pages, hkv, bs):
+    """Block scales with other block sizes, more KV heads than a group of eight, and rows that
+    begin inside blocks; a weight that is not 16-byte aligned."""
+    b = Batch(LENS, NEW, hkv=hkv, bs=bs, pages=pages, scales="block", seed=bs)
+    q, k, v = b.rows(hkv), b.rows(hkv), b.rows(hkv)
+    w = (1 + 0.3 * torch.randn(129, generator=b.g)).bfloat16()
+    rope = pgd.rope_table(max(LENS), 128)
+    got = run_norm_rope(b, hkv, q, k, v, q_weight=w.cuda()[1:], k_weight=w.cuda()[:128],
+                        eps=1e-6, rope=rope.cuda())
+    want, size = {}, {}
+    for s in range(len(LENS)):
+        for row, pos in ref.rows_of(b.cu, b.lens, s):
+            y, m = ref.norm_rotate(q[row], w[1:], 1e-6, rope, False, pos)
+            assert torch.all((got[row].double() - y).abs() <= 2.0 ** -8 * y.abs() + F32 * m)
+            want[row], size[row] = ref.norm_rotate(k[row], w[:128], 1e-6, rope, False, pos)
+    check_stored(b, "k", want, size, b.dk, b.dks, F32)
+    want = {r: v[r].double() for r in want}
+    check_stored(b, "v", want, {r: y.abs() for r, y in want.items()}, b.dv, b.dvs, 0.0)
+
+
+def test_rotation_table_too_short():
+    """A sequence longer than the table is reported and left out."""
+    b = Batch([20, 50, 30], [20, 10, 30], hkv=2, seed=7)
+    q, k = b.rows(4), b.rows(2)
+    with b_pool(b) as pool:
+        before = bits(b.dk).clone()
+        out = pgd.paged_qk_norm_rope_write(pool, b.to(q), b.to(k), b.to(k), *b.where(),
+                                           rope=pgd.rope_table(49, 128).cuda())
+        assert pgd.paged_gqa_get_error(pool) == _lib.PGD_ERR_SEQ_LEN
+    assert torch.all(out[20:30].isnan()) and not out[:20].isnan().any()
+    for t in range(50):
+        blk, slot = ref.place(b.table, 16, 1, t)
+        assert torch.equal(bits(b.dk)[blk, slot], before[blk, slot])
+
+
 def test_norm_rope_in_place_and_packed():
     """q_out = q, and q_out as other columns of the packed rows q comes from."""
     b = Batch(LENS, NEW, hkv=2, seed=5)
@@ -235,6 +272,31 @@ def test_attend_long(causal):
     """Several key tiles and several query tiles a head."""
     b = Batch([1000, 517, 2], [700, 517, 1], hkv=1, bs=32, seed=9)
     check_attend(b, 4, causal, 0)
+
+
+@pytest.mark.parametrize("pages", ["e4m3", "int8"])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 300)])
+def test_attend_block_scales_that_vary(pages, causal, window):
+    """Scales of K over a factor of 30, of V from 0 over five orders of magnitude, rising and
+    falling along the sequence, in many key tiles."""
+    b = Batch([1100, 700], [150, 700], hkv=2, pages=pages, scales="block", seed=3)
+    for s in range(2):
+        n = -(-b.lens[s] // 16)
+        i = torch.arange(n, dtype=torch.float32)
+        blk = b.table[s][:n].long()
+        up = 10.0 ** (5 * i / n - 5) if s == 0 else 10.0 ** (-5 * i / n)
+        b.v_scale[blk] *= up[:, None] * 100
+        b.k_scale[blk] *= (0.2 + 6 * torch.rand(n, 1, generator=b.g)) / 6
+        b.v_scale[blk[0]], b.k_scale[blk[3]] = 0.0, 0.0
+    check_attend(b, 4, causal, window)
+
+
+@pytest.mark.parametrize("pages,scales", [("bf16", "head"), ("e4m3", "head"), ("int8", "block")])
+def test_attend_few_rows_of_long_sequences(pages, scales):
+    """Sequences shared by the CTAs of a cluster: a few tokens over many key tiles."""
+    b = Batch([2500, 1, 40, 1290], [3, 1, 2, 1], hkv=1, pages=pages, scales=scales, seed=5)
+    for causal in (True, False):
+        check_attend(b, 5, causal, 0)
 
 
 def test_attend_more_queries_than_cached():
@@ -443,6 +505,7 @@ def test_refusals():
                      (dict(rope=256, rl=9, rd=0), H), (dict(rope=264, rl=9, rd=128), AL),
                      (dict(q=None), A), (dict(o=None), A), (dict(qs=500), H), (dict(os=513), AL),
                      (dict(o=(1 << 20) + 16), A), (dict(o=1 << 20, os=520), A),
+                     (dict(o=256), A), (dict(v=1 << 21), A),
                      (dict(qw=257), AL), (dict(kw=258, wd=0), AL)):
         assert nr(**kw) == want, kw
     abase = dict(q=1 << 20, qs=512, total=4, hq=4, B=1, causal=1, window=0, scale=1.0, o=1 << 21)
