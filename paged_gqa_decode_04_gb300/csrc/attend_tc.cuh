@@ -63,9 +63,6 @@ constexpr int kTile = 128;      // tokens of a key tile
 constexpr int kBlock = 128;     // rows of a block
 constexpr int kRowShift = 8;    // log2 of the rows of a CTA
 constexpr int kThreads = 512;
-// Registers a thread: launched with 128, then the 256 threads of the softmax take 200, the
-// 128 producers keep 64 and the last 128 keep 48, which is the launch's 65536 again.
-constexpr int kSoftmaxRegs = 200, kProducerRegs = 64, kIssuerRegs = 48;
 constexpr float kGrow = 8.f;    // base-2 growth of a maximum that is let pass
 
 struct Args {
@@ -89,21 +86,30 @@ struct Layout {
     static constexpr bool kQ8 = PAGE != PGD_BF16;
     static constexpr int kHalves = D / 64;                 // 128-byte columns of a 16-bit tile
     static constexpr int kSlot = kTile * D * 2;            // bytes of a K or V tile
+    // Registers a thread: launched with 128, then the 256 threads of the softmax, the 128
+    // producers and the last 128 share the launch's 65536 anew.  With scales per block the
+    // widening warps need more (482 against 497 us at 1500 of 16384 tokens, 32/8 heads), else
+    // the softmax does.
+    static constexpr int kSoftmaxRegs = PB ? 192 : 200;
+    static constexpr int kProducerRegs = PB ? 80 : 64;
+    static constexpr int kIssuerRegs = 48;
+    static_assert(256 * kSoftmaxRegs + 128 * (kProducerRegs + kIssuerRegs) == kThreads * 128,
+                  "registers of the launch");
+    // Stored tiles wait for their scales as well, so more of them pay where there are any
+    // (482 against 498 us at the same size).
     static constexpr int kSlots = kQ8 ? PB ? 3 : 4 : D == 128 ? 5 : 8;
     static constexpr int kQ = kBlock * D * 2;              // bytes of a block of queries
     static constexpr int kRing = 2 * kQ;
     // 8-bit pages: tiles as they are stored, and the scales of the tiles in flight (a tile is
-    // at most 1 + kRawSlots / 2 + kSlots / 2 ahead of the softmax).  A widened tile's room
-    // holds two more raw ones: with the longer widening of scaled values that is worth it
-    // (490 us, 523 with two, for 2048 tokens behind 8192 at 64 / 8 heads), without it is not
-    // (423 us, 405 with two).
+    // at most 1 + (kRawSlots + kSlots) / 2 ahead of the softmax): for each 8 tokens K's,
+    // log2 of V's and 1 over V's, then V's gain.
     static constexpr int kRawSlot = kTile * 128;
     static constexpr int kRawSlots = PB ? 4 : 2;
     static constexpr int kRaw = kRing + kSlots * kSlot;
-    static constexpr int kScaleTiles = 8;
+    static constexpr int kScaleTiles = 6;
     static constexpr int kScales = kRaw + (kQ8 ? kRawSlots * kRawSlot : 0);
-    static constexpr int kScaleBytes = 144;                // 16 of K, 16 of V, V's gain
-    static constexpr int kBars = kScales + (kQ8 ? kScaleTiles * kScaleBytes : 0);
+    static constexpr int kScaleBytes = 272;
+    static constexpr int kBars = kScales + (PB ? kScaleTiles * kScaleBytes : 0);
     static constexpr int kBytes = kBars + 288 + 1024;      // and room to align to 1024
     // warps that issue copies, and the tiles' 128-byte columns they fetch one by one
     static constexpr int kProducers = kQ8 ? 2 : 4;
@@ -322,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 8) {
         // ---------------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftmaxRegs));
         const Span p = blk ? sp[1] : sp[0];
         if (p.t1 > p.t0) {
             // the block's queries into shared memory, swizzled
@@ -389,15 +395,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t x[kTile], w[kTile / 4];
                 uint64_t sum[2];
                 float top[8];
-                // K's scales of each 8 tokens (times the logit multiplier) go on the scores, V's
-                // are in the widened tile, times a gain: the accumulator follows it
-                float ks[PB ? kTile / 8 : 1];
+                // Scales of each 8 tokens: K's (times the logit multiplier) go on the scores, V's,
+                // times a gain that the accumulator follows, on the weights: as a term of the
+                // exponent, divided out again for the sum of the weights alone
+                const float4* const sc = reinterpret_cast<const float4*>(
+                    smem + L::kScales + (PB ? (j - T0) % L::kScaleTiles * L::kScaleBytes : 0));
                 if (PB) {
-                    const float* const sc = reinterpret_cast<const float*>(
-                        smem + L::kScales + (j - T0) % L::kScaleTiles * L::kScaleBytes);
-#pragma unroll
-                    for (int i = 0; i < kTile / 8; ++i) ks[i] = sc[i];
-                    const float gain = sc[2 * kTile / 8];
+                    const float gain = sc[kTile / 8].x;
                     if (gain != vgain) {
                         if (j > first) rescale(gain / vgain);
                         vgain = gain;
@@ -408,16 +412,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // all 128 scores: the exponentials set the pace, the rest is issued in between
                 auto weigh = [&](int h) {
                     const float off = m == -INFINITY ? 0.f : -m;
-                    const uint64_t mm = pair(off, off);
 #pragma unroll
                     for (int g = 0; g <= 8; ++g) {
                         const int at = h * (kTile / 2) + g * 8;
-                        const float mul = PB && g < 8 ? ks[h * 8 + g] : scale;
-                        const uint64_t cc = pair(mul, mul);
+                        const float mul = PB && g < 8 ? sc[h * 8 + g].x : scale;
+                        const float add = PB && g < 8 ? off + sc[h * 8 + g].y : off;
+                        const uint64_t cc = pair(mul, mul), mm = pair(add, add);
                         if (g < 8) {
                             if (h == 0 && PB) {
-                                float u = max8(x + g * 8) * ks[g];
-                                float v = max8(x + kTile / 2 + g * 8) * ks[8 + g];
+                                float u = max8(x + g * 8) * sc[g].x;
+                                float v = max8(x + kTile / 2 + g * 8) * sc[8 + g].x;
                                 top[0] = g == 0 ? fmaxf(u, v) : max3(top[0], u, v);
                             } else if (h == 0) {
 #pragma unroll
@@ -439,12 +443,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                         if (g > 0) {
+                            uint64_t part = 0;  // of these 8 weights, with V's scale
 #pragma unroll
                             for (int i = -8; i < 0; i += 2) {
                                 const float e0 = __uint_as_float(x[at + i]);
                                 const float e1 = __uint_as_float(x[at + i + 1]);
-                                sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(e0, e1));
+                                if (PB)
+                                    part = i == -8 ? pair(e0, e1) : add2(part, pair(e0, e1));
+                                else
+                                    sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(e0, e1));
                                 w[g * 4 + i / 2] = operand2<PAGE>(e0, e1);
+                            }
+                            if (PB) {
+                                const float over = sc[h * 8 + g - 1].z;
+                                sum[g & 1] = fma2(part, pair(over, over), sum[g & 1]);
                             }
                         }
                     }
@@ -510,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (kQ8 && warp < 12) {
         // ---------------------------------------------------------- widening (8-bit pages)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kProducerRegs));
         // A warp reads 64 of the 128 codes of 8 rows at a time and stores them as f16.  Its
         // lanes take rows r and r ^ 5 in pairs, so that neither the reads (in 16-byte pieces
         // swizzled by r) nor the writes (every other piece, swizzled alike) share a bank.
@@ -525,16 +537,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!live) break;
                 const uint8_t* const src = smem + L::kRaw + raw * L::kRawSlot;
                 uint8_t* const dst = smem + L::kRing + slot * L::kSlot;
-                const float* const scales = reinterpret_cast<const float*>(
-                    smem + L::kScales + (j - T0) % L::kScaleTiles * L::kScaleBytes);
-                __half2 by[4];  // V's scale in f16, product in f16: 2^-11 of the value together,
-                                // little beside the output's own 2^-8; K's is kept out, where
-                                // it would move the scores
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (PB && side == 1)
-                        by[i] = __float2half2_rn(scales[kTile / 8 + (warp - 8) * 4 + i] *
-                                                 scales[2 * kTile / 8]);
                 const bool edge = side == 1 && (j * kTile < lo || hi - j * kTile < kTile);
                 uint4 x[8];
 #pragma unroll
@@ -551,13 +553,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     widen4<PAGE>(x[i].y, y[2], y[3]);
                     widen4<PAGE>(x[i].z, y[4], y[5]);
                     widen4<PAGE>(x[i].w, y[6], y[7]);
-                    if (PB && side == 1) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const __half2 v = __hmul2(*reinterpret_cast<__half2*>(y + e), by[i / 2]);
-                            y[e] = *reinterpret_cast<const uint32_t*>(&v);
-                        }
-                    }
                     const int t = j * kTile + r;
                     if (edge && (t < lo || t >= hi)) {  // V rows no query sees
 #pragma unroll
@@ -578,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (!kQ8 && warp < 12) {
         // -------------------------------------------------------------- producers
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kProducerRegs));
         // Copy k of a tile (page k / kHalves, column k % kHalves) is issued by warp k % 4,
         // lane k / 4: the lanes of one warp take turns, 54 cycles each.
         const int bs = a.r.block_size, me = warp - 8;
@@ -658,14 +653,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bar_wait(bar_full + 8 * (i % L::kSlots), i / L::kSlots & 1, &never);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssuerRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kIssuerRegs));
     }
     if (kQ8 && warp >= 14) {
         // -------------------------------------------------------- producers (8-bit pages)
         // One copy a page, issued by warp 14 + page % 2, lane page / 2.  Warp 14 also brings the
         // scales, lane by page, one tile ahead, and V's gain: a power of two that puts the
-        // first tile's largest V scale in [1, 2) and falls when one grows past 16 times that,
-        // so that scale times code stays within f16.
+        // first tile's largest V scale in [8, 16) and falls when one grows past 128: a weight,
+        // up to 2^kGrow, times its scale stays within f16 and keeps its 11 bits down to
+        // 2^-17 of the largest.
         const int bs = a.r.block_size, me = warp - 14;
         const int box = min(bs, kTile), pages = kTile / box;
         const int page = lane * L::kProducers + me;
@@ -713,22 +709,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!live) break;
                 if (scaling && side == 0) {
                     // the tile kScaleTiles back is done with: its slot in the ring was reused
-                    float* const to = reinterpret_cast<float*>(
+                    float4* const to = reinterpret_cast<float4*>(
                         smem + L::kScales + (j - T0) % L::kScaleTiles * L::kScaleBytes);
                     float most = vs;
 #pragma unroll
                     for (int m = 1; m < 32; m *= 2)
                         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
-                    if (most * gain > 16.f || gain == 0.f) {
-                        const int e = min(max((__float_as_int(most) >> 23) & 255, 2), 252);
-                        gain = __int_as_float((254 - e) << 23);
+                    if (most * gain > 128.f || gain == 0.f) {
+                        const int e = min(max((__float_as_int(most) >> 23) & 255, 5), 252);
+                        gain = __int_as_float((257 - e) << 23);
                     }
+                    // a scale of 0 stays above 0: masked scores times K's are still -infinity,
+                    // and weights times V's (0 in f16) can be summed without it
+                    const float by = vs * gain < 1e-20f ? 1e-20f : vs * gain;
+                    const float4 e = make_float4(ks < 1e-30f ? 1e-30f : ks * a.scale_log2,
+                                                 log2f(by), 1.f / by, 0.f);
                     if (lane < pages)
-                        for (int g = lane * box / 8; g < (lane + 1) * box / 8; ++g) {
-                            to[g] = ks < 1e-30f ? 1e-30f : ks * a.scale_log2;
-                            to[kTile / 8 + g] = vs;
-                        }
-                    if (lane == 0) to[2 * kTile / 8] = gain;
+                        for (int g = lane * box / 8; g < (lane + 1) * box / 8; ++g) to[g] = e;
+                    if (lane == 0) to[kTile / 8].x = gain;
                 }
                 __syncwarp();
                 if (lane == 0) {
