@@ -41,6 +41,24 @@
 // join their sums through shared memory, each other's in a cluster:
 // out = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k.
 //
+// 8-bit pages.  Warps 14 and 15 fetch the codes, warps 8-11 widen them to f16, exactly, into
+// the tiles the products read; queries and weights are f16 as well.  Scales per head are
+// constants of the CTA.  Scales per block go where a float32 value is at hand anyway, K's on
+// the scores and V's into the exponent of the weights (the row's sum takes them out again):
+// multiplied into V while it is widened they cost 8% of the whole (2048 of 8192 tokens, 64/8
+// heads: 489 against 465 us; 407 with scales per head, 337 over bfloat16).
+//
+// What bounds it.  At D = 128 a tile of one block is 2 x 8 products of 64 cycles (1024), and
+// each of its four softmax warps, one in every quarter of the SM, has 128 exponentials of
+// 4.07 cycles (521), about 900 cycles with the maxima, sums and conversions; the two blocks'
+// warps of a quarter together take 1500.  So the softmax hides behind the products of both
+// blocks (2048 cycles) with little to spare.  Measured (bfloat16, 64/8 heads, 2048 queries): of 32768
+// tokens 1404 us, 1.52 PFLOP/s, 79% of a library product's burst (1294 us and 86% before the
+// clock drops under the load); of 8192 tokens 337 us with the tensor cores busy 60% of the
+// time, since a CTA's query load, first tiles and epilogue (some 15 us) are not hidden and
+// causal pieces end unevenly.  Over 8-bit pages the widening warps share the issue slots
+// with the softmax: 42% (scales per block).
+//
 // Every wait is bounded; one that gives up latches PGD_ERR_TIMEOUT and ends the CTA.
 #pragma once
 
@@ -88,15 +106,15 @@ struct Layout {
     static constexpr int kSlot = kTile * D * 2;            // bytes of a K or V tile
     // Registers a thread: launched with 128, then the 256 threads of the softmax, the 128
     // producers and the last 128 share the launch's 65536 anew.  With scales per block the
-    // widening warps need more (482 against 497 us at 1500 of 16384 tokens, 32/8 heads), else
-    // the softmax does.
+    // widening warps need more (482 against 497 us: two chunks of 1400 tokens, 10k cached
+    // each, 32/8 heads), else the softmax does.
     static constexpr int kSoftmaxRegs = PB ? 192 : 200;
     static constexpr int kProducerRegs = PB ? 80 : 64;
     static constexpr int kIssuerRegs = 48;
     static_assert(256 * kSoftmaxRegs + 128 * (kProducerRegs + kIssuerRegs) == kThreads * 128,
                   "registers of the launch");
     // Stored tiles wait for their scales as well, so more of them pay where there are any
-    // (482 against 498 us at the same size).
+    // (482 against 498 us there).
     static constexpr int kSlots = kQ8 ? PB ? 3 : 4 : D == 128 ? 5 : 8;
     static constexpr int kQ = kBlock * D * 2;              // bytes of a block of queries
     static constexpr int kRing = 2 * kQ;

@@ -25,6 +25,11 @@
 // than 16 tokens are shared by up to 8 warps of a CTA, which exchange their maxima through
 // shared memory.  No two warps write one scale and there are no atomics, so the pages do
 // not depend on timing.
+//
+// Measured, 8 KV heads of 128 (share of the time a plain copy of the bytes takes): 67k tokens
+// into e4m3 pages with a scale per block 71.6 us (86%); norm, rotation and write of 67k tokens
+// with 32 query heads into bfloat16 pages 287 us (88%), of 17k tokens with 64 query heads into
+// e4m3 pages with a scale per block 142 us (69%: instructions, issued in 65% of the cycles).
 #include <cuda_fp8.h>
 
 #include "page_ops.h"
