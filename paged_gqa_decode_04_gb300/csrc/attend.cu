@@ -16,42 +16,69 @@
 namespace pgd {
 namespace {
 
-// CTAs that share the keys of a piece of rows (a cluster).  One CTA fits on an SM, so
-// `units` pieces take ceil(units c / SMs) rounds of 1 / c of the work each; c is raised
-// while that saves a tenth or more.  Joining the sums costs a CTA some 5 us, so each keeps
-// tiles of the longest sequence that the table can hold for it: 2 where SMs are idle
-// without it, 64 (about 100 us) where they only end unevenly.
-int choose_cluster(const Pool& p, int64_t units, int64_t max_tokens) {
-    auto rounds = [&](int c) { return double((units * c + p.num_sms - 1) / p.num_sms) / c; };
-    int best = 1;
-    for (int c = 2; c <= 8; c *= 2) {
-        const int keep = units * c <= p.num_sms ? 2 : 64;
-        if (max_tokens >= (int64_t)c * keep * attend::kTile && rounds(c) <= 0.9 * rounds(best))
-            best = c;
+// CTAs that share the keys of a piece of rows (a cluster of c).  With `units` pieces and `fit[c]`
+// clusters on the GPU at once there are ceil(units / fit[c]) rounds, each of tiles / c key tiles
+// of `tile` us and a CTA's start and end, 10 us and for a join 1 us a doubling and, with more
+// than 128 rows, 6 more.  The smallest sum is taken; tiles are those of the longest sequence that
+// the table can hold.  Measured over c = 1, 2, 4, 8 (us; the choice is marked):
+//     2 sequences, 2048 cached, 4 queries each     33   22   19*  32
+//     8 sequences, up to 4096, 2-8 queries each    48   33*  44   75
+//     one prompt of 512, 32/8 heads                21*  28   47  102
+//     2048 queries of 32768, 64/8 heads          1349 1260* 1455
+//     2048 queries of 8192, 64/8 heads            336* 379  522
+int choose_cluster(const int (&fit)[4], int64_t units, int64_t max_tokens, bool few, double tile) {
+    const double tiles = double((max_tokens + attend::kTile - 1) / attend::kTile);
+    int best = 0;
+    double least = 0;
+    for (int i = 0; i < 4; ++i) {
+        if (fit[i] < 1 || (i && tiles < (1 << i))) break;
+        const double us = double((units + fit[i] - 1) / fit[i]) *
+                          (tiles / (1 << i) * tile + 10 + (i ? i + (few ? 0 : 6) : 0));
+        if (i == 0 || us < least) best = i, least = us;
     }
-    return best;
+    return 1 << best;
 }
 
 template <int D, int PAGE, bool PB>
-cudaError_t launch(const attend::Args& a, const Pool& p, const PageMaps& maps, cudaStream_t s) {
+cudaError_t launch(attend::Args& a, const Pool& p, const PageMaps& maps, cudaStream_t s) {
     using namespace attend;
-    static std::atomic<uint64_t> ready{0};  // devices whose function attributes are set
-    if (!(ready.load() >> p.device & 1)) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            attend_kernel<D, PAGE, PB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D, PAGE, PB>::kBytes);
-        if (e != cudaSuccess) return e;
-        ready.fetch_or(uint64_t(1) << p.device);
-    }
+    constexpr int kDevices = 64;
+    static std::atomic<uint64_t> fits[kDevices];  // 16 bits a cluster size, 0: not asked yet
+    if (p.device < 0 || p.device >= kDevices) return cudaErrorInvalidDevice;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = a.cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(unsigned(a.pieces) * a.hkv * a.cluster);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Layout<D, PAGE, PB>::kBytes;
     cfg.stream = s;
     cfg.attrs = attr;
+    uint64_t known = fits[p.device].load();
+    if (!known) {
+        cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, PAGE, PB>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Layout<D, PAGE, PB>::kBytes);
+        if (e != cudaSuccess) return e;
+        known = p.num_sms;
+        for (int i = 1; i < 4; ++i) {
+            int n = 0;
+            attr[0].val.clusterDim.x = 1 << i;
+            cfg.gridDim = dim3(1 << i);
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, attend_kernel<D, PAGE, PB>, &cfg);
+            if (e != cudaSuccess) return e;
+            known |= uint64_t(n) << (16 * i);
+        }
+        fits[p.device].store(known);
+    }
+    int fit[4];
+    for (int i = 0; i < 4; ++i) fit[i] = int(known >> (16 * i) & 0xffff);
+    const bool few = (int64_t)a.r.total * a.group <= (int64_t)a.pieces * kBlock;
+    // us of a key tile of 256 rows (measured at D = 128)
+    const double tile = PAGE == PGD_BF16 ? 1.2 : PB ? 1.75 : 1.5;
+    a.cluster = choose_cluster(fit, (int64_t)a.pieces * a.hkv, a.r.max_len, few, tile);
+    attr[0].val.clusterDim.x = a.cluster;
+    cfg.gridDim = dim3(unsigned(a.pieces) * a.hkv * a.cluster);
     cfg.numAttrs = a.cluster > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, attend_kernel<D, PAGE, PB>, a, maps.k, maps.v);
 }
@@ -108,7 +135,6 @@ extern "C" int paged_gqa_attend(pgd_pool_t pool, const void* q, int64_t q_stride
     t.q_and = scale != 0.f ? 0xffffffffu : 0u;
     t.q_xor = scale < 0.f ? 0x80008000u : 0u;
     t.pieces = int(pieces);
-    t.cluster = choose_cluster(p, pieces * p.hkv, cap);
     t.k_scale = p.k_scale;
     t.v_scale = p.v_scale;
     const PageMaps& maps = page_maps(pool);

@@ -921,13 +921,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // unnormalised rows, maxima and sums to shared memory, then every CTA of the
         // cluster joins a share of the rows
-        float* const stat = reinterpret_cast<float*>(smem);  // [256][2], and a flag
+        float2* const stat = reinterpret_cast<float2*>(smem);  // of the 256 rows
         if (warp < 8) {
             const uint32_t to = tmem + (uint32_t(warp % 4 * 32) << 16) + 2 * kTile + blk * D;
             const bool have = blk ? sp[1].t1 > sp[1].t0 : sp[0].t1 > sp[0].t0;
             const int r = blk * kBlock + my_row;
-            stat[2 * r] = m;
-            stat[2 * r + 1] = l;
+            stat[r] = make_float2(m, failed ? NAN : l);
             if (have && at_row - lane < rows) {
 #pragma unroll
                 for (int i = 0; i < D; i += 32) {
@@ -948,52 +947,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (threadIdx.x == 0) reinterpret_cast<int*>(stat)[512] = failed;
         cluster_sync();
         if (warp < 8) {
             // part k of a row: CTA k of the cluster, or with paired blocks block k % 2 of CTA k / 2
             const int parts = paired ? 2 * a.cluster : a.cluster;
             auto cta_of = [&](int k) { return paired ? k / 2 : k; };
             auto row_of = [&](int r, int k) { return paired ? r + k % 2 * kBlock : r; };
-            constexpr int kQuads = D / 4;   // four columns a thread
-            constexpr int kAtOnce = 4;      // parts whose sums are on their way together
-            for (int i = threadIdx.x + share * 256; i < rows * kQuads; i += a.cluster * 256) {
-                const int r = i / kQuads, c = i % kQuads;
-                float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f, top = -INFINITY;
-                int any_failed = 0;
-                for (int k0 = 0; k0 < parts; k0 += kAtOnce) {
-                    float2 st[kAtOnce], flag[kAtOnce];
-                    float4 v[kAtOnce];
+            // four columns a thread, kLines rows of a warp at once
+            constexpr int kQuads = D / 4, kLines = 32 / kQuads;
+            const int step = a.cluster * 8 * kLines;
+            const int c = lane % kQuads, line = lane / kQuads;
+            const int from = (share * 8 + warp) * kLines;
+            Rows at(row0 + from + line, group, step);
+            // kR rows with kP parts each are on their way together: four loads, and none for a
+            // part that is not there (two parts loaded as four: 481 against 462 us for two
+            // chunks of 1400 tokens, 10k cached each; four rows of two spill, 513)
+            auto join = [&](auto some_rows, auto some_parts) {
+                constexpr int kR = decltype(some_rows)::value, kP = decltype(some_parts)::value;
+                for (int r0 = from; r0 < rows; r0 += kR * step) {
+                    float o[kR][4], sum[kR], top[kR];
 #pragma unroll
-                    for (int k = 0; k < kAtOnce; ++k) {
-                        const int part = min(k0 + k, parts - 1), rk = row_of(r, part);
-                        st[k] = peer_ld2(peer_addr(base + rk * 8, cta_of(part)));
-                        flag[k] = peer_ld2(peer_addr(base + 2048, cta_of(part)));
-                        v[k] = peer_ld4(peer_addr(
-                            base + L::kRing + rk * (D * 4) + ((c ^ rk) & (kQuads - 1)) * 16,
-                            cta_of(part)));
+                    for (int u = 0; u < kR; ++u) {
+                        o[u][0] = o[u][1] = o[u][2] = o[u][3] = sum[u] = 0.f;
+                        top[u] = -INFINITY;
+                    }
+                    for (int k0 = 0; k0 < parts; k0 += kP) {
+                        float2 st[kR][kP];
+                        float4 v[kR][kP];
+#pragma unroll
+                        for (int u = 0; u < kR; ++u)
+#pragma unroll
+                            for (int k = 0; k < kP; ++k) {
+                                const int part = min(k0 + k, parts - 1);
+                                const int r = row_of(min(r0 + u * step + line, rows - 1), part);
+                                st[u][k] = peer_ld2(peer_addr(base + r * 8, cta_of(part)));
+                                v[u][k] = peer_ld4(peer_addr(
+                                    base + L::kRing + r * (D * 4) + ((c ^ r) & (kQuads - 1)) * 16,
+                                    cta_of(part)));
+                            }
+#pragma unroll
+                        for (int u = 0; u < kR; ++u)
+#pragma unroll
+                            for (int k = 0; k < kP; ++k) {
+                                // a part without a tile of the row left nothing there
+                                const float2 x = st[u][k];
+                                if (k0 + k >= parts || x.y == 0.f) continue;
+                                const float now = fmaxf(top[u], x.x);
+                                const float keep = ex2(top[u] - now), w = ex2(x.x - now);
+                                top[u] = now;
+                                sum[u] = fmaf(w, x.y, sum[u] * keep);
+                                o[u][0] = fmaf(w, v[u][k].x, o[u][0] * keep);
+                                o[u][1] = fmaf(w, v[u][k].y, o[u][1] * keep);
+                                o[u][2] = fmaf(w, v[u][k].z, o[u][2] * keep);
+                                o[u][3] = fmaf(w, v[u][k].w, o[u][3] * keep);
+                            }
                     }
 #pragma unroll
-                    for (int k = 0; k < kAtOnce; ++k) {
-                        any_failed |= __float_as_int(flag[k].x);
-                        // a part without a tile of the row left nothing there
-                        if (k0 + k >= parts || st[k].y == 0.f) continue;
-                        const float now = fmaxf(top, st[k].x);
-                        const float keep = ex2(top - now), w = ex2(st[k].x - now);
-                        top = now;
-                        sum = fmaf(w, st[k].y, sum * keep);
-                        o[0] = fmaf(w, v[k].x, o[0] * keep);
-                        o[1] = fmaf(w, v[k].y, o[1] * keep);
-                        o[2] = fmaf(w, v[k].z, o[2] * keep);
-                        o[3] = fmaf(w, v[k].w, o[3] * keep);
+                    for (int u = 0; u < kR; ++u, at.next()) {
+                        if (r0 + u * step + line >= rows) continue;
+                        // a row that sees a token has a sum of 1 or more; NaN where a part failed
+                        const float inv = sum[u] == 0.f ? 0.f : __fdividef(1.f, sum[u]);
+                        *reinterpret_cast<uint2*>(
+                            a.out + (out_at + at.token * a.hq + at.head) * D + c * 4) =
+                            make_uint2(bf16x2(o[u][0] * inv, o[u][1] * inv),
+                                       bf16x2(o[u][2] * inv, o[u][3] * inv));
                     }
                 }
-                const float inv = any_failed ? NAN : sum == 0.f ? 0.f : 1.f / sum;
-                const uint32_t R = row0 + r;
-                *reinterpret_cast<uint2*>(
-                    a.out + (out_at + (int64_t)(R / group) * a.hq + R % group) * D + c * 4) =
-                    make_uint2(bf16x2(o[0] * inv, o[1] * inv), bf16x2(o[2] * inv, o[3] * inv));
-            }
+            };
+            using std::integral_constant;
+            if (parts > 2)
+                join(integral_constant<int, 1>(), integral_constant<int, 4>());
+            else
+                join(integral_constant<int, 2>(), integral_constant<int, 2>());
         }
         cluster_sync();  // shared memory stays until every CTA has read it
     }
