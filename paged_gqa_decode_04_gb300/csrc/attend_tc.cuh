@@ -36,8 +36,8 @@
 // an older maximum, at most 256, which costs no precision in either float type.
 //
 // Few rows.  128 rows or fewer go to both blocks, every other tile each, so that one's
-// softmax still hides behind the other's products; and where the batch has fewer pieces of
-// rows than the GPU has SMs, up to 8 CTAs of a cluster share a piece's key tiles.  The parts
+// softmax still hides behind the other's products; and where that pays, 2, 4 or 8 CTAs of a
+// cluster share a piece's key tiles (choose_cluster in attend.cu).  The parts
 // join their sums through shared memory, each other's in a cluster:
 // out = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k.
 //
@@ -45,7 +45,7 @@
 // the tiles the products read; queries and weights are f16 as well.  Scales per head are
 // constants of the CTA.  Scales per block go where a float32 value is at hand anyway, K's on
 // the scores and V's into the exponent of the weights (the row's sum takes them out again):
-// multiplied into V while it is widened they cost 8% of the whole (2048 of 8192 tokens, 64/8
+// multiplied into V while it is widened they cost 5% of the whole (2048 of 8192 tokens, 64/8
 // heads: 489 against 465 us; 407 with scales per head, 337 over bfloat16).
 //
 // What bounds it.  At D = 128 a tile of one block is 2 x 8 products of 64 cycles (1024), and
@@ -53,7 +53,7 @@
 // 4.07 cycles (521), about 900 cycles with the maxima, sums and conversions; the two blocks'
 // warps of a quarter together take 1500.  So the softmax hides behind the products of both
 // blocks (2048 cycles) with little to spare.  Measured (bfloat16, 64/8 heads, 2048 queries): of 32768
-// tokens 1404 us, 1.52 PFLOP/s, 79% of a library product's burst (1294 us and 86% before the
+// tokens 1357 us, 1.57 PFLOP/s, 81% of a library product's burst (1260 us and 88% before the
 // clock drops under the load); of 8192 tokens 337 us with the tensor cores busy 60% of the
 // time, since a CTA's query load, first tiles and epilogue (some 15 us) are not hidden and
 // causal pieces end unevenly.  Over 8-bit pages the widening warps share the issue slots
