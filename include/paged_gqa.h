@@ -326,6 +326,8 @@ int paged_gqa_workspace_size_host(pgd_pool_t pool, int B, int q_len, int Hq, int
  *                (ascending, cu_seqlens[B] <= total; none is fine).  Rows past
  *                cu_seqlens[B] are left as they were
  *   seq_lens     [B] int32, cached tokens per sequence
+ *   max_blocks   columns of block_table.  The launch is sized on the host for the longest
+ *                sequence they can hold: a table far wider than the sequences costs time
  *   causal       1: the n_b queries of a sequence are its last n_b cached tokens, already
  *                written; query i sits at p = Lb - n_b + i and attends to [lo, p], lo =
  *                max(0, p - window + 1) when window > 0, else 0 (p < 0: nothing).

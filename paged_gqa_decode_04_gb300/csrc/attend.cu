@@ -20,7 +20,9 @@ namespace {
 // clusters on the GPU at once there are ceil(units / fit[c]) rounds, each of tiles / c key tiles
 // of `tile` us and a CTA's start and end, 10 us and for a join 1 us a doubling and, with more
 // than 128 rows, 6 more.  The smallest sum is taken; tiles are those of the longest sequence that
-// the table can hold.  Measured over c = 1, 2, 4, 8 (us; the choice is marked):
+// the table can hold, which may be far more than there are: where pieces fill the GPU four times,
+// the uneven end is not worth that risk and c is 1 (4 prompts of up to 4096 behind a table for
+// 131072: 265 us, 466 with c = 2).  Measured over c = 1, 2, 4, 8 (us; the choice is marked):
 //     2 sequences, 2048 cached, 4 queries each     33   22   19*  32
 //     8 sequences, up to 4096, 2-8 queries each    48   33*  44   75
 //     one prompt of 512, 32/8 heads                21*  28   47  102
@@ -31,7 +33,7 @@ int choose_cluster(const int (&fit)[4], int64_t units, int64_t max_tokens, bool 
     int best = 0;
     double least = 0;
     for (int i = 0; i < 4; ++i) {
-        if (fit[i] < 1 || (i && tiles < (1 << i))) break;
+        if (fit[i] < 1 || (i && (tiles < (1 << i) || units > 4 * fit[0]))) break;
         const double us = double((units + fit[i] - 1) / fit[i]) *
                           (tiles / (1 << i) * tile + 10 + (i ? i + (few ? 0 : 6) : 0));
         if (i == 0 || us < least) best = i, least = us;
