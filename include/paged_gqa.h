@@ -330,7 +330,8 @@ int paged_gqa_workspace_size_host(pgd_pool_t pool, int B, int q_len, int Hq, int
  *                sequence they can hold: a table far wider than the sequences costs time
  *   causal       1: the n_b queries of a sequence are its last n_b cached tokens, already
  *                written; query i sits at p = Lb - n_b + i and attends to [lo, p], lo =
- *                max(0, p - window + 1) when window > 0, else 0 (p < 0: nothing).
+ *                max(0, p - window + 1) when window > 0, else 0 (p < 0: nothing); with a
+ *                window, total + max_blocks * block_size stays below 2^31.
  *                0: every query attends to all Lb cached tokens (window must be 0);
  *                n_b and Lb are independent
  * A query that attends to nothing gets zeros.  Blocks that lie wholly before every

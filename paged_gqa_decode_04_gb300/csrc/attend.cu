@@ -115,6 +115,10 @@ extern "C" int paged_gqa_attend(pgd_pool_t pool, const void* q, int64_t q_stride
     }
     const int cap = max_blocks * p.block_size;
     const int group = Hq / p.hkv;
+    // a window that no length exceeds is none; the lower ends of the others, down to
+    // 1 - total - window, stay within 31 bits
+    if (window >= cap) window = 0;
+    if (window > 0 && (int64_t)total + cap > INT32_MAX) return PGD_ERR_SHAPE;
     if ((int64_t)total * group > INT32_MAX / 2) return PGD_ERR_SHAPE;
     const int64_t pieces = max_pieces(total, B, group, attend::kRowShift, 1);
     if (pieces * p.hkv * 8 > INT32_MAX) return PGD_ERR_SHAPE;

@@ -740,7 +740,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // a scale of 0 stays above 0: masked scores times K's are still -infinity,
                     // and weights times V's (0 in f16) can be summed without it
                     const float by = vs * gain < 1e-20f ? 1e-20f : vs * gain;
-                    const float4 e = make_float4(ks < 1e-30f ? 1e-30f : ks * a.scale_log2,
+                    const float on = ks * a.scale_log2;
+                    const float4 e = make_float4(on < 1e-30f ? 1e-30f : on,
                                                  log2f(by), 1.f / by, 0.f);
                     if (lane < pages)
                         for (int g = lane * box / 8; g < (lane + 1) * box / 8; ++g) to[g] = e;

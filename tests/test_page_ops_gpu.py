@@ -308,6 +308,35 @@ def test_attend_more_queries_than_cached():
         assert torch.all(got[300:310] == 0)
 
 
+def test_attend_largest_window():
+    """A window of 2^31 - 1 is none, also for queries before the first cached token."""
+    b = Batch([5, 0, 40, 200], [300, 10, 64, 130], hkv=2, seed=1)
+    q = b.rows(4)
+    got = check_attend(b, 4, True, 2 ** 31 - 1, q=q)
+    assert torch.equal(got, check_attend(b, 4, True, 0, q=q))
+
+
+@pytest.mark.parametrize("pages,scales", [("bf16", "head"), ("e4m3", "block"), ("int8", "head")])
+@pytest.mark.parametrize("B", [3, 12, 26])
+def test_attend_shared_by_clusters_of_every_size(B, pages, scales):
+    """Wide tables make clusters of 8, 4 and 2 CTAs share a piece of rows, though there are
+    few key tiles: shares without a tile, blocks of 256 rows, one block and less."""
+    b = Batch([700 + 16 * i for i in range(B)], [(150, 20, 200, 90)[i % 4] for i in range(B)],
+              hkv=1, pages=pages, scales=scales, seed=B)
+    wide = torch.full((B, 4096 - b.table.shape[1]), -1, dtype=torch.int32)
+    b.table = torch.cat([b.table, wide], 1).contiguous()
+    check_attend(b, 4, True, 0)
+    check_attend(b, 4, False, 0)
+    check_attend(b, 4, True, 100)
+
+
+@pytest.mark.parametrize("pages,scales", [("bf16", "head"), ("e4m3", "head"), ("int8", "block")])
+def test_attend_small_logit_scales(pages, scales):
+    """A scale near the smallest float32: all weights are equal, masked tokens have none."""
+    b = Batch([300, 70], [140, 70], hkv=2, pages=pages, scales=scales, seed=8)
+    check_attend(b, 4, True, 40, scale=1e-37)
+
+
 @pytest.mark.parametrize("pages", ["bf16", "e4m3"])
 def test_attend_windows_skip_released_blocks(pages):
     """Blocks wholly before every window may be gone: table entry -1, pages poisoned."""
@@ -508,15 +537,18 @@ def test_refusals():
                      (dict(o=256), A), (dict(v=1 << 21), A),
                      (dict(qw=257), AL), (dict(kw=258, wd=0), AL)):
         assert nr(**kw) == want, kw
-    abase = dict(q=1 << 20, qs=512, total=4, hq=4, B=1, causal=1, window=0, scale=1.0, o=1 << 21)
+    abase = dict(q=1 << 20, qs=512, total=4, hq=4, B=1, causal=1, window=0, scale=1.0, o=1 << 21,
+                 mb=2)
     at = lambda **kw: (lambda a: raw(
-        "paged_gqa_attend", h, a["q"], a["qs"], a["total"], a["hq"], 256, a["B"], 256, 2, 256,
-        a["causal"], a["window"], a["scale"], a["o"], None))({**abase, **kw})
+        "paged_gqa_attend", h, a["q"], a["qs"], a["total"], a["hq"], 256, a["B"], 256, a["mb"],
+        256, a["causal"], a["window"], a["scale"], a["o"], None))({**abase, **kw})
     assert at(total=0) == _lib.PGD_OK
     for kw, want in ((dict(hq=0), A), (dict(hq=3), H), (dict(causal=2), A), (dict(window=-1), A),
                      (dict(causal=0, window=4), A), (dict(scale=float("inf")), A),
                      (dict(q=None), A), (dict(o=None), A), (dict(q=(1 << 20) + 2), AL),
-                     (dict(qs=511), H), (dict(qs=516), AL), (dict(o=(1 << 20) + 256), A)):
+                     (dict(qs=511), H), (dict(qs=516), AL), (dict(o=(1 << 20) + 256), A),
+                     # positions less a window would pass 31 bits
+                     (dict(total=4000, mb=(1 << 27) - 64, window=9, o=1 << 26), H)):
         assert at(**kw) == want, kw
     ok(pool)
     assert torch.equal(bits(b.dk), before)
