@@ -52,11 +52,11 @@
 // each of its four softmax warps, one in every quarter of the SM, has 128 exponentials of
 // 4.07 cycles (521), about 900 cycles with the maxima, sums and conversions; the two blocks'
 // warps of a quarter together take 1500.  So the softmax hides behind the products of both
-// blocks (2048 cycles) with little to spare.  Measured (bfloat16, 64/8 heads, 2048 queries): of 32768
-// tokens 1357 us, 1.57 PFLOP/s, 81% of a library product's burst (1260 us and 88% before the
-// clock drops under the load); of 8192 tokens 337 us with the tensor cores busy 60% of the
-// time, since a CTA's query load, first tiles and epilogue (some 15 us) are not hidden and
-// causal pieces end unevenly.  Over 8-bit pages the widening warps share the issue slots
+// blocks (2048 cycles) with little to spare.  Measured (bfloat16, 64/8 heads, 2048 queries):
+// of 32768 tokens 1357 us, 1.57 PFLOP/s, 81% of a library product's burst (1260 us and 88%
+// before the clock drops under the load); of 8192 tokens 337 us with the tensor cores busy 60%
+// of the time, since a CTA's search, query load, first tile and epilogue (some 10 us) are not
+// hidden and causal pieces end unevenly.  Over 8-bit pages the widening warps share the issue slots
 // with the softmax: 42% (scales per block).
 //
 // Every wait is bounded; one that gives up latches PGD_ERR_TIMEOUT and ends the CTA.

@@ -412,7 +412,8 @@ __device__ __forceinline__ void write_blocks(const WriteArgs& a, float* smax) {
     const int lo = blk.lo, hi = blk.hi;
     const int64_t stride = side ? a.v_stride : a.k_stride;
     // this lane's elements of packed row j of the block, and of pool row j
-    const Act* const src = static_cast<const Act*>(side ? a.v : a.k) + blk.row() * stride + h * D + d0;
+    const Act* const src =
+        static_cast<const Act*>(side ? a.v : a.k) + blk.row() * stride + h * D + d0;
     const int row = a.hkv * D;
     const int64_t id = max(blk.id, (int64_t)0);
     uint8_t* const dst = static_cast<uint8_t*>(side ? a.v_pool : a.k_pool) +

@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(kWarps * 32) read_kernel(const ReadArgs a) {
 #pragma unroll
         for (int i = 0; i < kTokens; ++i) {
             if (slot[i] == -2) continue;
-            uint4 k = widen<PAGE>(x[2 * i], sc[2 * i]), v = widen<PAGE>(x[2 * i + 1], sc[2 * i + 1]);
+            uint4 k = widen<PAGE>(x[2 * i], sc[2 * i]);
+            uint4 v = widen<PAGE>(x[2 * i + 1], sc[2 * i + 1]);
             if (slot[i] == -1) k = v = make_uint4(nan2, nan2, nan2, nan2);
             ko[i * row_vec + j] = k;
             vo[i * row_vec + j] = v;
