@@ -46,7 +46,7 @@
 // constants of the CTA.  Scales per block go where a float32 value is at hand anyway, K's on
 // the scores and V's into the exponent of the weights (the row's sum takes them out again):
 // multiplied into V while it is widened they cost 5% of the whole (2048 of 8192 tokens, 64/8
-// heads: 489 against 465 us; 407 with scales per head, 337 over bfloat16).
+// heads: 489 against 465 us; now 445, 402 with scales per head, 337 over bfloat16).
 //
 // What bounds it.  At D = 128 a tile of one block is 2 x 8 products of 64 cycles (1024), and
 // each of its four softmax warps, one in every quarter of the SM, has 128 exponentials of
@@ -81,6 +81,13 @@ constexpr int kTile = 128;      // tokens of a key tile
 constexpr int kBlock = 128;     // rows of a block
 constexpr int kRowShift = 8;    // log2 of the rows of a CTA
 constexpr int kThreads = 512;
+// Registers a thread: launched with 128, then the 256 threads of the softmax take 200, the
+// 128 producers or widening warps keep 64 and the last 128 keep 48, which is the launch's
+// 65536 again (192, 80 and 48 with scales per block: 460 against 445 us at 2048 of 8192
+// tokens, 64/8 heads).
+constexpr int kSoftmaxRegs = 200, kProducerRegs = 64, kIssuerRegs = 48;
+static_assert(256 * kSoftmaxRegs + 128 * (kProducerRegs + kIssuerRegs) == kThreads * 128,
+              "registers of the launch");
 constexpr float kGrow = 8.f;    // base-2 growth of a maximum that is let pass
 
 struct Args {
@@ -104,25 +111,15 @@ struct Layout {
     static constexpr bool kQ8 = PAGE != PGD_BF16;
     static constexpr int kHalves = D / 64;                 // 128-byte columns of a 16-bit tile
     static constexpr int kSlot = kTile * D * 2;            // bytes of a K or V tile
-    // Registers a thread: launched with 128, then the 256 threads of the softmax, the 128
-    // producers and the last 128 share the launch's 65536 anew.  With scales per block the
-    // widening warps need more (482 against 497 us: two chunks of 1400 tokens, 10k cached
-    // each, 32/8 heads), else the softmax does.
-    static constexpr int kSoftmaxRegs = PB ? 192 : 200;
-    static constexpr int kProducerRegs = PB ? 80 : 64;
-    static constexpr int kIssuerRegs = 48;
-    static_assert(256 * kSoftmaxRegs + 128 * (kProducerRegs + kIssuerRegs) == kThreads * 128,
-                  "registers of the launch");
-    // Stored tiles wait for their scales as well, so more of them pay where there are any
-    // (482 against 498 us there).
-    static constexpr int kSlots = kQ8 ? PB ? 3 : 4 : D == 128 ? 5 : 8;
+    static constexpr int kSlots = kQ8 ? 4 : D == 128 ? 5 : 8;
     static constexpr int kQ = kBlock * D * 2;              // bytes of a block of queries
     static constexpr int kRing = 2 * kQ;
-    // 8-bit pages: tiles as they are stored, and the scales of the tiles in flight (a tile is
-    // at most 1 + (kRawSlots + kSlots) / 2 ahead of the softmax): for each 8 tokens K's,
+    // 8-bit pages: tiles as they are stored, and the scales of the tiles in flight (those of
+    // tile j + 1 are written when V of j has a slot, so when V of j - 3 is done with, and the
+    // weights that it was multiplied with before that): for each 8 tokens K's,
     // log2 of V's and 1 over V's, then V's gain.
     static constexpr int kRawSlot = kTile * 128;
-    static constexpr int kRawSlots = PB ? 4 : 2;
+    static constexpr int kRawSlots = 2;
     static constexpr int kRaw = kRing + kSlots * kSlot;
     static constexpr int kScaleTiles = 6;
     static constexpr int kScales = kRaw + (kQ8 ? kRawSlots * kRawSlot : 0);
@@ -346,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 8) {
         // ---------------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const Span p = blk ? sp[1] : sp[0];
         if (p.t1 > p.t0) {
             // the block's queries into shared memory, swizzled
@@ -540,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (kQ8 && warp < 12) {
         // ---------------------------------------------------------- widening (8-bit pages)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kProducerRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
         // A warp reads 64 of the 128 codes of 8 rows at a time and stores them as f16.  Its
         // lanes take rows r and r ^ 5 in pairs, so that neither the reads (in 16-byte pieces
         // swizzled by r) nor the writes (every other piece, swizzled alike) share a bank.
@@ -591,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (!kQ8 && warp < 12) {
         // -------------------------------------------------------------- producers
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kProducerRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
         // Copy k of a tile (page k / kHalves, column k % kHalves) is issued by warp k % 4,
         // lane k / 4: the lanes of one warp take turns, 54 cycles each.
         const int bs = a.r.block_size, me = warp - 8;
@@ -671,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bar_wait(bar_full + 8 * (i % L::kSlots), i / L::kSlots & 1, &never);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kIssuerRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssuerRegs));
     }
     if (kQ8 && warp >= 14) {
         // -------------------------------------------------------- producers (8-bit pages)
@@ -704,6 +701,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             vs = scale_of(a.v_scale, id_s, 0.f);
             id_s = id_of(T0 + 1, lane);
         }
+        // The scales of tile j; warp 14's arrival at the tile's keys hands them over.  That of
+        // kScaleTiles before is done with: its values were used before the keys after it.
+        auto put_scales = [&](int j) {
+            float4* const to = reinterpret_cast<float4*>(
+                smem + L::kScales + (j - T0) % L::kScaleTiles * L::kScaleBytes);
+            // scales are not negative, so their bits are ordered alike
+            const float most = __uint_as_float(
+                __reduce_max_sync(0xffffffffu, __float_as_uint(vs) & 0x7fffffffu));
+            if (most * gain > 128.f || gain == 0.f) {
+                const int e = min(max((__float_as_int(most) >> 23) & 255, 5), 252);
+                gain = __int_as_float((257 - e) << 23);
+            }
+            // a scale of 0 stays above 0: masked scores times K's are still -infinity,
+            // and weights times V's (0 in f16) can be summed without it
+            const float by = vs * gain < 1e-20f ? 1e-20f : vs * gain;
+            const float on = ks * a.scale_log2;
+            const float4 e =
+                make_float4(on < 1e-30f ? 1e-30f : on, __log2f(by), __fdividef(1.f, by), 0.f);
+            if (lane < pages)
+                for (int g = lane * box / 8; g < (lane + 1) * box / 8; ++g) to[g] = e;
+            if (lane == 0) to[kTile / 8].x = gain;
+        };
+        if (scaling) put_scales(T0);
         uint32_t raw = 0, turn = 0, n = 0;
         bool live = true;
         for (int j = T0; j < T1 && live; ++j) {
@@ -725,28 +745,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int side = 0; side < 2; ++side) {
                 if (live) live = warp_wait(bar_raw_empty + 8 * raw, turn ^ 1, gave_up);
                 if (!live) break;
-                if (scaling && side == 0) {
-                    // the tile kScaleTiles back is done with: its slot in the ring was reused
-                    float4* const to = reinterpret_cast<float4*>(
-                        smem + L::kScales + (j - T0) % L::kScaleTiles * L::kScaleBytes);
-                    float most = vs;
-#pragma unroll
-                    for (int m = 1; m < 32; m *= 2)
-                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
-                    if (most * gain > 128.f || gain == 0.f) {
-                        const int e = min(max((__float_as_int(most) >> 23) & 255, 5), 252);
-                        gain = __int_as_float((257 - e) << 23);
-                    }
-                    // a scale of 0 stays above 0: masked scores times K's are still -infinity,
-                    // and weights times V's (0 in f16) can be summed without it
-                    const float by = vs * gain < 1e-20f ? 1e-20f : vs * gain;
-                    const float on = ks * a.scale_log2;
-                    const float4 e = make_float4(on < 1e-30f ? 1e-30f : on,
-                                                 log2f(by), 1.f / by, 0.f);
-                    if (lane < pages)
-                        for (int g = lane * box / 8; g < (lane + 1) * box / 8; ++g) to[g] = e;
-                    if (lane == 0) to[kTile / 8].x = gain;
-                }
                 __syncwarp();
                 if (lane == 0) {
                     if (bytes)
@@ -764,6 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             id = next;
             ks = next_ks;
             vs = next_vs;
+            // behind this tile's copies, which it would hold up
+            if (scaling && live && j + 1 < T1) put_scales(j + 1);
         }
         if (!live) {  // no copy of this warp may land after the CTA has ended
             volatile int never = 0;
