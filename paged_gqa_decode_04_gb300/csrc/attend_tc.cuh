@@ -57,7 +57,7 @@
 // before the clock drops under the load); of 8192 tokens 337 us with the tensor cores busy 60%
 // of the time, since a CTA's search, query load, first tile and epilogue (some 10 us) are not
 // hidden and causal pieces end unevenly.  Over 8-bit pages the widening warps share the issue slots
-// with the softmax: 42% (scales per block).
+// with the softmax: 44% (scales per block).
 //
 // Every wait is bounded; one that gives up latches PGD_ERR_TIMEOUT and ends the CTA.
 #pragma once
