@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
                     tmem_st32(to + i, o);
                 }
-                wait_st();  // a tile may rescale twice, for the gain and for the maximum
+                if (PB) wait_st();  // a tile may rescale twice, for the gain and for the maximum
             };
             const int first = p.t0 + (paired ? blk : 0), by = paired ? 2 : 1;  // its tiles
             // One tile of scores; `edge`: some row does not see all of it.

@@ -6,8 +6,12 @@ import torch
 import paged_gqa_decode_04_gb300 as pgd
 from oracle import page_ops as ref
 from page_ops_cases import Batch
+from paged_gqa_decode_04_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
+
+FORMS = [("bf16", "head", 64), ("bf16", "head", 128), ("e4m3", "head", 128),
+         ("int8", "head", 128), ("e4m3", "block", 128), ("int8", "block", 128)]
 
 
 def check_rows(b, got, q, scale, causal, window, skip=()):
@@ -64,4 +68,61 @@ def test_attend_gain_and_maximum_change_in_one_tile(pages, rows):
         check_rows(b, got, q, 1.0, causal, 0)
         got = got.view(n, rows, 4, 128)
         assert torch.equal(got, got[:1].expand_as(got))
+    pool.close()
+
+
+# lengths, new rows, KV heads, columns of the table (0: as many as needed), logical block
+# that is bad in the last sequence: pieces of both blocks of rows, one block, and pieces
+# that clusters share
+BAD_PAGES = [([40, 300], [40, 300], 2, 0, 9), ([40, 300], [40, 300], 2, 0, 18),
+             ([129, 700], [20, 260], 2, 0, 33), ([9, 150], [9, 30], 2, 0, 8),
+             ([2498], [4], 1, 0, 156), ([800, 700], [3, 150], 1, 4096, 38)]
+
+
+@pytest.mark.parametrize("case", range(len(BAD_PAGES)))
+@pytest.mark.parametrize("form", range(len(FORMS)))
+def test_attend_bad_page_reaches_only_the_rows_that_read_it(form, case):
+    pages, scales, d = FORMS[form]
+    lens, new, hkv, columns, at = BAD_PAGES[case]
+    b = Batch(lens, new, hkv=hkv, d=d, pages=pages, scales=scales, seed=at)
+    if columns:
+        wide = torch.full((len(lens), columns - b.table.shape[1]), -1, dtype=torch.int32)
+        b.table = torch.cat([b.table, wide], 1).contiguous()
+    q = b.rows(4 * hkv)
+    pool = b.pool()
+    cu, table, len_t = b.where()
+    s = len(lens) - 1
+    table[s, at] = (-1, -2 ** 31, 2 ** 31 - 1, b.k.shape[0])[(form + case) % 4]
+    for causal, window in ((True, 0), (True, 37), (False, 0)):
+        got = pgd.paged_gqa_attend(pool, b.to(q), cu, table, len_t, 0.1, causal=causal,
+                                   window=window)
+        lost = set()
+        for row, pos in ref.rows_of(b.cu, b.lens, s):
+            lo, hi = (max(0, pos - window + 1) if window else 0, pos + 1) if causal \
+                else (0, lens[s])
+            if lo < min(16 * at + 16, lens[s]) and hi > 16 * at:
+                lost.add(row)
+        assert pgd.paged_gqa_get_error(pool) == (_lib.PGD_ERR_BLOCK_ID if lost else 0)
+        nan = got.isnan().cpu()
+        assert set(nan.any(2).any(1).nonzero()[:, 0].tolist()) == lost
+        assert nan[sorted(lost)].all()
+        check_rows(b, got, q, 0.1, causal, window, skip=lost)
+    pool.close()
+
+
+@pytest.mark.parametrize("pages", ["bf16", "e4m3"])
+def test_attend_several_bad_pages(pages):
+    """Windowed rows between two bad pages read neither of them."""
+    b = Batch([900], [900], hkv=1, pages=pages, seed=3)
+    q = b.rows(3)
+    pool = b.pool()
+    cu, table, len_t = b.where()
+    for at in (2, 3, 30, 50):
+        table[0, at] = -1
+    got = pgd.paged_gqa_attend(pool, b.to(q), cu, table, len_t, 0.1, window=100)
+    lost = {p for p in range(900) if any(16 * at <= p < 16 * at + 16 + 99 for at in (2, 3, 30, 50))}
+    assert pgd.paged_gqa_get_error(pool) == _lib.PGD_ERR_BLOCK_ID
+    nan = got.isnan().all(2).all(1).cpu()
+    assert set(nan.nonzero()[:, 0].tolist()) == lost
+    check_rows(b, got, q, 0.1, True, 100, skip=lost)
     pool.close()
