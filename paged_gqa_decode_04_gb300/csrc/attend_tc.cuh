@@ -21,7 +21,9 @@
 // and 16 for V: one warp needs 2830 cycles for what the products take 2048 for, four need
 // 1650.  (Copies of 16 bytes by the threads of four warps, cp.async: 4850.)  Pages no query
 // of the CTA sees are not fetched, and V rows outside the visible range are zeroed, so that
-// nothing in an unused slot is multiplied.
+// nothing in an unused slot is multiplied.  A page whose block id is out of range has V
+// zeroed as well (8-bit pages: fetched from a coordinate outside the tensor, which reads zeros),
+// so that rows that do not see it stay right; those that do become NaN at the end.
 //
 // Warps: 0-3 and 4-7 the softmax of the two blocks, 8-11 the producers, 12 and 13 issue the
 // products of one block each; 14 and 15 only round the group up to four warps, the unit
@@ -156,6 +158,36 @@ __device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int first, 
         p.lo = p.hi = 0;
     }
     return p;
+}
+
+__device__ __forceinline__ bool valid(const Ragged& r, int id) {
+    return id >= 0 && id < r.num_blocks;
+}
+
+// A CTA that met a block id out of range: the rows of its piece that see such a page become
+// NaN.  It looks everything up again, so that nothing is held for it through the softmax, and
+// comes once all results of the cluster are written.
+template <int D>
+__device__ __forceinline__ void erase_rows(const Args& a) {
+    const int64_t unit = blockIdx.x / a.cluster, head = unit / a.pieces;
+    const int piece = a.pieces - 1 - int(unit % a.pieces);
+    const Seq s = load_seq(a.r, find_seq(a.r, piece, a.group, kRowShift, 1));
+    const int row0 = int(piece - first_piece(a.r, s.b, a.group, kRowShift, 1)) << kRowShift;
+    const int32_t* const table = a.r.table + (int64_t)s.b * a.r.max_blocks;
+    const int end = min(s.n * a.group, row0 + (1 << kRowShift));
+    for (int row = row0 + threadIdx.x; row < end; row += kThreads) {
+        const int token = row / a.group, pos = s.len - s.n + token;
+        const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+        const int hi = a.causal ? pos + 1 : s.len;
+        bool bad = false;
+        for (int i = lo / a.r.block_size; lo < hi && i <= (hi - 1) / a.r.block_size; ++i)
+            bad |= !valid(a.r, __ldg(table + i));
+        if (!bad) continue;
+        const int64_t at = (s.row0 + (int64_t)token) * a.hq + head * a.group + row % a.group;
+        uint4* const out = reinterpret_cast<uint4*>(a.out + at * D);
+        for (int i = 0; i < D / 8; ++i)
+            out[i] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+    }
 }
 
 // Token and head of the group of row r, r + step, r + 2 step, ..: one division for all.
@@ -611,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool live = true;
         for (int j = T0; j < T1 && live; ++j) {
             const int next = id_of(j + 1);
-            const bool ok = id >= 0 && id < a.r.num_blocks;
+            const bool ok = valid(a.r, id);
             if (seen(j) && !ok) {
                 latch(a.r.err, PGD_ERR_BLOCK_ID);
                 *bad = 1;
@@ -690,8 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return seen(j, pg) ? __ldg(table + (j * kTile + pg * box) / bs) : -1;
         };
         auto scale_of = [&](const float* scales, int id, float none) {
-            return id >= 0 && id < a.r.num_blocks ? __ldg(scales + (int64_t)id * a.hkv + head)
-                                                  : none;
+            return valid(a.r, id) ? __ldg(scales + (int64_t)id * a.hkv + head) : none;
         };
         int id = id_of(T0, page), id_s = -1;
         float ks = 1.f, vs = 0.f, gain = 0.f;
@@ -735,10 +766,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 next_vs = scale_of(a.v_scale, id_s, 0.f);
                 id_s = id_of(j + 2, lane);
             }
-            const bool ok = id >= 0 && id < a.r.num_blocks;
-            if (seen(j, page) && !ok) {
+            const bool ok = seen(j, page);
+            if (ok && !valid(a.r, id)) {
                 latch(a.r.err, PGD_ERR_BLOCK_ID);
                 *bad = 1;
+                id = -1;  // outside the tensor: zeros
             }
             const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * box * 128;
             const int row = (j * kTile + page * box) % bs;
@@ -871,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    const bool failed = *gave_up || *bad || !s.ok;
+    const bool failed = *gave_up || !s.ok;
     if (*gave_up && threadIdx.x == 0) latch(a.r.err, PGD_ERR_TIMEOUT);
 
     // -------------------------------------------------------------------- results
@@ -1025,6 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_sync();  // shared memory stays until every CTA has read it
     }
     __syncthreads();
+    if (*bad) erase_rows<D>(a);
     if (warp == 12) tmem_free(tmem, 512);
 }
 
