@@ -338,10 +338,12 @@ int paged_gqa_workspace_size_host(pgd_pool_t pool, int B, int q_len, int Hq, int
  * query's window are never read.  Cached keys and values are expected to be finite where a
  * query of the sequence may attend to them; slots past Lb may hold anything.
  * bfloat16 and 8-bit pools (PGD_ERR_UNSUPPORTED for float32; with 8-bit pages queries
- * stay below 65504 in magnitude and scales are not negative; with scales per block a weight
- * times V's scale keeps 11 bits down to 2^-17 of the largest, then 2^-28 of that).  No
- * workspace.  Sequences whose cu_seqlens or length is impossible latch PGD_ERR_SEQ_LEN, block
- * ids out of range PGD_ERR_BLOCK_ID; the rows that would have read them are written as NaN.
+ * stay below 65504 in magnitude and scales are not negative; with scales per head a weight
+ * keeps 11 bits down to 2^-21 of the largest, then half a step of 2^-31 of that; with scales
+ * per block a weight times V's scale keeps 11 bits down to 2^-17 of the largest, then 2^-28 of
+ * that).  No workspace.  Sequences whose cu_seqlens or length is impossible latch
+ * PGD_ERR_SEQ_LEN, block ids out of range PGD_ERR_BLOCK_ID; the rows that would have read them
+ * are written as NaN.
  */
 int paged_gqa_attend(pgd_pool_t pool, const void *q, int64_t q_stride, int total, int Hq,
                      const int32_t *cu_seqlens, int B, const int32_t *block_table,

@@ -91,6 +91,11 @@ constexpr int kSoftmaxRegs = 200, kProducerRegs = 64, kIssuerRegs = 48;
 static_assert(256 * kSoftmaxRegs + 128 * (kProducerRegs + kIssuerRegs) == kThreads * 128,
               "registers of the launch");
 constexpr float kGrow = 8.f;    // base-2 growth of a maximum that is let pass
+// Base-2 lift of f16 weights over 8-bit pages with scales per head: up to 2^(kGrow + kLift) they
+// stay below 65504, and keep 11 bits down to 2^-21 of the running maximum's, then steps of 2^-31
+// of it (without: 2^-14 and 2^-24, so that a long tail of weights below 2^-25 vanished in P V,
+// though not in their sum).  The sum and the accumulator have the same factor.
+constexpr float kLift = 7.f;
 
 struct Args {
     Ragged r;
@@ -459,7 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // scores' registers and 8 at a time; along with the first half the largest of
                 // all 128 scores: the exponentials set the pace, the rest is issued in between
                 auto weigh = [&](int h) {
-                    const float off = m == -INFINITY ? 0.f : -m;
+                    float off = m == -INFINITY ? 0.f : -m;
+                    if (kQ8 && !PB) off += kLift;
 #pragma unroll
                     for (int g = 0; g <= 8; ++g) {
                         const int at = h * (kTile / 2) + g * 8;

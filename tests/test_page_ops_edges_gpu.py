@@ -126,3 +126,32 @@ def test_attend_several_bad_pages(pages):
     assert set(nan.nonzero()[:, 0].tolist()) == lost
     check_rows(b, got, q, 0.1, True, 100, skip=lost)
     pool.close()
+
+
+@pytest.mark.parametrize("exponent", [23.6, 25.5])
+@pytest.mark.parametrize("pages", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows", [2, 90])
+def test_attend_tail_far_below_the_largest_weight(pages, rows, exponent):
+    """One token with all but a 2^-exponent-th of every other token's weight, its value zero:
+    the output is the tail's, c N w / (1 + N w).  Weights are held times 2^7 in 11 bits, in
+    steps of 2^-24 at least: to half a step, max(2^-11 w, 2^-32)."""
+    n = 3001
+    b = Batch([n], [rows], hkv=1, pages=pages, seed=1)
+    b.k.view(torch.uint8).zero_()
+    first = int(b.table[0, 0])
+    b.k[first, 0] = torch.ones(1, 128).to(b.k.dtype)
+    c = 56.0 if pages == "e4m3" else 77.0
+    b.v[:] = torch.full(b.v.shape, c).to(b.v.dtype)
+    b.v[first, 0] = torch.zeros(1, 128).to(b.v.dtype)
+    b.k_scale.fill_(1.0), b.v_scale.fill_(1.0)
+    q = torch.full((rows, 4, 128), 1.0).bfloat16()
+    scale = float(np.float32(exponent * np.log(2) / 128))
+    pool = b.pool()
+    got = pgd.paged_gqa_attend(pool, q.cuda(), *b.where(), scale, causal=False).cpu().double()
+    assert pgd.paged_gqa_get_error(pool) == 0
+    pool.close()
+    w = 2.0 ** -exponent
+    want = c * (n - 1) * w / (1 + (n - 1) * w)
+    # the weights' rounding; float32 scores, exponentials and sums; the output's rounding
+    tol = want * (max(2.0 ** -11, 2.0 ** -32 / w) + 2.0 ** -12 + 2.0 ** -8)
+    assert (got - want).abs().max() <= tol
