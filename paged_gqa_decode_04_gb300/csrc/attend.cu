@@ -8,6 +8,7 @@
 // cores: attend_tc.cuh.  This file checks the arguments and chooses the launch.
 #include <atomic>
 
+#include "attend_plan.h"
 #include "attend_tc.cuh"
 #include "page_maps.h"
 #include "page_ops.h"
@@ -15,31 +16,6 @@
 
 namespace pgd {
 namespace {
-
-// CTAs that share the keys of a piece of rows (a cluster of c).  With `units` pieces and `fit[c]`
-// clusters on the GPU at once there are ceil(units / fit[c]) rounds, each of tiles / c key tiles
-// of `tile` us and a CTA's start and end, 10 us and for a join 1 us a doubling and, with more
-// than 128 rows, 6 more.  The smallest sum is taken; tiles are those of the longest sequence that
-// the table can hold, which may be far more than there are: where pieces fill the GPU four times,
-// the uneven end is not worth that risk and c is 1 (4 prompts of up to 4096 behind a table for
-// 131072: 265 us, 466 with c = 2).  Measured over c = 1, 2, 4, 8 (us; the choice is marked):
-//     2 sequences, 2048 cached, 4 queries each     33   22   19*  32
-//     8 sequences, up to 4096, 2-8 queries each    48   33*  44   75
-//     one prompt of 512, 32/8 heads                21*  28   47  102
-//     2048 queries of 32768, 64/8 heads          1349 1260* 1455
-//     2048 queries of 8192, 64/8 heads            336* 379  522
-int choose_cluster(const int (&fit)[4], int64_t units, int64_t max_tokens, bool few, double tile) {
-    const double tiles = double((max_tokens + attend::kTile - 1) / attend::kTile);
-    int best = 0;
-    double least = 0;
-    for (int i = 0; i < 4; ++i) {
-        if (fit[i] < 1 || (i && (tiles < (1 << i) || units > 4 * fit[0]))) break;
-        const double us = double((units + fit[i] - 1) / fit[i]) *
-                          (tiles / (1 << i) * tile + 10 + (i ? i + (few ? 0 : 6) : 0));
-        if (i == 0 || us < least) best = i, least = us;
-    }
-    return 1 << best;
-}
 
 template <int D, int PAGE, bool PB>
 cudaError_t launch(attend::Args& a, const Pool& p, const PageMaps& maps, cudaStream_t s) {
@@ -78,7 +54,8 @@ cudaError_t launch(attend::Args& a, const Pool& p, const PageMaps& maps, cudaStr
     const bool few = (int64_t)a.r.total * a.group <= (int64_t)a.pieces * kBlock;
     // us of a key tile of 256 rows (measured at D = 128)
     const double tile = PAGE == PGD_BF16 ? 1.2 : PB ? 1.75 : 1.5;
-    a.cluster = choose_cluster(fit, (int64_t)a.pieces * a.hkv, a.r.max_len, few, tile);
+    a.cluster = choose_cluster(fit, (int64_t)a.pieces * a.hkv,
+                               piece_tiles(a.r.max_len, a.window, a.group), few, tile);
     attr[0].val.clusterDim.x = a.cluster;
     cfg.gridDim = dim3(unsigned(a.pieces) * a.hkv * a.cluster);
     cfg.numAttrs = a.cluster > 1 ? 1 : 0;

@@ -39,7 +39,7 @@
 //
 // Few rows.  128 rows or fewer go to both blocks, every other tile each, so that one's
 // softmax still hides behind the other's products; and where that pays, 2, 4 or 8 CTAs of a
-// cluster share a piece's key tiles (choose_cluster in attend.cu).  The parts
+// cluster share a piece's key tiles (choose_cluster in attend_plan.h).  The parts
 // join their sums through shared memory, each other's in a cluster:
 // out = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k.
 //
@@ -70,6 +70,7 @@
 
 #include <type_traits>
 
+#include "attend_plan.h"
 #include "page_ops.h"
 #include "ragged.cuh"
 #include "umma.cuh"
@@ -79,9 +80,7 @@ namespace attend {
 
 using namespace umma;
 
-constexpr int kTile = 128;      // tokens of a key tile
 constexpr int kBlock = 128;     // rows of a block
-constexpr int kRowShift = 8;    // log2 of the rows of a CTA
 constexpr int kThreads = 512;
 // Registers a thread: launched with 128, then the 256 threads of the softmax take 200, the
 // 128 producers or widening warps keep 64 and the last 128 keep 48, which is the launch's

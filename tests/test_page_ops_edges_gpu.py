@@ -155,3 +155,19 @@ def test_attend_tail_far_below_the_largest_weight(pages, rows, exponent):
     # the weights' rounding; float32 scores, exponentials and sums; the output's rounding
     tol = want * (max(2.0 ** -11, 2.0 ** -32 / w) + 2.0 ** -12 + 2.0 ** -8)
     assert (got - want).abs().max() <= tol
+
+
+@pytest.mark.parametrize("pages,scales", [("bf16", "head"), ("e4m3", "block"), ("int8", "head")])
+@pytest.mark.parametrize("new", [(150, 20, 200), (3, 2, 1)])
+def test_attend_windows_shared_by_clusters(new, pages, scales):
+    """Windows of a dozen key tiles behind a wide table, which clusters of 8 CTAs share."""
+    b = Batch([2500, 2200, 1900], new, hkv=1, pages=pages, scales=scales, seed=new[0])
+    wide = torch.full((3, 4096 - b.table.shape[1]), -1, dtype=torch.int32)
+    b.table = torch.cat([b.table, wide], 1).contiguous()
+    q = b.rows(4)
+    pool = b.pool()
+    for window in (1500, 200, 1):
+        got = pgd.paged_gqa_attend(pool, b.to(q), *b.where(), 0.09, window=window)
+        assert pgd.paged_gqa_get_error(pool) == 0
+        check_rows(b, got, q, 0.09, True, window)
+    pool.close()
