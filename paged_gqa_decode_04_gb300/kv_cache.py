@@ -136,6 +136,8 @@ def _check_tables(pool, cu_seqlens, block_table, seq_lens):
     B = seq_lens.shape[0]
     if cu_seqlens.shape[0] != B + 1 or block_table.shape[0] != B:
         raise ValueError("shape mismatch between cu_seqlens, block_table and seq_lens")
+    if B >= 2 ** 31 or block_table.shape[1] >= 2 ** 31:   # the library takes them as C ints
+        raise ValueError("block_table must have fewer than 2^31 rows and columns")
     for t in (cu_seqlens, block_table, seq_lens):
         if t.get_device() != dev or not t.is_contiguous():   # -1 for CPU tensors
             raise ValueError("tables must be contiguous CUDA tensors on the pool's device")
@@ -300,8 +302,9 @@ def paged_gqa_attend(pool, q, cu_seqlens, block_table, seq_lens, scale, causal=T
     _check_rows(pool, "out", out, Hq, total)
     if not out.is_contiguous():
         raise ValueError("out must be contiguous")
+    window = min(max(int(window), -1), 2 ** 31 - 1)   # none there is longer; C takes an int
     _check(_lib.load().paged_gqa_attend(
         pool.handle, q.data_ptr(), qs, total, Hq, cu_seqlens.data_ptr(), B,
         block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), int(bool(causal)),
-        int(window), float(scale), out.data_ptr(), _stream_on(pool, stream)), "paged_gqa_attend")
+        window, float(scale), out.data_ptr(), _stream_on(pool, stream)), "paged_gqa_attend")
     return out

@@ -171,3 +171,16 @@ def test_attend_windows_shared_by_clusters(new, pages, scales):
         assert pgd.paged_gqa_get_error(pool) == 0
         check_rows(b, got, q, 0.09, True, window)
     pool.close()
+
+
+@pytest.mark.parametrize("window", [2 ** 31, 2 ** 32 + 5, 2 ** 70])
+def test_attend_windows_beyond_an_int(window):
+    """A window that no length reaches is none, whatever its width; one below zero is refused."""
+    b = Batch([200], [60], hkv=1, seed=2)
+    q = b.rows(2)
+    pool = b.pool()
+    got = pgd.paged_gqa_attend(pool, b.to(q), *b.where(), 0.1, window=window)
+    assert torch.equal(got, pgd.paged_gqa_attend(pool, b.to(q), *b.where(), 0.1))
+    with pytest.raises(pgd.PagedGQAError, match="PGD_ERR_ARG"):
+        pgd.paged_gqa_attend(pool, b.to(q), *b.where(), 0.1, window=-window)
+    pool.close()
