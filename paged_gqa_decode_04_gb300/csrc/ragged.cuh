@@ -23,7 +23,7 @@ struct Ragged {
     int max_blocks;
     int block_size;
     int64_t num_blocks;
-    int max_len;           // largest length allowed (table capacity, position table)
+    int max_len;           // largest length of a sequence with rows (blocks, rotation table)
     int* err;
 };
 
@@ -81,11 +81,15 @@ __device__ __forceinline__ int find_seq(const Ragged& r, int64_t x, int mul, int
 }
 
 // Latch the error of every sequence that fails its checks (one CTA of a launch calls
-// this, so that none is missed however cu is laid out).
+// this, so that none is missed however cu is laid out).  One without rows asks for no
+// position: it may be as long as its blocks.
 __device__ __forceinline__ void check_all(const Ragged& r, bool rows_within_len) {
     for (int b = threadIdx.x; b < r.B; b += blockDim.x) {
         const Seq s = load_seq(r, b);
-        if (!s.ok || (rows_within_len && s.n > s.len)) latch(r.err, PGD_ERR_SEQ_LEN);
+        const int end = __ldg(r.cu + b + 1);
+        const bool idle = s.row0 >= 0 && end == s.row0 && end <= r.total && s.len >= 0 &&
+                          s.len <= r.max_blocks * r.block_size;
+        if ((!s.ok && !idle) || (rows_within_len && s.n > s.len)) latch(r.err, PGD_ERR_SEQ_LEN);
     }
 }
 

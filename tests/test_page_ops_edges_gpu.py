@@ -184,3 +184,26 @@ def test_attend_windows_beyond_an_int(window):
     with pytest.raises(pgd.PagedGQAError, match="PGD_ERR_ARG"):
         pgd.paged_gqa_attend(pool, b.to(q), *b.where(), 0.1, window=-window)
     pool.close()
+
+
+def test_idle_sequences_may_be_longer_than_the_rotation_table():
+    """A sequence without new rows asks for no angle: nothing is reported for it, whatever its
+    length is; one that is longer than its table's blocks still is."""
+    b = Batch([20, 300, 30, 250], [20, 0, 30, 0], hkv=2, seed=7)
+    q, k = b.rows(4), b.rows(2)
+    rope = pgd.rope_table(30, 128)
+    pool = b.pool()
+    out = pgd.paged_qk_norm_rope_write(pool, b.to(q), b.to(k), b.to(k), *b.where(),
+                                       rope=rope.cuda())
+    assert pgd.paged_gqa_get_error(pool) == 0
+    for s in (0, 2):
+        for row, pos in ref.rows_of(b.cu, b.lens, s):
+            y, m = ref.norm_rotate(q[row], None, 0.0, rope, False, pos)
+            assert torch.all((out[row].cpu().double() - y).abs()
+                             <= 2.0 ** -8 * y.abs() + 2.0 ** -20 * m)
+    cu, table, lens = b.where()
+    lens[1] = 16 * table.shape[1] + 1
+    pgd.paged_qk_norm_rope_write(pool, b.to(q), b.to(k), b.to(k), cu, table, lens,
+                                 rope=rope.cuda())
+    assert pgd.paged_gqa_get_error(pool) == _lib.PGD_ERR_SEQ_LEN
+    pool.close()
