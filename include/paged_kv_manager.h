@@ -134,8 +134,9 @@ int paged_kv_append(pgd_pool_t pool, const void *k_new, const void *v_new,
 /*
  * Device: store K and V rows in the pages, quantised as they are written.
  *   float32 and bfloat16 pages: copies.
- *   8-bit pages, scale per KV head: code = x / k_scale[h], rounded to the nearest code
- *     (ties to even) and saturated (e4m3 +-448, int8 +-127); the scales are read only.
+ *   8-bit pages, scale per KV head: code = x / k_scale[h] (x times the rounded reciprocal),
+ *     rounded to the nearest code (ties to even) and saturated (e4m3 +-448, int8 +-127); the
+ *     scales are read only.  A scale below 2^-126 counts as 0, and scale 0 gives codes 0.
  *   8-bit pages, scale per block and KV head: the call also sets the scale of every
  *     block it writes to the largest of max|x| / 448 (127 for int8; the product with the
  *     rounded reciprocal) over the rows it
@@ -145,8 +146,8 @@ int paged_kv_append(pgd_pool_t pool, const void *k_new, const void *v_new,
  *     most half a code step each time).  A block written from slot 0 on takes its scale
  *     from this call alone.  A largest magnitude whose scale would be below 2^-126 gives
  *     scale 0 and codes 0.  The handle's scale arrays are written.
- * Infinities and NaN take no part in a block's scale; an infinity saturates (in a
- * block of scale 0 it counts as a NaN), a NaN is stored as the NaN code of e4m3 and
+ * Infinities and NaN take no part in a block's scale; an infinity saturates (where the
+ * scale is 0 it counts as a NaN), a NaN is stored as the NaN code of e4m3 and
  * as 0 in int8.
  * Slots of a call must be distinct: blocks shared by several sequences are copied
  * first (paged_kv_copy_blocks), also partly filled ones that this call adds to.

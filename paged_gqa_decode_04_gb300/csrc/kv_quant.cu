@@ -140,7 +140,11 @@ __device__ __forceinline__ constexpr float code_max() {
     return PAGE == PGD_INT8 ? 127.f : 448.f;
 }
 
-__device__ __forceinline__ float inverse(float scale) { return scale > 0.f ? 1.f / scale : 0.f; }
+// 0 for scales below the smallest normal number, whose reciprocal may be infinite (zeros would
+// become NaN).
+__device__ __forceinline__ float inverse(float scale) {
+    return scale >= kTiny ? 1.f / scale : 0.f;
+}
 
 // 8 codes of values already divided by their scale: nearest, ties to even, saturated.
 // NaN gives the NaN code of e4m3 and 0 in int8, which has none.

@@ -207,3 +207,48 @@ def test_idle_sequences_may_be_longer_than_the_rotation_table():
                                  rope=rope.cuda())
     assert pgd.paged_gqa_get_error(pool) == _lib.PGD_ERR_SEQ_LEN
     pool.close()
+
+
+@pytest.mark.parametrize("pages", ["e4m3", "int8"])
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -149, 2.0 ** -130, 2.0 ** -127])
+def test_write_scales_too_small_to_divide_by(pages, scale):
+    """A scale below the smallest normal number counts as zero: codes 0, for zeros too."""
+    b = Batch([20, 16], [20, 16], hkv=2, pages=pages)
+    k = b.rows(2)
+    k[3], k[5, 0, :7] = 0, 0
+    b.k_scale[0], b.v_scale[1] = scale, scale
+    pool = b.pool()
+    pgd.paged_kv_write(pool, b.to(k), b.to(k), *b.where())
+    assert pgd.paged_gqa_get_error(pool) == 0
+    pool.close()
+    for s in range(2):
+        for _, pos in ref.rows_of(b.cu, b.lens, s):
+            blk, slot = ref.place(b.table, 16, s, pos)
+            assert torch.all(b.dk.cpu()[blk, slot, 0].float() == 0)
+            assert torch.all(b.dv.cpu()[blk, slot, 1].float() == 0)
+            assert b.dk.cpu()[blk, slot, 1].float().isfinite().all()
+
+
+@pytest.mark.parametrize("pages", ["e4m3", "int8"])
+def test_write_behind_tokens_of_a_scale_too_small(pages):
+    """A block whose scale so far is below the smallest normal number: zero rows keep it and
+    get codes 0, others set a new one."""
+    b = Batch([20, 20], [8, 8], hkv=2, pages=pages, scales="block")
+    k = b.rows(2)
+    k[:8] = 0
+    for s in range(2):
+        b.k_scale[b.table[s, 0].long()] = 2.0 ** -140
+    pool = b.pool()
+    pgd.paged_kv_write(pool, b.to(k), b.to(k), *b.where())
+    assert pgd.paged_gqa_get_error(pool) == 0
+    pool.close()
+    got = b.dk.cpu()
+    for pos in range(12, 20):
+        blk, slot = ref.place(b.table, 16, 0, pos)
+        assert torch.all(got[blk, slot].float() == 0)
+        blk, slot = ref.place(b.table, 16, 1, pos)
+        s = b.dks.cpu()[blk].double()[:, None]
+        x = k[8 + pos - 12].double()
+        half = ref.half_step((x / s).clamp(-ref.TOP[got.dtype], ref.TOP[got.dtype]), got.dtype)
+        assert torch.all((got[blk, slot].double() * s - x).abs()
+                         <= s * half * (1 + 2.0 ** -20) + 2.0 ** -22 * x.abs())
