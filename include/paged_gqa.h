@@ -334,6 +334,7 @@ int paged_gqa_workspace_size_host(pgd_pool_t pool, int B, int q_len, int Hq, int
  *                window, total + max_blocks * block_size stays below 2^31.
  *                0: every query attends to all Lb cached tokens (window must be 0);
  *                n_b and Lb are independent
+ *   scale        logit scale, of any sign, below 2.3e38 in magnitude
  * A query that attends to nothing gets zeros.  Blocks that lie wholly before every
  * query's window are never read.  Cached keys and values are expected to be finite where a
  * query of the sequence may attend to them; slots past Lb may hold anything.

@@ -72,7 +72,8 @@ extern "C" int paged_gqa_attend(pgd_pool_t pool, const void* q, int64_t q_stride
                                 const int32_t* block_table, int max_blocks,
                                 const int32_t* seq_lens, int causal, int window, float scale,
                                 void* out, void* stream) {
-    if (!pool || Hq < 1 || window < 0 || (causal != 0 && causal != 1) || !isfinite(scale))
+    const float scale_log2 = fabsf(scale) * 1.4426950408889634f;
+    if (!pool || Hq < 1 || window < 0 || (causal != 0 && causal != 1) || !isfinite(scale_log2))
         return PGD_ERR_ARG;
     if (window > 0 && !causal) return PGD_ERR_ARG;
     const Pool& p = pool_desc(pool);
@@ -114,7 +115,7 @@ extern "C" int paged_gqa_attend(pgd_pool_t pool, const void* q, int64_t q_stride
     t.causal = causal;
     t.window = window;
     // a scale below zero turns the queries' sign, one of zero leaves no query
-    t.scale_log2 = scale != 0.f ? fabsf(scale) * 1.4426950408889634f : 1.f;
+    t.scale_log2 = scale != 0.f ? scale_log2 : 1.f;
     t.q_and = scale != 0.f ? 0xffffffffu : 0u;
     t.q_xor = scale < 0.f ? 0x80008000u : 0u;
     t.pieces = int(pieces);

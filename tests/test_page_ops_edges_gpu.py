@@ -252,3 +252,16 @@ def test_write_behind_tokens_of_a_scale_too_small(pages):
         half = ref.half_step((x / s).clamp(-ref.TOP[got.dtype], ref.TOP[got.dtype]), got.dtype)
         assert torch.all((got[blk, slot].double() * s - x).abs()
                          <= s * half * (1 + 2.0 ** -20) + 2.0 ** -22 * x.abs())
+
+
+@pytest.mark.parametrize("scale", [2.5e38, -3.4e38])
+def test_attend_refuses_scales_that_overflow(scale):
+    """Scores are held in units of log 2: a scale that is infinite there is refused."""
+    b = Batch([20], [4], hkv=1, seed=1)
+    q = torch.zeros(4, 2, 128).bfloat16().cuda()
+    pool = b.pool()
+    with pytest.raises(pgd.PagedGQAError, match="PGD_ERR_ARG"):
+        pgd.paged_gqa_attend(pool, q, *b.where(), scale)
+    largest = pgd.paged_gqa_attend(pool, q, *b.where(), 2.3e38 * np.sign(scale))
+    assert torch.equal(largest, pgd.paged_gqa_attend(pool, q, *b.where(), 0.0))
+    pool.close()
