@@ -352,9 +352,10 @@ int paged_gqa_attend(pgd_pool_t pool, const void *q, int64_t q_stride, int total
                      float scale, void *out, void *stream);
 
 /*
- * Diagnostic of the failure path: launch one thread that waits, with the
- * bounded wait the pipeline kernels use and a limit of limit_us microseconds
- * (1 .. 1e6), on a barrier nothing arrives on.  The wait gives up, latches
+ * Diagnostic of the failure path: launch one warp that waits, with the
+ * bounded waits the decode and attention kernels use and a limit of limit_us
+ * microseconds (1 .. 1e6) for each, on a barrier nothing arrives on.  The
+ * waits give up, it latches
  * PGD_ERR_TIMEOUT in the handle's error word (read it with
  * paged_gqa_get_error) and the kernel returns; nothing faults and the context
  * stays usable.  The pages have no counterpart; it tests this library.

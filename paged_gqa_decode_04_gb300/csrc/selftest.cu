@@ -1,20 +1,38 @@
 // Diagnostic: exercise the bounded-wait path of the pipeline kernels without
-// faulting anything.  One thread initialises an mbarrier that nothing will
-// ever arrive on and waits on it with the same helper the decode kernel uses,
-// but with a caller-chosen limit; when the limit passes it latches
-// PGD_ERR_TIMEOUT in the pool's error word and returns, so the context stays
-// usable and the host reads the status with paged_gqa_get_error.
+// faulting anything.  One warp initialises an mbarrier that nothing will
+// ever arrive on and waits on it with the same helpers the decode and the
+// attention kernels use, but with a caller-chosen limit for each; when all of
+// them have given up it latches PGD_ERR_TIMEOUT in the pool's error word and
+// returns, so the context stays usable and the host reads the status with
+// paged_gqa_get_error.
 #include "decode_tma.cuh"
+#include "umma.cuh"
 
 namespace pgd {
 namespace {
 
 __global__ void wait_timeout_kernel(uint64_t limit_ns, int* err) {
     __shared__ __align__(8) uint64_t bar;
+    __shared__ int gave_up[3];
     const uint32_t b = tma::smem_u32(&bar);
-    tma::mbar_init(b, 1);
-    tma::fence_barrier_init();
-    if (!tma::mbar_wait(b, 0, limit_ns)) latch_error(err, PGD_ERR_TIMEOUT);
+    if (threadIdx.x == 0) {
+        tma::mbar_init(b, 1);
+        tma::fence_barrier_init();
+        gave_up[0] = gave_up[1] = 0;
+        gave_up[2] = 1;  // as if another thread of the CTA had given up
+    }
+    __syncwarp();
+    bool came = false;
+    if (threadIdx.x == 0) {
+        came |= tma::mbar_wait(b, 0, limit_ns);
+        came |= umma::bar_wait(b, 0, &gave_up[0], limit_ns);
+        came |= umma::bar_wait(b, 0, &gave_up[2]);
+    }
+    __syncwarp();
+    came |= umma::warp_wait(b, 0, &gave_up[1], limit_ns);
+    came |= umma::warp_wait(b, 0, &gave_up[2]);
+    came |= !gave_up[0] || !gave_up[1];
+    if (!__any_sync(0xffffffffu, came) && threadIdx.x == 0) latch_error(err, PGD_ERR_TIMEOUT);
 }
 
 }  // namespace
@@ -26,7 +44,7 @@ extern "C" int paged_gqa_selftest_wait_timeout(pgd_pool_t pool, int64_t limit_us
     int prev = -1;
     if (cudaGetDevice(&prev) != cudaSuccess) return PGD_ERR_CUDA;
     if (prev != p.device && cudaSetDevice(p.device) != cudaSuccess) return PGD_ERR_CUDA;
-    pgd::wait_timeout_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>(
+    pgd::wait_timeout_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(
         (uint64_t)limit_us * 1000ull, p.err);
     const cudaError_t e = cudaGetLastError();
     if (prev != p.device) cudaSetDevice(prev);

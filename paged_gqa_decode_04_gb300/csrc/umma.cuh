@@ -36,15 +36,17 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 }
 
 // Wait for the phase of `bar` with the given parity.  False when it has not come within
-// two seconds, or when another thread of the CTA gave up (*gave_up, shared memory): the
+// `limit` ns, or when another thread of the CTA gave up (*gave_up, shared memory): the
 // caller then leaves its loop, so that the whole CTA ends.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+constexpr uint64_t kWaitLimit = 2000000000ull;
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
+                                         uint64_t limit = kWaitLimit) {
     if (bar_try(bar, parity)) return true;
     uint64_t t0, t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
     while (!bar_try(bar, parity)) {
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-        if (*gave_up || t - t0 > 2000000000ull) {
+        if (*gave_up || t - t0 > limit) {
             *gave_up = 1;
             return false;
         }
@@ -54,7 +56,8 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
 
 // The same for a whole warp.  Every lane asks and the loop goes by their vote, so that the
 // warp never diverges: one lane asking for all (measured: some 300 cycles a wait) is slower.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
+                                          uint64_t limit = kWaitLimit) {
     uint64_t t0 = 0;
     for (int i = 0;; ++i) {
         if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
@@ -62,7 +65,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
         uint64_t t;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
         if (t0 == 0) t0 = t;
-        if (__any_sync(0xffffffffu, *gave_up || t - t0 > 2000000000ull)) {
+        if (__any_sync(0xffffffffu, *gave_up || t - t0 > limit)) {
             *gave_up = 1;
             return false;
         }

@@ -1,11 +1,15 @@
 """Edges of the ragged page operators on the GPU, against their float64 definitions."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import paged_gqa_decode_04_gb300 as pgd
 from oracle import page_ops as ref
-from page_ops_cases import Batch
+from page_ops_cases import Batch, check_stored
 from paged_gqa_decode_04_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
@@ -264,4 +268,136 @@ def test_attend_refuses_scales_that_overflow(scale):
         pgd.paged_gqa_attend(pool, q, *b.where(), scale)
     largest = pgd.paged_gqa_attend(pool, q, *b.where(), 2.3e38 * np.sign(scale))
     assert torch.equal(largest, pgd.paged_gqa_attend(pool, q, *b.where(), 0.0))
+    pool.close()
+
+
+def many(B, seed, **kw):
+    """B sequences, most of them of a few tokens, with runs of sequences that have no new rows
+    at both ends and in the middle."""
+    r = np.random.default_rng(seed)
+    lens = r.integers(0, 24, size=B)
+    lens[r.integers(0, B, size=3)] = (150, 300, 90)
+    new = np.minimum(lens, r.integers(0, 6, size=B))
+    new[r.integers(0, B, size=2)] = 300
+    new = np.minimum(new, lens)
+    for lo, n in ((0, 3), (B // 2, B // 5), (B - 2, 2)):
+        new[lo:lo + n] = 0
+    return Batch(lens.tolist(), new.tolist(), bs=8, seed=seed, pad=3, **kw)
+
+
+@pytest.mark.parametrize("B", [31, 33, 64, 1030])
+@pytest.mark.parametrize("pages,scales", [("bf16", "head"), ("e4m3", "block")])
+def test_batches_of_many_sequences(B, pages, scales):
+    """Up to three rounds of the search for a row's sequence, through every operator."""
+    b = many(B, B, hkv=1, pages=pages, scales=scales)
+    rope = pgd.rope_table(300, 16)
+    q, k, v = b.rows(2), b.rows(1), b.rows(1)
+    rows = b.held_rows()
+    pool = b.pool()
+    out = pgd.paged_qk_norm_rope_write(pool, b.to(q), b.to(k), b.to(v), *b.where(),
+                                       rope=rope.cuda()).cpu().double()
+    assert pgd.paged_gqa_get_error(pool) == 0
+    want, size = {}, {}
+    for s in range(B):
+        for row, pos in ref.rows_of(b.cu, b.lens, s):
+            y, m = ref.norm_rotate(q[row], None, 0.0, rope, False, pos)
+            assert torch.all((out[row] - y).abs() <= 2.0 ** -8 * y.abs() + 2.0 ** -20 * m)
+            want[row], size[row] = ref.norm_rotate(k[row], None, 0.0, rope, False, pos)
+    check_stored(b, "k", want, size, b.dk, b.dks, 2.0 ** -20)
+    same = {r: v[r].double() for r in rows}
+    check_stored(b, "v", same, {r: y.abs() for r, y in same.items()}, b.dv, b.dvs, 0.0)
+    pool.close()
+    pool = b.pool()                                   # the pages as they were
+    pgd.paged_kv_write(pool, b.to(k), b.to(v), *b.where())
+    assert pgd.paged_gqa_get_error(pool) == 0
+    for name, x, after, sc in (("k", k, b.dk, b.dks), ("v", v, b.dv, b.dvs)):
+        want = {r: x[r].double() for r in rows}
+        check_stored(b, name, want, {r: y.abs() for r, y in want.items()}, after, sc, 0.0)
+    pool.close()
+    pool = b.pool()
+    got = pgd.paged_kv_read(pool, b.total, *b.where())
+    assert pgd.paged_gqa_get_error(pool) == 0
+    for x, p, s in zip(got, (b.k, b.v), (b.k_scale, b.v_scale)):
+        for r, y in ref.read(p, s, b.cu, b.table, b.lens).items():
+            assert torch.all((x[r].cpu().double() - y).abs() <= (2.0 ** -8 + 2.0 ** -23) * y.abs())
+    for causal in (True, False):
+        o = pgd.paged_gqa_attend(pool, b.to(q), *b.where(), 0.09, causal=causal)
+        assert pgd.paged_gqa_get_error(pool) == 0
+        check_rows(b, o, q, 0.09, causal, 0)
+    pool.close()
+
+
+@pytest.mark.parametrize("lens,new,columns", [([1500, 700], [300, 700], 0), ([2600], [3], 0),
+                                              ([900, 33], [150, 33], 8192)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 1000)])
+def test_attend_heads_of_64_over_many_tiles(lens, new, columns, causal, window):
+    """The ring of eight tiles in several turns, with and without clusters."""
+    b = Batch(lens, new, hkv=1, d=64, seed=len(lens) + columns)
+    if columns:
+        wide = torch.full((len(lens), columns - b.table.shape[1]), -1, dtype=torch.int32)
+        b.table = torch.cat([b.table, wide], 1).contiguous()
+    q = b.rows(4)
+    pool = b.pool()
+    got = pgd.paged_gqa_attend(pool, b.to(q), *b.where(), 0.125, causal=causal, window=window)
+    assert pgd.paged_gqa_get_error(pool) == 0
+    check_rows(b, got, q, 0.125, causal, window)
+    pool.close()
+
+
+CAPTURED_FIRST = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+import paged_gqa_decode_04_gb300 as pgd
+from page_ops_cases import Batch, bits
+b = Batch([300, 40], [100, 40], hkv=2, pages=%r, scales="block", seed=1)
+q, k = b.to(b.rows(8)), b.to(b.rows(2))
+pool, where = b.pool(), b.where()
+out = torch.zeros_like(q, memory_format=torch.contiguous_format)
+qo = torch.zeros_like(out)
+kv = [torch.zeros((b.total, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+rope = pgd.rope_table(300, 128, device="cuda")
+def step(s):
+    pgd.paged_qk_norm_rope_write(pool, q, k, k, *where, rope=rope, q_out=qo, stream=s)
+    pgd.paged_gqa_attend(pool, qo, *where, 0.09, out=out, stream=s)
+    pgd.paged_kv_read(pool, b.total, *where, out=kv, stream=s)
+torch.cuda.synchronize()
+g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.graph(g, stream=s):
+    step(s)
+g.replay()
+torch.cuda.synchronize()
+first = [t.clone() for t in (out, qo, *kv)]
+pool = b.pool()                                       # the pages as they were, other buffers
+step(s)
+s.synchronize()
+assert pgd.paged_gqa_get_error(pool) == 0
+for x, y in zip(first, (out, qo, *kv)):
+    assert x.abs().sum() > 0 and torch.equal(bits(x), bits(y))
+print("same")
+"""
+
+
+@pytest.mark.parametrize("pages", ["bf16", "e4m3"])
+def test_first_calls_of_a_process_are_captured(pages):
+    """The library's first calls inside a graph capture, replayed: what eager calls give."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = CAPTURED_FIRST % (os.path.dirname(here), here, pages)
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240)
+    assert res.returncode == 0 and res.stdout.strip() == "same", res.stderr[-2000:]
+
+
+def test_waits_that_run_out_leave_the_attention_usable():
+    """The attention's bounded waits give up, each by its own limit or because another thread
+    did; the status is read and cleared, and the next call is right."""
+    b = Batch([300, 40], [100, 40], hkv=2, seed=1)
+    q = b.rows(8)
+    pool = b.pool()
+    s = torch.cuda.current_stream().cuda_stream
+    for limit_us in (1, 1000):
+        assert _lib.load().paged_gqa_selftest_wait_timeout(pool.handle, limit_us, s) == 0
+        assert pgd.paged_gqa_get_error(pool) == _lib.PGD_ERR_TIMEOUT
+        got = pgd.paged_gqa_attend(pool, b.to(q), *b.where(), 0.09)
+        assert pgd.paged_gqa_get_error(pool) == 0
+        check_rows(b, got, q, 0.09, True, 0)
     pool.close()
