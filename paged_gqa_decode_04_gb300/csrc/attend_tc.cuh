@@ -23,7 +23,8 @@
 // of the CTA sees are not fetched, and V rows outside the visible range are zeroed, so that
 // nothing in an unused slot is multiplied.  A page whose block id is out of range has V
 // zeroed as well (8-bit pages: fetched from a coordinate outside the tensor, which reads zeros),
-// so that rows that do not see it stay right; those that do become NaN at the end.
+// so that rows that do not see it stay right; those that do are marked (mark_lost) and become
+// NaN at the end.
 //
 // Warps: 0-3 and 4-7 the softmax of the two blocks, 8-11 the producers, 12 and 13 issue the
 // products of one block each; 14 and 15 only round the group up to four warps, the unit
@@ -131,7 +132,7 @@ struct Layout {
     static constexpr int kScales = kRaw + (kQ8 ? kRawSlots * kRawSlot : 0);
     static constexpr int kScaleBytes = 272;
     static constexpr int kBars = kScales + (PB ? kScaleTiles * kScaleBytes : 0);
-    static constexpr int kBytes = kBars + 288 + 1024;      // and room to align to 1024
+    static constexpr int kBytes = kBars + 320 + 1024;      // and room to align to 1024
     // warps that issue copies, and the tiles' 128-byte columns they fetch one by one
     static constexpr int kProducers = kQ8 ? 2 : 4;
     static constexpr int kColumns = kQ8 ? 1 : kHalves;
@@ -168,29 +169,16 @@ __device__ __forceinline__ bool valid(const Ragged& r, int id) {
     return id >= 0 && id < r.num_blocks;
 }
 
-// A CTA that met a block id out of range: the rows of its piece that see such a page become
-// NaN.  It looks everything up again, so that nothing is held for it through the softmax, and
-// comes once all results of the cluster are written.
-template <int D>
-__device__ __forceinline__ void erase_rows(const Args& a) {
-    const int64_t unit = blockIdx.x / a.cluster, head = unit / a.pieces;
-    const int piece = a.pieces - 1 - int(unit % a.pieces);
-    const Seq s = load_seq(a.r, find_seq(a.r, piece, a.group, kRowShift, 1));
-    const int row0 = int(piece - first_piece(a.r, s.b, a.group, kRowShift, 1)) << kRowShift;
-    const int32_t* const table = a.r.table + (int64_t)s.b * a.r.max_blocks;
-    const int end = min(s.n * a.group, row0 + (1 << kRowShift));
-    for (int row = row0 + threadIdx.x; row < end; row += kThreads) {
-        const int token = row / a.group, pos = s.len - s.n + token;
+// A page, tokens [t, t + n), has a block id out of range: the rows of the piece that see it are
+// marked in `lost`, a bit a row, to become NaN.  Apart from the kernel's own code, whose loops it
+// would slow down (2048 of 8192 tokens over bfloat16 pages, 64/8 heads: 337 -> 356 us).
+__device__ __noinline__ void mark_lost(const Args& a, const Seq& s, int row0, int t, int n,
+                                       uint32_t* lost) {
+    for (int r = 0; r < 1 << kRowShift; ++r) {
+        const int pos = s.len - s.n + (row0 + r) / a.group;
         const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
         const int hi = a.causal ? pos + 1 : s.len;
-        bool bad = false;
-        for (int i = lo / a.r.block_size; lo < hi && i <= (hi - 1) / a.r.block_size; ++i)
-            bad |= !valid(a.r, __ldg(table + i));
-        if (!bad) continue;
-        const int64_t at = (s.row0 + (int64_t)token) * a.hq + head * a.group + row % a.group;
-        uint4* const out = reinterpret_cast<uint4*>(a.out + at * D);
-        for (int i = 0; i < D / 8; ++i)
-            out[i] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+        if (lo < t + n && hi > t) atomicOr(lost + r / 32, 1u << r % 32);
     }
 }
 
@@ -293,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t bar_raw = bars + 192, bar_raw_empty = bar_raw + 8 * L::kRawSlots;
     const uint32_t bar_empty = bar_full + 8 * L::kSlots;
     volatile int* const gave_up = reinterpret_cast<int*>(smem + L::kBars + 272);
-    volatile int* const bad = reinterpret_cast<int*>(smem + L::kBars + 276);
+    uint32_t* const lost = reinterpret_cast<uint32_t*>(smem + L::kBars + 288);  // of 256 rows
     uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(smem + L::kBars + 280);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -323,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(bar_empty + 8 * i, 2);
         }
         *gave_up = 0;
-        *bad = 0;
+        for (int i = 0; i < 8; ++i) lost[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
 
@@ -649,11 +637,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = T0; j < T1 && live; ++j) {
             const int next = id_of(j + 1);
             const bool ok = valid(a.r, id);
-            if (seen(j) && !ok) {
-                latch(a.r.err, PGD_ERR_BLOCK_ID);
-                *bad = 1;
-            }
             const unsigned which = __ballot_sync(0xffffffffu, ok);
+            const bool gone = seen(j) && !ok;
+            if (__any_sync(0xffffffffu, gone)) {  // rare: the warp stays together beside it
+                if (gone) {
+                    latch(a.r.err, PGD_ERR_BLOCK_ID);
+                    mark_lost(a, s, row0, j * kTile + my_page * box, box, lost);
+                }
+                __syncwarp();
+            }
             const uint32_t bytes = __popc(which) * box * 128;
             // rows no query sees, or that have no page, among this warp's copies
             const bool patch = j * kTile < lo || hi - j * kTile < kTile ||
@@ -774,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool ok = seen(j, page);
             if (ok && !valid(a.r, id)) {
                 latch(a.r.err, PGD_ERR_BLOCK_ID);
-                *bad = 1;
+                mark_lost(a, s, row0, j * kTile + page * box, box, lost);
                 id = -1;  // outside the tensor: zeros
             }
             const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * box * 128;
@@ -908,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    const bool failed = *gave_up || !s.ok;
+    const bool failed = *gave_up || !s.ok || (warp < 8 && lost[at_row / 32] >> lane & 1);
     if (*gave_up && threadIdx.x == 0) latch(a.r.err, PGD_ERR_TIMEOUT);
 
     // -------------------------------------------------------------------- results
@@ -1062,7 +1054,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_sync();  // shared memory stays until every CTA has read it
     }
     __syncthreads();
-    if (*bad) erase_rows<D>(a);
     if (warp == 12) tmem_free(tmem, 512);
 }
 
