@@ -401,3 +401,57 @@ def test_waits_that_run_out_leave_the_attention_usable():
         assert pgd.paged_gqa_get_error(pool) == 0
         check_rows(b, got, q, 0.09, True, 0)
     pool.close()
+
+
+@pytest.mark.parametrize("pages", ["bf16", "e4m3"])
+def test_prompts_and_steps_on_the_block_manager_s_tables(pages):
+    """Prompts and steps of single tokens written and attended to through the tables of the block
+    manager (a position reserved for each token), with a fork whose shared block is copied."""
+    lens, bs, blocks = [37, 5, 64], 16, 24
+    b = Batch(lens, lens, hkv=2, bs=bs, pages=pages, scales="block", seed=11)
+    shape = (blocks, bs, 2, 128)
+    b.k, b.v = torch.zeros(shape, dtype=b.k.dtype), torch.zeros(shape, dtype=b.v.dtype)
+    if pages == "e4m3":
+        b.k_scale, b.v_scale = torch.zeros(blocks, 2), torch.zeros(blocks, 2)
+    pool = b.pool()
+    kvm = pgd.KVBlockManager(blocks, bs, max_seqs=4, max_blocks_per_seq=8)
+    for s, n in enumerate(lens):
+        kvm.add_sequence(s)
+        for _ in range(n):
+            assert kvm.append_slots([s])[1] == []
+    kvm.fork(0, 3)
+    q, k, v = b.rows(8), b.rows(2), b.rows(2)
+    rope = pgd.rope_table(128, 128, device="cuda")
+
+    def step(q, k, v, cu, seqs, causal_rows):
+        table, lens = [torch.from_numpy(x) for x in kvm.block_tables(seqs)]
+        where = [cu.cuda(), table.cuda(), lens.cuda()]
+        qo = pgd.paged_qk_norm_rope_write(pool, q.cuda(), k.cuda(), v.cuda(), *where, rope=rope)
+        got = pgd.paged_gqa_attend(pool, qo, *where, 0.09)
+        assert pgd.paged_gqa_get_error(pool) == 0
+        now = [t.cpu() if t is not None else None for t in (b.dk, b.dv, b.dks, b.dvs)]
+        want, size = ref.attend(qo.cpu(), *now, cu, table, lens, 0.09, True, 0)
+        assert len(want) == causal_rows
+        for row, y in want.items():
+            tol = 2.0 ** -8 * y.abs() + (2.0 ** -8 + 2.0 ** -12) * size[row]
+            assert torch.all((got[row].cpu().double() - y).abs() <= tol)
+        return now, table, lens
+
+    step(q, k, v, b.cu, [0, 1, 2], sum(lens))
+    q, k, v = [torch.randn((4, h, 128), generator=b.g).bfloat16() for h in (8, 2, 2)]
+    slots, copies = kvm.append_slots([0, 1, 2, 3])
+    assert len(copies) == 1                              # the last block that 0 and 3 share
+    src, dst = (torch.tensor(c, dtype=torch.int32, device="cuda") for c in zip(*copies))
+    pgd.paged_kv_copy_blocks(pool, src, dst)
+    now, table, lens = step(q, k, v, torch.arange(5).int(), [0, 1, 2, 3], 4)
+    for s in range(4):                                   # the step's rows where the manager says
+        blk, slot = ref.place(table, bs, s, int(lens[s]) - 1)
+        assert blk * bs + slot == int(slots[s])
+        stored = ref.values(now[1], now[3], blk, slot)
+        # within half a step of the type, at the widest spacing of e4m3 (32 of 448)
+        most = v[s].double().abs() if now[3] is None else 16 * now[3][blk].double()[:, None]
+        assert torch.all((stored - v[s].double()).abs() <= most * (1 + 2.0 ** -20))
+        if now[3] is None:
+            assert torch.equal(stored, v[s].double())
+    kvm.close()
+    pool.close()
