@@ -136,7 +136,9 @@ int paged_kv_pool_create_fp8(pgd_pool_t *out, const void *k_pool, const void *v_
  * The other arguments and rules are those of paged_kv_pool_create_fp8
  * (head_dim 128, block_size a power of two in 8..256, bfloat16 q and out).
  * The scale arrays are read by the decode kernels at every call, so a caller
- * may rewrite a block's row between calls (stream-ordered).  Quantized KV
+ * may rewrite a block's row between calls (stream-ordered).  Like the pools,
+ * scales per block have to be writable for the calls that write tokens
+ * (paged_kv_write, paged_qk_norm_rope_write, paged_kv_copy_blocks).  Quantized KV
  * pages: int8 / fp8 quantization, "Modern LLM Inference ...", section 6;
  * "The Ultimate Guide ... Part 2", "KV Cache Compression".
  * PGD_ERR_DTYPE for another code, PGD_ERR_ARG for another granularity or a
@@ -338,11 +340,14 @@ int paged_gqa_workspace_size_host(pgd_pool_t pool, int B, int q_len, int Hq, int
  * A query that attends to nothing gets zeros.  Blocks that lie wholly before every
  * query's window are never read.  Cached keys and values are expected to be finite where a
  * query of the sequence may attend to them; slots past Lb may hold anything.
- * bfloat16 and 8-bit pools (PGD_ERR_UNSUPPORTED for float32; with 8-bit pages queries
- * stay below 65504 in magnitude and scales are not negative; with scales per head a weight
- * keeps 11 bits down to 2^-21 of the largest, then half a step of 2^-31 of that; with scales
- * per block a weight times V's scale keeps 11 bits down to 2^-17 of the largest, then 2^-28 of
- * that).  No workspace.  Sequences whose cu_seqlens or length is impossible latch
+ * bfloat16 and 8-bit pools (PGD_ERR_UNSUPPORTED for float32).  Scores, their maximum, the sum
+ * of the weights and the output are held in float32, the weights that V is multiplied with in
+ * the 16 bits of the products' operands: bfloat16, f16 over 8-bit pages.  With 8-bit pages
+ *   - queries are taken as f16: below 65504 in magnitude, in steps of 2^-24 below 2^-14;
+ *   - scales are not negative;
+ *   - a weight keeps 11 bits down to 2^-21 of the largest, then steps of 2^-31 of that; with
+ *     scales per block a weight times V's scale does down to 2^-17, then 2^-28 of that.
+ * No workspace.  Sequences whose cu_seqlens or length is impossible latch
  * PGD_ERR_SEQ_LEN, block ids out of range PGD_ERR_BLOCK_ID; the rows that would have read them
  * are written as NaN.
  */

@@ -125,7 +125,7 @@ int paged_kv_append(pgd_pool_t pool, const void *k_new, const void *v_new,
  * for float32 pools and bfloat16 for all others.  total = 0 or B = 0 does nothing.
  *
  * A sequence with an impossible length (cu_seqlens descending or past total, seq_lens
- * outside [0, max_blocks * block_size], more rows than cached tokens, a position past
+ * outside [0, max_blocks * block_size], more rows than cached tokens, a row's position past
  * the rotation table) latches PGD_ERR_SEQ_LEN: none of its tokens is stored and its
  * output rows are NaN.  A block id outside [0, num_blocks) latches PGD_ERR_BLOCK_ID:
  * the tokens of that block are not stored, or read back as NaN.
@@ -139,9 +139,9 @@ int paged_kv_append(pgd_pool_t pool, const void *k_new, const void *v_new,
  *     scales are read only.  A scale below 2^-126 counts as 0, and scale 0 gives codes 0.
  *   8-bit pages, scale per block and KV head: the call also sets the scale of every
  *     block it writes to the largest of max|x| / 448 (127 for int8; the product with the
- *     rounded reciprocal) over the rows it
- *     stores there and, where the block already holds earlier tokens of the sequence
- *     (the first row is not at slot 0), the block's scale before the call.  If that
+ *     rounded reciprocal) over the rows it stores there and, where the block already holds
+ *     earlier tokens of the sequence (the first row is not at slot 0), the block's scale
+ *     before the call.  If that
  *     grows the scale, the earlier tokens' codes are rounded again at the new scale (at
  *     most half a code step each time).  A block written from slot 0 on takes its scale
  *     from this call alone.  A largest magnitude whose scale would be below 2^-126 gives

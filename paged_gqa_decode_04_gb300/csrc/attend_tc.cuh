@@ -4,7 +4,8 @@
 //     O += P V,   l += sum of P,   out = O / l
 //
 // with S and O in float32 in TMEM, m and l in float32 in registers and P rounded to 16
-// bits, the type the product takes (at most half a step, 2^-8 in bfloat16, of each weight).
+// bits, the type the product takes (at most half a step of each weight, 2^-8 in bfloat16 and
+// 2^-11 in f16 over 8-bit pages); l is the sum of the weights before they are rounded.
 //
 // Rows.  The G query heads of a KV head see the same keys, so a CTA takes 256 consecutive
 // rows (token, head of the group) of one sequence and KV head: a key tile is fetched once
@@ -49,18 +50,19 @@
 // constants of the CTA.  Scales per block go where a float32 value is at hand anyway, K's on
 // the scores and V's into the exponent of the weights (the row's sum takes them out again):
 // multiplied into V while it is widened they cost 5% of the whole (2048 of 8192 tokens, 64/8
-// heads: 489 against 465 us; now 445, 402 with scales per head, 337 over bfloat16).
+// heads: 489 against 465 us; now 446, 396 with scales per head, 338 over bfloat16).
 //
 // What bounds it.  At D = 128 a tile of one block is 2 x 8 products of 64 cycles (1024), and
 // each of its four softmax warps, one in every quarter of the SM, has 128 exponentials of
 // 4.07 cycles (521), about 900 cycles with the maxima, sums and conversions; the two blocks'
 // warps of a quarter together take 1500.  So the softmax hides behind the products of both
 // blocks (2048 cycles) with little to spare.  Measured (bfloat16, 64/8 heads, 2048 queries):
-// of 32768 tokens 1357 us, 1.57 PFLOP/s, 81% of a library product's burst (1260 us and 88%
-// before the clock drops under the load); of 8192 tokens 337 us with the tensor cores busy 60%
+// of 32768 tokens 1364 us, 1.56 PFLOP/s, 81% of a library product's burst (1265 us and 87%
+// before the clock drops under the load); of 8192 tokens 338 us with the tensor cores busy 61%
 // of the time, since a CTA's search, query load, first tile and epilogue (some 10 us) are not
 // hidden and causal pieces end unevenly.  Over 8-bit pages the widening warps share the issue slots
-// with the softmax: 44% (scales per block).
+// with the softmax: 44% (scales per block).  ptxas spills 104 bytes of stores and 248 of loads
+// over bfloat16 pages, 180 and 416 to 200 and 464 over 8-bit ones.
 //
 // Every wait is bounded; one that gives up latches PGD_ERR_TIMEOUT and ends the CTA.
 #pragma once

@@ -290,7 +290,8 @@ def paged_gqa_attend(pool, q, cu_seqlens, block_table, seq_lens, scale, causal=T
     cached tokens and attend to what comes before them (the `window` most recent
     tokens when window > 0): prompts and chunks of prompts.  Not causal: every query
     attends to all seq_lens[b] cached tokens: cross attention.  Returns out
-    [total, Hq, D]; rows past cu_seqlens[B] are left as they were.
+    [total, Hq, D]; rows past cu_seqlens[B] are left as they were.  Sums are float32, the
+    weights that V is multiplied with bfloat16 (f16 over 8-bit pages, see paged_gqa.h).
     """
     B = _check_tables(pool, cu_seqlens, block_table, seq_lens)
     if q.dim() != 3:
