@@ -357,6 +357,74 @@ int paged_gqa_attend(pgd_pool_t pool, const void *q, int64_t q_stride, int total
                      float scale, void *out, void *stream);
 
 /*
+ * Attention with shaped scores: paged_gqa_attend and paged_gqa_decode_ex with three more
+ * arguments.  The score of token t for the query at position p in head h is
+ *
+ *     s = scale * <q, k_t>
+ *     s = softcap * tanh(s / softcap)      where softcap > 0
+ *     s = s - slopes[h] * |p - t|          where slopes is not NULL
+ *
+ * with p as in the plain call: Lb - n_b + i for query i of the n_b of a sequence (causal or
+ * not), Lb - q_len + i in a decode.
+ *   softcap      0 (none) or 2^-64 .. 2^64
+ *   slopes       [Hq] float32, device, 4-byte aligned, finite, or NULL.  Scores and bias are
+ *                summed in float32, in units of log 2: a bias of 2^k natural units has steps
+ *                of about 2^(k-23)
+ *   visible      (attend) [total][2] int32, device, 8-byte aligned, or NULL: the row sees
+ *                tokens [first, end) of its sequence alone, of those that causality and the
+ *                window let it see.  Packed documents: where a row's document begins and ends;
+ *                a prefix that every row sees: [0, max(p + 1, prefix)) with causal = 0.  Any
+ *                values are fine; a row that sees nothing gets zeros.  Between the first and
+ *                the last token that rows of a sequence see, its cached keys and values are
+ *                expected to be finite and its block ids valid
+ * With softcap 0, slopes NULL and visible NULL these are the plain calls.  Checks, errors,
+ * workspace (decode: paged_gqa_workspace_size_ex) and everything else are theirs; the decode
+ * also serves float32 pools (q_len 1, no window).
+ */
+int paged_gqa_attend_shaped(pgd_pool_t pool, const void *q, int64_t q_stride, int total, int Hq,
+                            const int32_t *cu_seqlens, int B, const int32_t *block_table,
+                            int max_blocks, const int32_t *seq_lens, int causal, int window,
+                            float scale, float softcap, const float *slopes,
+                            const int32_t *visible, void *out, void *stream);
+
+int paged_gqa_decode_shaped(pgd_pool_t pool, const void *q, int B, int q_len, int Hq,
+                            const int32_t *block_table, int max_blocks, const int32_t *seq_lens,
+                            int window, float scale, float softcap, const float *slopes,
+                            void *out, void *workspace, size_t workspace_bytes, int num_splits,
+                            void *stream);
+
+/*
+ * paged_gqa_decode_ex (window 0) for sequences that share prefixes in groups, as forks of one
+ * prompt do: a group's prefix is read once for all its sequences.
+ *   cu_groups    [num_groups + 1] int32: sequences cu_groups[g] .. cu_groups[g+1] - 1 are group
+ *                g (ascending, within 0 .. B; sequences of no group are read whole)
+ *   shared_lens  [num_groups] int32: the first shared_lens[g] cached tokens of group g's
+ *                sequences are the same (0: nothing is shared).  They are read through the
+ *                table row of one sequence of the group, in whole blocks, and only as far as
+ *                every query of the group sees them; sequences of length 0 do not count.  The
+ *                other rows' entries for those blocks may be the same blocks (forks) or equal
+ *                copies, and are not read
+ *   softcap,
+ *   slopes       as in paged_gqa_decode_shaped; 0 and NULL for plain scores
+ *   workspace    paged_gqa_workspace_size_shared bytes (at least), 256-byte aligned,
+ *                zero-filled before first use; calls that may overlap need distinct ones
+ * The result is that of paged_gqa_decode_ex beyond float32 rounding.  Groups that do not ascend
+ * within the batch or a negative shared length latch PGD_ERR_SEQ_LEN, and every sequence is
+ * then read whole.  A block id out of range in a shared prefix makes the rows of its whole
+ * group NaN.  bfloat16 and 8-bit pools (PGD_ERR_UNSUPPORTED for float32); over 8-bit pages the
+ * limits of paged_gqa_attend hold for the prefix.  Three kernel launches.
+ */
+int paged_gqa_decode_shared(pgd_pool_t pool, const void *q, int B, int q_len, int Hq,
+                            const int32_t *cu_groups, const int32_t *shared_lens, int num_groups,
+                            const int32_t *block_table, int max_blocks, const int32_t *seq_lens,
+                            float scale, float softcap, const float *slopes, void *out,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes for paged_gqa_decode_shared with num_groups groups. */
+int paged_gqa_workspace_size_shared(pgd_pool_t pool, int B, int q_len, int Hq, int num_groups,
+                                    size_t *bytes);
+
+/*
  * Diagnostic of the failure path: launch one warp that waits, with the
  * bounded waits the decode and attention kernels use and a limit of limit_us
  * microseconds (1 .. 1e6) for each, on a barrier nothing arrives on.  The

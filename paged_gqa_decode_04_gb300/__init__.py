@@ -12,9 +12,10 @@ import torch
 
 from . import _lib
 from ._lib import PagedGQAError, STATUS_NAMES, strerror  # noqa: F401
-from .kv_cache import (KVBlockManager, paged_gqa_attend, paged_kv_append,  # noqa: F401
-                       paged_kv_copy_blocks, paged_kv_read, paged_kv_write,
-                       paged_qk_norm_rope_write, rope_table)
+from .kv_cache import (KVBlockManager, alloc_workspace_shared, paged_gqa_attend,  # noqa: F401
+                       paged_gqa_decode_shared, paged_gqa_workspace_size_shared,
+                       paged_kv_append, paged_kv_copy_blocks, paged_kv_read, paged_kv_write,
+                       paged_qk_norm_rope_write, rope_table, _slopes_ptr)
 
 __all__ = [
     "PagedKVPool", "PagedGQAError", "paged_kv_pool_create", "paged_kv_pool_destroy",
@@ -24,7 +25,8 @@ __all__ = [
     "paged_gqa_decode_host", "paged_gqa_workspace_size_host", "paged_gqa_plan",
     "strerror", "decode", "KVBlockManager", "paged_kv_append", "paged_kv_copy_blocks",
     "paged_kv_write", "paged_kv_read", "paged_qk_norm_rope_write", "rope_table",
-    "paged_gqa_attend",
+    "paged_gqa_attend", "paged_gqa_decode_shared", "paged_gqa_workspace_size_shared",
+    "alloc_workspace_shared",
 ]
 
 _DTYPES = {torch.float32: _lib.PGD_F32, torch.bfloat16: _lib.PGD_BF16}
@@ -205,12 +207,14 @@ def paged_gqa_workspace_size_ex(pool, B, q_len, Hq, num_splits=0):
 
 
 def paged_gqa_decode_ex(pool, q, block_table, seq_lens, scale, window=0, out=None,
-                        workspace=None, num_splits=0, stream=None):
+                        workspace=None, num_splits=0, stream=None, softcap=0.0, slopes=None):
     """Several query tokens per sequence and an optional window.
 
     q [B, q_len, Hq, D] (bf16): the last q_len cached tokens of each sequence,
     each attending causally to the positions before it, or only to the
     `window` most recent ones when window > 0.  Returns out [B, q_len, Hq, D].
+    Shaped scores: softcap > 0 takes s to softcap * tanh(s / softcap), slopes [Hq] float32
+    then subtract slopes[h] * distance.
     """
     lib = _lib.load()
     _check_decode_args(pool, q, block_table, seq_lens, 4)
@@ -220,11 +224,13 @@ def paged_gqa_decode_ex(pool, q, block_table, seq_lens, scale, window=0, out=Non
     if workspace is None:
         nbytes = paged_gqa_workspace_size_ex(pool, B, q_len, Hq, num_splits)
         workspace = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=q.device)
-    _check(lib.paged_gqa_decode_ex(pool.handle, q.data_ptr(), B, q_len, Hq,
-                                   block_table.data_ptr(), block_table.shape[1],
-                                   seq_lens.data_ptr(), int(window), float(scale),
-                                   out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                   int(num_splits), _stream_handle(stream)), "paged_gqa_decode_ex")
+    _check(lib.paged_gqa_decode_shaped(pool.handle, q.data_ptr(), B, q_len, Hq,
+                                       block_table.data_ptr(), block_table.shape[1],
+                                       seq_lens.data_ptr(), int(window), float(scale),
+                                       float(softcap), _slopes_ptr(pool, slopes, Hq),
+                                       out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                       int(num_splits), _stream_handle(stream)),
+           "paged_gqa_decode_ex")
     return out
 
 

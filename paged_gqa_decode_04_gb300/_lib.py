@@ -73,6 +73,15 @@ def load(path=LIB_PATH):
     lib.paged_gqa_decode_ex.argtypes = [vp, vp, i32, i32, i32, vp, i32, vp, i32, ctypes.c_float,
                                         vp, vp, sz, i32, vp]
     lib.paged_gqa_decode_ex.restype = i32
+    lib.paged_gqa_decode_shaped.argtypes = [vp, vp, i32, i32, i32, vp, i32, vp, i32,
+                                            ctypes.c_float, ctypes.c_float, vp, vp, vp, sz, i32,
+                                            vp]
+    lib.paged_gqa_decode_shaped.restype = i32
+    lib.paged_gqa_decode_shared.argtypes = [vp, vp, i32, i32, i32, vp, vp, i32, vp, i32, vp,
+                                            ctypes.c_float, ctypes.c_float, vp, vp, vp, sz, vp]
+    lib.paged_gqa_decode_shared.restype = i32
+    lib.paged_gqa_workspace_size_shared.argtypes = [vp, i32, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.paged_gqa_workspace_size_shared.restype = i32
     lib.paged_gqa_workspace_size_ex.argtypes = [vp, i32, i32, i32, i32, ctypes.POINTER(sz)]
     lib.paged_gqa_workspace_size_ex.restype = i32
     lib.paged_gqa_decode_noalloc.argtypes = [vp, vp, i32, i32, vp, i32, vp, ctypes.c_float, vp,
@@ -113,8 +122,10 @@ def load(path=LIB_PATH):
          i32, i32] + rag[1:] + [vp])
     lib.paged_gqa_attend.argtypes = ([vp, vp, i64, i32, i32] + rag[1:] +
                                      [i32, i32, ctypes.c_float, vp, vp])
+    lib.paged_gqa_attend_shaped.argtypes = ([vp, vp, i64, i32, i32] + rag[1:] +
+                                            [i32, i32] + [ctypes.c_float] * 2 + [vp] * 4)
     for name in ("paged_kv_write", "paged_kv_read", "paged_qk_norm_rope_write",
-                 "paged_gqa_attend"):
+                 "paged_gqa_attend", "paged_gqa_attend_shaped"):
         getattr(lib, name).restype = i32
     for name in ("pgd_kvm_create", "pgd_kvm_destroy", "pgd_kvm_add_sequence", "pgd_kvm_fork",
                  "pgd_kvm_free_sequence", "pgd_kvm_append_slots", "pgd_kvm_block_tables",

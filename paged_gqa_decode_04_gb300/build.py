@@ -24,7 +24,11 @@ SOURCES = ["api.cpp", "block_manager.cpp", "decode_simple.cu", "decode_tma_d64.c
            "decode_tma_fp8pb.cu", "decode_tma_fp8pb_share.cu", "decode_tma_fp8pb_sep.cu",
            "decode_tma_i8pb.cu", "decode_tma_i8pb_share.cu", "decode_tma_i8pb_sep.cu",
            "kv_write.cu", "kv_quant.cu", "kv_read.cu", "attend.cu", "merge.cu", "noalloc.cu",
-           "selftest.cu"]
+           "selftest.cu", "decode_ex.cu", "shared.cu"]
+# shaped scores and shared prefixes, by page type
+SOURCES += ["%s_%s.cu" % (stem, page) if stem != "decode_tma" else "decode_tma_%s_ex.cu" % page
+            for page in ("d64", "d128", "fp8", "fp8pb", "i8", "i8pb")
+            for stem in ("attend_shaped", "decode_tma")]
 
 
 def nvcc():

@@ -8,6 +8,7 @@
 #include <new>
 
 #include "page_maps.h"
+#include "page_ops.h"
 #include "paged_kv_manager.h"
 #include "pgd_internal.h"
 
@@ -21,11 +22,6 @@ namespace pgd {
 namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// 8-bit pages (either code)
-bool is_q8(int dtype) { return dtype == PGD_FP8_E4M3 || dtype == PGD_INT8; }
-
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Make `dev` current for the scope of a call; restore the caller's device.
 struct DeviceGuard {
@@ -107,11 +103,11 @@ bool encode_row_map(CUtensorMap* map, const void* base, int64_t num_blocks, int 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
 int resolve_parts(const Pool& p, int num_splits) {
     return num_splits > 0 ? num_splits : p.num_sms;
 }
-
-}  // namespace
 
 const Pool& pool_desc(pgd_pool_t h) { return h->p; }
 const PageMaps& page_maps(pgd_pool_t h) { return h->maps; }
@@ -212,6 +208,52 @@ int check_decode(const Pool& p, const void* q, int B, int q_len, int Hq,
     *wl = workspace_layout(B, p.hkv, q_len * (Hq / p.hkv), plan->hg, p.d, plan->parts);
     if (!aligned(workspace, 256) || workspace_bytes < wl->total) return PGD_ERR_WORKSPACE;
     return PGD_OK;
+}
+
+DecodeArgs decode_args(const Pool& p, const void* q, int B, int q_len, int Hq,
+                       const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
+                       int window, float scale, float softcap, const float* slopes, void* out,
+                       void* workspace, int num_splits, const Plan& plan,
+                       const WorkspaceLayout& wl) {
+    DecodeArgs a;
+    memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.k_pool = p.k;
+    a.v_pool = p.v;
+    a.out = out;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.B = B;
+    a.q_len = q_len;
+    a.window = window;
+    a.hq = Hq;
+    a.hkv = p.hkv;
+    a.group = Hq / p.hkv;
+    a.d = p.d;
+    a.block_size = p.block_size;
+    a.max_blocks = max_blocks;
+    a.num_blocks = p.num_blocks;
+    a.scale_log2 = scale * kLog2e;
+    a.k_scale = p.k_scale;
+    a.v_scale = p.v_scale;
+    a.scale_per_block = p.scale_per_block;
+    a.num_parts = plan.parts;
+    a.auto_parts = num_splits == 0;
+    a.hg = plan.hg;
+    a.units = p.hkv / plan.hg;
+    a.tile_tokens = plan.tile_tokens;
+    a.run_cost = p.dtype == PGD_F32 ? 0 : kRunCostTiles;  // the float32 path's merge kernel: 0
+    a.err = p.err;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.counters = reinterpret_cast<int*>(ws + wl.counters_off);
+    a.merge_variant = plan.merge_variant == 3 ? 0 : plan.merge_variant;
+    a.tile_base = reinterpret_cast<int64_t*>(ws + wl.tile_base_off);
+    a.part_lse = reinterpret_cast<float*>(ws + wl.part_lse_off);
+    a.part_o = reinterpret_cast<float*>(ws + wl.part_o_off);
+    a.cap = softcap * kLog2e;
+    a.cap_inv = softcap > 0.f ? 1.f / a.cap : 0.f;
+    a.slopes = slopes;
+    return a;
 }
 
 }  // namespace pgd
@@ -359,78 +401,48 @@ int paged_gqa_workspace_size(pgd_pool_t pool, int B, int Hq, int num_splits, siz
 }
 
 namespace {
-// The decode of paged_gqa_decode_ex; out_on_host: `out` is host memory written
-// through its mapped address (paged_gqa_decode_host), where the merge stays
+// The decode of paged_gqa_decode_ex and paged_gqa_decode_shaped; out_on_host: `out` is host
+// memory written through its mapped address (paged_gqa_decode_host), where the merge stays
 // fused in the decode kernel (a second kernel's writes would cross the host
 // link after the first one's: measured slower end to end).
 int decode_ex_impl(pgd_pool_t pool, const void* q, int B, int q_len, int Hq,
                    const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
-                   int window, float scale, void* out, void* workspace, size_t workspace_bytes,
-                   int num_splits, void* stream, bool out_on_host) {
+                   int window, float scale, float softcap, const float* slopes, void* out,
+                   void* workspace, size_t workspace_bytes, int num_splits, void* stream,
+                   bool out_on_host) {
     if (!pool) return PGD_ERR_ARG;
     const Pool& p = pool->p;
     Plan plan;
     WorkspaceLayout wl;
     {
-        const int rc = check_decode(p, q, B, q_len, Hq, block_table, max_blocks, seq_lens, window,
-                                    scale, out, workspace, workspace_bytes, num_splits, &plan,
-                                    &wl);
+        int rc = check_shaping(softcap, slopes);
+        if (rc != PGD_OK) return rc;
+        rc = check_decode(p, q, B, q_len, Hq, block_table, max_blocks, seq_lens, window, scale,
+                          out, workspace, workspace_bytes, num_splits, &plan, &wl);
         if (rc != PGD_OK) return rc;
     }
     if (B == 0) return PGD_OK;
     if (out_on_host && plan.merge_variant == 2) plan.merge_variant = 0;
-    const int G = Hq / p.hkv;
-    const int parts = plan.parts;
-    const int hg = plan.hg;
 
     DeviceGuard g(p.device);
     if (!g.ok) return PGD_ERR_CUDA;
-
-    DecodeArgs a;
-    memset(&a, 0, sizeof(a));
-    a.q = q;
-    a.k_pool = p.k;
-    a.v_pool = p.v;
-    a.out = out;
-    a.block_table = block_table;
-    a.seq_lens = seq_lens;
-    a.B = B;
-    a.q_len = q_len;
-    a.window = window;
-    a.hq = Hq;
-    a.hkv = p.hkv;
-    a.group = G;
-    a.d = p.d;
-    a.block_size = p.block_size;
-    a.max_blocks = max_blocks;
-    a.num_blocks = p.num_blocks;
-    a.scale_log2 = scale * 1.4426950408889634f;
-    a.k_scale = p.k_scale;
-    a.v_scale = p.v_scale;
-    a.scale_per_block = p.scale_per_block;
-    a.num_parts = parts;
-    a.auto_parts = num_splits == 0;
-    a.hg = hg;
-    a.units = p.hkv / hg;
-    a.tile_tokens = plan.tile_tokens;
-    a.run_cost = p.dtype == PGD_F32 ? 0 : kRunCostTiles;  // the float32 path's merge kernel: 0
-    a.err = p.err;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    a.counters = reinterpret_cast<int*>(ws + wl.counters_off);
-    a.merge_variant = plan.merge_variant == 3 ? 0 : plan.merge_variant;
-    a.tile_base = reinterpret_cast<int64_t*>(ws + wl.tile_base_off);
-    a.part_lse = reinterpret_cast<float*>(ws + wl.part_lse_off);
-    a.part_o = reinterpret_cast<float*>(ws + wl.part_o_off);
-
+    DecodeArgs a = decode_args(p, q, B, q_len, Hq, block_table, max_blocks, seq_lens, window,
+                               scale, softcap, slopes, out, workspace, num_splits, plan, wl);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (p.dtype != PGD_F32) {
+    if (p.dtype == PGD_F32) {
+        if (launch_decode_simple(a, p.dtype, s) != cudaSuccess) return PGD_ERR_CUDA;
+        if (launch_merge(a, p.dtype, s) != cudaSuccess) return PGD_ERR_CUDA;
+    } else if (softcap > 0.f || slopes) {
+        // where the plain decode shares or separates its merge the runs are long or many:
+        // joined by a second kernel
+        a.join = a.merge_variant != 0;
+        if (launch_decode_ex(a, p, s) != cudaSuccess) return PGD_ERR_CUDA;
+        if (a.join && launch_join(a, s) != cudaSuccess) return PGD_ERR_CUDA;
+    } else {
         // the TMA kernel merges split runs itself, except in the separate-merge
         // variant, whose partials a second kernel merges over all SMs
         if (launch_decode_tma(a, p, s) != cudaSuccess) return PGD_ERR_CUDA;
         if (a.merge_variant == 2 && launch_merge_runs(a, s) != cudaSuccess) return PGD_ERR_CUDA;
-    } else {
-        if (launch_decode_simple(a, p.dtype, s) != cudaSuccess) return PGD_ERR_CUDA;
-        if (launch_merge(a, p.dtype, s) != cudaSuccess) return PGD_ERR_CUDA;
     }
     return PGD_OK;
 }
@@ -441,7 +453,18 @@ int paged_gqa_decode_ex(pgd_pool_t pool, const void* q, int B, int q_len, int Hq
                         int window, float scale, void* out, void* workspace,
                         size_t workspace_bytes, int num_splits, void* stream) {
     return decode_ex_impl(pool, q, B, q_len, Hq, block_table, max_blocks, seq_lens, window, scale,
-                          out, workspace, workspace_bytes, num_splits, stream, false);
+                          0.f, nullptr, out, workspace, workspace_bytes, num_splits, stream,
+                          false);
+}
+
+int paged_gqa_decode_shaped(pgd_pool_t pool, const void* q, int B, int q_len, int Hq,
+                            const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
+                            int window, float scale, float softcap, const float* slopes,
+                            void* out, void* workspace, size_t workspace_bytes, int num_splits,
+                            void* stream) {
+    return decode_ex_impl(pool, q, B, q_len, Hq, block_table, max_blocks, seq_lens, window, scale,
+                          softcap, slopes, out, workspace, workspace_bytes, num_splits, stream,
+                          false);
 }
 
 int paged_gqa_decode(pgd_pool_t pool, const void* q, int B, int Hq, const int32_t* block_table,
@@ -534,8 +557,8 @@ int paged_gqa_decode_host(pgd_pool_t pool, const void* h_q, int B, int q_len, in
     const bool copy_out = out == nullptr;
     if (copy_out) out = ws + hl.out_off;
     rc = decode_ex_impl(pool, q, B, q_len, Hq, static_cast<const int32_t*>(bt), max_blocks,
-                        static_cast<const int32_t*>(sl), window, scale, out, workspace, dec,
-                        num_splits, stream, !copy_out);
+                        static_cast<const int32_t*>(sl), window, scale, 0.f, nullptr, out,
+                        workspace, dec, num_splits, stream, !copy_out);
     if (rc != PGD_OK) return rc;
     if (copy_out && cudaMemcpyAsync(h_out, out, hl.io_bytes, cudaMemcpyDefault, s) != cudaSuccess)
         return PGD_ERR_CUDA;

@@ -1,4 +1,4 @@
-// paged_gqa_attend: attention of a ragged batch of query tokens over the pages,
+// paged_gqa_attend, paged_gqa_attend_shaped: attention of a ragged batch of query tokens over the pages,
 // causal (prompts, chunks of prompts) or over all cached tokens (cross attention).
 // See include/paged_gqa.h for the contract.
 //
@@ -6,85 +6,55 @@
 //
 // in one pass over the tokens with a running maximum and sum in float32, on the tensor
 // cores: attend_tc.cuh.  This file checks the arguments and chooses the launch.
-#include <atomic>
-
-#include "attend_plan.h"
-#include "attend_tc.cuh"
-#include "page_maps.h"
+#include "attend_launch.cuh"
 #include "page_ops.h"
 #include "ragged.cuh"
 
 namespace pgd {
-namespace {
+namespace attend {
+#define PGD_EXTERN(D, PAGE, PB)                                                              \
+    extern template cudaError_t launch_shaped<D, PAGE, PB>(Args&, const Pool&, const PageMaps&, \
+                                                           cudaStream_t);
+PGD_ATTEND_PAGES(PGD_EXTERN)
+#undef PGD_EXTERN
 
-template <int D, int PAGE, bool PB>
-cudaError_t launch(attend::Args& a, const Pool& p, const PageMaps& maps, cudaStream_t s) {
-    using namespace attend;
-    constexpr int kDevices = 64;
-    static std::atomic<uint64_t> fits[kDevices];  // 16 bits a cluster size, 0: not asked yet
-    if (p.device < 0 || p.device >= kDevices) return cudaErrorInvalidDevice;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Layout<D, PAGE, PB>::kBytes;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    uint64_t known = fits[p.device].load();
-    if (!known) {
-        cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, PAGE, PB>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Layout<D, PAGE, PB>::kBytes);
-        if (e != cudaSuccess) return e;
-        known = p.num_sms;
-        for (int i = 1; i < 4; ++i) {
-            int n = 0;
-            attr[0].val.clusterDim.x = 1 << i;
-            cfg.gridDim = dim3(1 << i);
-            cfg.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&n, attend_kernel<D, PAGE, PB>, &cfg);
-            if (e != cudaSuccess) return e;
-            known |= uint64_t(n) << (16 * i);
-        }
-        fits[p.device].store(known);
-    }
-    int fit[4];
-    for (int i = 0; i < 4; ++i) fit[i] = int(known >> (16 * i) & 0xffff);
-    const bool few = (int64_t)a.r.total * a.group <= (int64_t)a.pieces * kBlock;
-    // us of a key tile of 256 rows (measured at D = 128)
-    const double tile = PAGE == PGD_BF16 ? 1.2 : PB ? 1.75 : 1.5;
-    a.cluster = choose_cluster(fit, (int64_t)a.pieces * a.hkv,
-                               piece_tiles(a.r.max_len, a.window, a.group), few, tile);
-    attr[0].val.clusterDim.x = a.cluster;
-    cfg.gridDim = dim3(unsigned(a.pieces) * a.hkv * a.cluster);
-    cfg.numAttrs = a.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attend_kernel<D, PAGE, PB>, a, maps.k, maps.v);
+cudaError_t launch_attend(Args& a, const Pool& p, const PageMaps& maps, bool shaped,
+                          cudaStream_t s) {
+#define PGD_LAUNCH(D, PAGE, PB)                                                              \
+    if (p.d == D && p.dtype == PAGE && (p.dtype == PGD_BF16 || (p.scale_per_block != 0) == PB)) \
+        return shaped ? launch_shaped<D, PAGE, PB>(a, p, maps, s)                            \
+                      : launch<D, PAGE, PB, 0>(a, p, maps, s);
+    PGD_ATTEND_PAGES(PGD_LAUNCH)
+#undef PGD_LAUNCH
+    return cudaErrorInvalidValue;
 }
-
-}  // namespace
+}  // namespace attend
 }  // namespace pgd
 
 using namespace pgd;
 
-extern "C" int paged_gqa_attend(pgd_pool_t pool, const void* q, int64_t q_stride, int total,
-                                int Hq, const int32_t* cu_seqlens, int B,
-                                const int32_t* block_table, int max_blocks,
-                                const int32_t* seq_lens, int causal, int window, float scale,
-                                void* out, void* stream) {
+extern "C" int paged_gqa_attend_shaped(pgd_pool_t pool, const void* q, int64_t q_stride,
+                                       int total, int Hq, const int32_t* cu_seqlens, int B,
+                                       const int32_t* block_table, int max_blocks,
+                                       const int32_t* seq_lens, int causal, int window,
+                                       float scale, float softcap, const float* slopes,
+                                       const int32_t* visible, void* out, void* stream) {
     const float scale_log2 = fabsf(scale) * 1.4426950408889634f;
     if (!pool || Hq < 1 || window < 0 || (causal != 0 && causal != 1) || !isfinite(scale_log2))
         return PGD_ERR_ARG;
     if (window > 0 && !causal) return PGD_ERR_ARG;
+    int rc = check_shaping(softcap, slopes);
+    if (rc != PGD_OK) return rc;
     const Pool& p = pool_desc(pool);
     if (Hq % p.hkv != 0) return PGD_ERR_SHAPE;
     if (p.dtype == PGD_F32) return PGD_ERR_UNSUPPORTED;
-    int rc = check_ragged(p, total, cu_seqlens, B, block_table, max_blocks, seq_lens);
+    rc = check_ragged(p, total, cu_seqlens, B, block_table, max_blocks, seq_lens);
     if (rc != PGD_OK || B == 0 || total == 0) return rc;
     const int64_t width = (int64_t)Hq * p.d;
     rc = check_rows(q, q_stride, width, 2);
     if (rc == PGD_OK) rc = check_rows(out, width, width, 2);
     if (rc != PGD_OK) return rc;
+    if (visible && !is_aligned(visible, 8)) return PGD_ERR_ALIGN;
     {
         const char* q0 = static_cast<const char*>(q);
         const char* o0 = static_cast<char*>(out);
@@ -121,16 +91,21 @@ extern "C" int paged_gqa_attend(pgd_pool_t pool, const void* q, int64_t q_stride
     t.pieces = int(pieces);
     t.k_scale = p.k_scale;
     t.v_scale = p.v_scale;
-    const PageMaps& maps = page_maps(pool);
-    cudaError_t e;
-    if (p.dtype == PGD_BF16)
-        e = p.d == 64 ? launch<64, PGD_BF16, false>(t, p, maps, s)
-                      : launch<128, PGD_BF16, false>(t, p, maps, s);
-    else if (p.dtype == PGD_FP8_E4M3)
-        e = p.scale_per_block ? launch<128, PGD_FP8_E4M3, true>(t, p, maps, s)
-                              : launch<128, PGD_FP8_E4M3, false>(t, p, maps, s);
-    else
-        e = p.scale_per_block ? launch<128, PGD_INT8, true>(t, p, maps, s)
-                              : launch<128, PGD_INT8, false>(t, p, maps, s);
+    t.cap = softcap * kLog2e;
+    t.cap_inv = softcap > 0.f ? 1.f / t.cap : 0.f;
+    t.slopes = slopes;
+    t.visible = reinterpret_cast<const int2*>(visible);
+    const bool shaped = softcap > 0.f || slopes || visible;
+    const cudaError_t e = attend::launch_attend(t, p, page_maps(pool), shaped, s);
     return e == cudaSuccess ? PGD_OK : PGD_ERR_CUDA;
+}
+
+extern "C" int paged_gqa_attend(pgd_pool_t pool, const void* q, int64_t q_stride, int total,
+                                int Hq, const int32_t* cu_seqlens, int B,
+                                const int32_t* block_table, int max_blocks,
+                                const int32_t* seq_lens, int causal, int window, float scale,
+                                void* out, void* stream) {
+    return paged_gqa_attend_shaped(pool, q, q_stride, total, Hq, cu_seqlens, B, block_table,
+                                   max_blocks, seq_lens, causal, window, scale, 0.f, nullptr,
+                                   nullptr, out, stream);
 }

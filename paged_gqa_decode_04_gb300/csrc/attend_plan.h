@@ -46,5 +46,24 @@ inline int choose_cluster(const int (&fit)[4], int64_t units, int64_t most_tiles
     return 1 << best;
 }
 
+// Parts that the `tokens` of a shared prefix are cut into: two key tiles each or more, at most
+// `splits` (0 for no tokens).
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int prefix_parts(int tokens, int splits) {
+    const int pairs = (tokens + 2 * kTile - 1) / (2 * kTile);
+    return pairs < splits ? pairs : splits;
+}
+
+// CTAs that a piece of 256 query rows of one KV head is given for its group's prefix: as many
+// as the GPU holds at once, for `rows` rows a KV head of `groups` groups.
+inline int prefix_splits(int64_t rows, int groups, int hkv, int num_sms) {
+    int64_t pieces = (rows + (1 << kRowShift) - 1) >> kRowShift;
+    if (pieces < groups) pieces = groups;
+    const int64_t splits = num_sms / (pieces * hkv);
+    return splits < 1 ? 1 : splits > 64 ? 64 : int(splits);
+}
+
 }  // namespace attend
 }  // namespace pgd

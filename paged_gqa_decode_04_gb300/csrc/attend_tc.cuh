@@ -76,6 +76,7 @@
 #include "attend_plan.h"
 #include "page_ops.h"
 #include "ragged.cuh"
+#include "softcap.cuh"
 #include "umma.cuh"
 
 namespace pgd {
@@ -113,7 +114,23 @@ struct Args {
     int cluster;            // CTAs sharing a piece's keys
     const float* k_scale;   // 8-bit pages: [hkv], or [num_blocks][hkv]
     const float* v_scale;
+    // kShaped kernels
+    float cap, cap_inv;     // soft cap of the scores in base-2 units, and 1 over it
+    const float* slopes;    // [hq], natural units a token of distance
+    const int2* visible;    // [total] tokens [first, end) that a row may see; null: all
+    // shared prefixes: r.cu, r.B, r.total are groups of sequences (cu[g] .. cu[g+1] - 1 are
+    // those of group g) and queries; r.lens and r.table are the sequences' own
+    const int32_t* shared;  // [groups] tokens the group's sequences share; null: not this form
+    int32_t* starts;        // [batch] what of them is used, for the decode that follows
+    int batch, q_len;
+    int splits;             // CTAs that share a piece's keys, each with a part of its own
+    float* part_o;          // [splits][total * hq][D] normalised
+    float* part_lse;        // [splits][total * hq] base 2, -infinity: saw nothing
 };
+
+// What a kernel does beside the plain attention: kShaped rows with a visible range of their own
+// and shared prefixes; with kCap and kBias besides, scores capped and less slope * distance.
+constexpr int kShaped = 1, kCap = 2, kBias = 4;
 
 template <int D, int PAGE, bool PB>
 struct Layout {
@@ -167,6 +184,75 @@ __device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int first, 
     return p;
 }
 
+// Tokens [x, y) that row R of a sequence sees, (0, 0) where that is none.
+__device__ __forceinline__ int2 row_range(const Args& a, const Seq& s, int R) {
+    const int i = R / a.group, pos = s.len - s.n + i;
+    int lo = 0, hi = a.causal ? pos + 1 : s.len;
+    if (a.window > 0) lo = max(0, pos - a.window + 1);
+    if (a.visible) {
+        const int2 v = __ldg(a.visible + s.row0 + i);
+        lo = max(lo, v.x);
+        hi = min(hi, v.y);
+    }
+    return hi > lo ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
+// The same as span_of from the ranges of the rows themselves, which a warp looks at: rows
+// [first, first + 32) of the piece that are below `rows`.  A row that sees nothing does not
+// count; its scores are left as they come and the row becomes zeros at the end.
+__device__ __forceinline__ int4 range_of_warp(const Args& a, const Seq& s, int row0, int first,
+                                              int rows) {
+    const int r = first + (threadIdx.x & 31);
+    int2 v = make_int2(0, 0);
+    if (r < rows && s.ok) v = row_range(a, s, row0 + r);
+    const bool sees = v.y > v.x;
+    return make_int4(__reduce_min_sync(0xffffffffu, sees ? v.x : INT32_MAX),
+                     __reduce_max_sync(0xffffffffu, sees ? v.y : 0),
+                     __reduce_max_sync(0xffffffffu, sees ? v.x : 0),
+                     __reduce_min_sync(0xffffffffu, sees ? v.y : INT32_MAX));
+}
+
+// What group g shares of its sequences' tokens: at most what the caller says and what the
+// first query of each sequence sees, in whole blocks; and a sequence whose table names it.
+// Sequences without tokens, or of a length out of range, do not count.  By a warp.
+__device__ __forceinline__ int group_len(const Args& a, int g, int* first) {
+    const int lo = __ldg(a.r.cu + g), hi = __ldg(a.r.cu + g + 1);
+    int most = __ldg(a.shared + g), who = INT32_MAX;
+    if (lo >= 0 && hi <= a.batch)
+        for (int b = lo + int(threadIdx.x & 31); b < hi; b += 32) {
+            const int len = __ldg(a.r.lens + b);
+            if (len < 1 || len > a.r.max_len) continue;
+            most = min(most, len - a.q_len + 1);
+            who = min(who, b);
+        }
+    most = __reduce_min_sync(0xffffffffu, most);
+    who = __reduce_min_sync(0xffffffffu, who);
+    *first = who;
+    return who == INT32_MAX || most < 0 ? 0 : most / a.r.block_size * a.r.block_size;
+}
+
+// The starts of all sequences, by one CTA.  Groups that do not ascend within the batch, or
+// that share less than nothing, latch PGD_ERR_SEQ_LEN, and then nothing is shared at all: the
+// decode that follows reads every sequence whole.
+static __device__ __noinline__ void write_starts(const Args& a) {
+    bool bad = false;
+    for (int g = threadIdx.x; g < a.r.B; g += kThreads)
+        bad |= __ldg(a.r.cu + g) < 0 || __ldg(a.r.cu + g) > __ldg(a.r.cu + g + 1) ||
+               __ldg(a.r.cu + g + 1) > a.batch || __ldg(a.shared + g) < 0;
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0) latch(a.r.err, PGD_ERR_SEQ_LEN);
+    const int lo = bad ? a.batch : __ldg(a.r.cu), hi = bad ? a.batch : __ldg(a.r.cu + a.r.B);
+    for (int b = threadIdx.x; b < a.batch; b += kThreads)
+        if (b < lo || b >= hi) a.starts[b] = 0;
+    if (bad) return;
+    for (int g = threadIdx.x / 32; g < a.r.B; g += kThreads / 32) {
+        int first;
+        const int n = group_len(a, g, &first);
+        for (int b = __ldg(a.r.cu + g) + int(threadIdx.x & 31); b < __ldg(a.r.cu + g + 1); b += 32)
+            a.starts[b] = n;
+    }
+}
+
 __device__ __forceinline__ bool valid(const Ragged& r, int id) {
     return id >= 0 && id < r.num_blocks;
 }
@@ -174,12 +260,16 @@ __device__ __forceinline__ bool valid(const Ragged& r, int id) {
 // A page, tokens [t, t + n), has a block id out of range: the rows of the piece that see it are
 // marked in `lost`, a bit a row, to become NaN.  Apart from the kernel's own code, whose loops it
 // would slow down (2048 of 8192 tokens over bfloat16 pages, 64/8 heads: 337 -> 356 us).
-__device__ __noinline__ void mark_lost(const Args& a, const Seq& s, int row0, int t, int n,
+static __device__ __noinline__ void mark_lost(const Args& a, const Seq& s, int row0, int t, int n,
                                        uint32_t* lost) {
     for (int r = 0; r < 1 << kRowShift; ++r) {
         const int pos = s.len - s.n + (row0 + r) / a.group;
-        const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-        const int hi = a.causal ? pos + 1 : s.len;
+        int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+        int hi = a.causal ? pos + 1 : s.len;
+        if (a.visible) {
+            const int2 v = (row0 + r) / a.group < s.n ? row_range(a, s, row0 + r) : make_int2(0, 0);
+            lo = v.x, hi = v.y;
+        }
         if (lo < t + n && hi > t) atomicOr(lost + r / 32, 1u << r % 32);
     }
 }
@@ -267,7 +357,7 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
     }
 }
 
-template <int D, int PAGE, bool PB>
+template <int D, int PAGE, bool PB, int MOD>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
@@ -287,8 +377,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(smem + L::kBars + 280);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int share = a.cluster > 1 ? (int)cluster_rank() : 0;
-    if (blockIdx.x == 0) check_all(a.r, false);
+    int share = a.cluster > 1 ? (int)cluster_rank() : 0;
+    const bool prefix = MOD != 0 && a.shared;  // attention to shared prefixes
+    if (prefix && blockIdx.x == 0) {           // a CTA of its own, beside the grid of pieces
+        write_starts(a);
+        return;
+    }
+    if (!prefix && blockIdx.x == 0) check_all(a.r, false);
 
     // one thread sets the barriers up while the other warps look for their sequence
     if (threadIdx.x == 416) {
@@ -318,14 +413,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     // the piece of rows: the longest walks first, which for causal rows are the last ones
-    const int64_t unit = blockIdx.x / a.cluster;
+    int64_t unit = blockIdx.x / a.cluster;
+    if (prefix) {
+        unit = (blockIdx.x - 1) / a.splits;
+        share = int((blockIdx.x - 1) % a.splits);
+    }
     const int piece = a.pieces - 1 - int(unit % a.pieces);
     const int head = int(unit / a.pieces);
-    const int b = find_seq(a.r, piece, a.group, kRowShift, 1);
+    const int per = prefix ? a.group * a.q_len : a.group;  // rows of a unit of cu
+    const int b = find_seq(a.r, piece, per, kRowShift, 1);
     if (b >= a.r.B) return;  // the same for the whole cluster
-    const Seq s = load_seq(a.r, b);
+    Seq s;
+    int names = b;           // the sequence whose table names the blocks
+    if (prefix) {
+        const int lo = __ldg(a.r.cu + b), hi = __ldg(a.r.cu + b + 1);
+        if (lo < 0 || hi < lo || hi > a.batch) return;
+        s.b = b;
+        s.row0 = lo * a.q_len;
+        s.n = (hi - lo) * a.q_len;
+        s.len = group_len(a, b, &names);
+        s.ok = true;
+        // nothing to read, or no part for this CTA: the starts say so
+        if (share >= prefix_parts(s.len, a.splits)) return;
+    } else {
+        s = load_seq(a.r, b);
+    }
+    const int parts_of_keys = prefix ? prefix_parts(s.len, a.splits) : a.cluster;
     const uint32_t group = a.group;
-    const int row0 = int(piece - first_piece(a.r, b, a.group, kRowShift, 1)) << kRowShift;
+    const int row0 = int(piece - first_piece(a.r, b, per, kRowShift, 1)) << kRowShift;
     // rows of the piece (an impossible sequence's only become NaN)
     const int n = s.ok ? s.n : min(__ldg(a.r.cu + b + 1), a.r.total) - s.row0;
     if (row0 < 0 || s.row0 < 0 || n <= 0) return;
@@ -333,8 +448,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rows <= 0) return;
 
     Span sp[2];
-    sp[0] = span_of(a, s, row0, row0 + min(rows, kBlock) - 1);
-    sp[1] = span_of(a, s, row0 + kBlock, row0 + rows - 1);
+    if (MOD != 0 && a.visible) {
+        int4* const of_warp = reinterpret_cast<int4*>(smem);  // before the queries come there
+        if (warp < 8) {
+            const int4 v = range_of_warp(a, s, row0, warp * 32, rows);
+            if (lane == 0) of_warp[warp] = v;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            int4 v = of_warp[4 * i];
+            for (int w = 1; w < 4; ++w) {
+                const int4 u = of_warp[4 * i + w];
+                v = make_int4(min(v.x, u.x), max(v.y, u.y), max(v.z, u.z), min(v.w, u.w));
+            }
+            sp[i] = Span{0, 0, 0, 0, v.z, v.w};
+            if (v.y > v.x) {
+                sp[i].lo = v.x, sp[i].hi = v.y;
+                sp[i].t0 = v.x / kTile;
+                sp[i].t1 = (v.y - 1) / kTile + 1;
+            }
+        }
+    } else {
+        sp[0] = span_of(a, s, row0, row0 + min(rows, kBlock) - 1);
+        sp[1] = span_of(a, s, row0 + kBlock, row0 + rows - 1);
+    }
     const bool some0 = sp[0].t1 > sp[0].t0, some1 = sp[1].t1 > sp[1].t0;
     // tokens and tiles of the CTA
     const int lo = some0 ? (some1 ? min(sp[0].lo, sp[1].lo) : sp[0].lo) : sp[1].lo;
@@ -342,17 +480,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     int T0 = lo / kTile, T1 = hi > lo ? (hi - 1) / kTile + 1 : T0;
     // 128 rows or fewer: both blocks take them, and every other tile each, where every CTA of
     // the cluster has two (all of them decide alike)
-    const bool paired = rows <= kBlock && T1 - T0 >= 2 * a.cluster;
-    if (a.cluster > 1) {  // this CTA's share of the tiles
+    const bool paired = rows <= kBlock && T1 - T0 >= 2 * parts_of_keys;
+    if (parts_of_keys > 1) {  // this CTA's share of the tiles
         const int tiles = T1 - T0, t = T0;
-        T0 = t + tiles * share / a.cluster;
-        T1 = t + tiles * (share + 1) / a.cluster;
+        T0 = t + tiles * share / parts_of_keys;
+        T1 = t + tiles * (share + 1) / parts_of_keys;
     }
     if (paired) sp[1] = sp[0];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         sp[i].t0 = max(sp[i].t0, T0);
         sp[i].t1 = max(sp[i].t0, min(sp[i].t1, T1));
+    }
+    // With a bias that falls with distance the last tiles come first: the scores' maxima would
+    // grow with every tile otherwise.  j counts tiles as they come, tile_at(j) is the tile.
+    constexpr bool kBack = (MOD & kBias) != 0;
+    auto tile_at = [&](int j) { return kBack ? T0 + T1 - 1 - j : j; };
+    if (kBack) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t0 = sp[i].t0;
+            sp[i].t0 = T0 + T1 - sp[i].t1;
+            sp[i].t1 = T0 + T1 - t0;
+        }
     }
 
     if (warp == 12) tmem_alloc(smem_addr(tmem_at), 512);
@@ -406,10 +556,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             const uint32_t R = row0 + at_row;
             int my_lo = 0, my_hi = 0;
-            if (at_row < rows) {
+            if (MOD != 0 && at_row < rows) {
+                const int2 v = row_range(a, s, R);
+                my_lo = v.x, my_hi = v.y;
+            } else if (at_row < rows) {
                 const int pos = s.len - s.n + int(R / group);
                 my_hi = a.causal ? pos + 1 : s.len;
                 if (a.window > 0) my_lo = max(0, pos - a.window + 1);
+            }
+            float slope = 0.f;  // in base-2 units
+            int pos = 0;        // of the row's token
+            if ((MOD & kBias) && at_row < rows) {
+                const int i = int(R / group);
+                slope = __ldg(a.slopes + head * a.group + R % group) * 1.4426950408889634f;
+                pos = s.len - s.n + i;
+                if (prefix)
+                    pos = __ldg(a.r.lens + (s.row0 + i) / a.q_len) - a.q_len + i % a.q_len;
             }
             const uint32_t lanes = uint32_t(warp % 4 * 32) << 16;
             const uint32_t ts = tmem + lanes + blk * kTile;
@@ -432,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (PB) wait_st();  // a tile may rescale twice, for the gain and for the maximum
             };
             const int first = p.t0 + (paired ? blk : 0), by = paired ? 2 : 1;  // its tiles
+            constexpr bool kShape = (MOD & (kCap | kBias)) != 0;
             // One tile of scores; `edge`: some row does not see all of it.
             auto tile = [&](int j, auto edge) {
                 uint32_t x[kTile], w[kTile / 4];
@@ -458,11 +621,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int g = 0; g <= 8; ++g) {
                         const int at = h * (kTile / 2) + g * 8;
-                        const float mul = PB && g < 8 ? sc[h * 8 + g].x : scale;
+                        const float mul = kShape ? 1.f : PB && g < 8 ? sc[h * 8 + g].x : scale;
                         const float add = PB && g < 8 ? off + sc[h * 8 + g].y : off;
                         const uint64_t cc = pair(mul, mul), mm = pair(add, add);
                         if (g < 8) {
-                            if (h == 0 && PB) {
+                            if (kShape) {  // the maximum is known
+                            } else if (h == 0 && PB) {
                                 float u = max8(x + g * 8) * sc[g].x;
                                 float v = max8(x + kTile / 2 + g * 8) * sc[8 + g].x;
                                 top[0] = g == 0 ? fmaxf(u, v) : max3(top[0], u, v);
@@ -507,14 +671,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The first half's weights are relative to the old maximum while the new one is
                 // found; the tile is read again where that has grown too far.
                 bool grown;
-                do {
+                if constexpr (kShape) {
+                    // Scores as they are asked for come first, then their maximum: the tile
+                    // would have to be shaped again if that were found with the weights.
+#pragma unroll
+                    for (int i = 0; i < kTile; i += 32) tmem_ld32(ts + i, x + i);
+                    wait_ld();
+#pragma unroll
+                    for (int i = 0; i < kTile; i += 32) keep32(x + i);
+                    const int t0 = tile_at(j) * kTile, from = my_lo - t0, until = my_hi - t0;
+                    const float far = float(t0 - pos);
+#pragma unroll
+                    for (int g = 0; g < kTile / 8; ++g) {
+                        const float mul = PB ? sc[g].x : scale;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int i = g * 8 + e;
+                            float y = __uint_as_float(x[i]) * mul;
+                            if (MOD & kCap) y = capped(y, a.cap, a.cap_inv);
+                            if (MOD & kBias) y = fmaf(-slope, fabsf(far + float(i)), y);
+                            if (decltype(edge)::value && (i < from || i >= until)) y = -INFINITY;
+                            x[i] = __float_as_uint(y);
+                        }
+                        const float u = max8(x + g * 8);
+                        top[0] = g == 0 ? u : fmaxf(top[0], u);
+                    }
+                    const bool over = top[0] > m + kGrow;
+                    if (__any_sync(0xffffffffu, over)) {
+                        float keep = 1.f;
+                        if (over) {
+                            keep = m == -INFINITY ? 0.f : ex2(m - top[0]);
+                            l *= keep;
+                            m = top[0];
+                        }
+                        if (j > first) rescale(keep);
+                    }
+                    sum[0] = sum[1] = 0;
+                    weigh(0);
+                    grown = false;
+                } else do {
 #pragma unroll
                     for (int i = 0; i < kTile; i += 32) tmem_ld32(ts + i, x + i);
                     wait_ld();
 #pragma unroll
                     for (int i = 0; i < kTile; i += 32) keep32(x + i);
                     if (decltype(edge)::value) {
-                        const int from = my_lo - j * kTile, until = my_hi - j * kTile;
+                        const int t0 = tile_at(j) * kTile, from = my_lo - t0, until = my_hi - t0;
 #pragma unroll
                         for (int i = 0; i < kTile; ++i)
                             if (i < from || i >= until) x[i] = 0xff800000u;  // -infinity
@@ -556,12 +758,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = first; j < p.t1; j += by, phase ^= 1) {
                 if (!warp_wait(bar_s + 8 * blk, phase, gave_up)) break;
                 fence_after();
-                if (j * kTile < p.lo_all || p.hi_all - j * kTile < kTile)
+                if (tile_at(j) * kTile < p.lo_all || p.hi_all - tile_at(j) * kTile < kTile)
                     tile(j, std::true_type());
                 else
                     tile(j, std::false_type());
             }
             warp_wait(bar_o + 8 * blk, 0, gave_up);
+            if (MOD != 0 && my_hi <= my_lo) {  // a row that sees nothing
+                m = -INFINITY;
+                l = 0.f;
+            }
         }
     } else if (kQ8 && warp < 12) {
         // ---------------------------------------------------------- widening (8-bit pages)
@@ -580,7 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!live) break;
                 const uint8_t* const src = smem + L::kRaw + raw * L::kRawSlot;
                 uint8_t* const dst = smem + L::kRing + slot * L::kSlot;
-                const bool edge = side == 1 && (j * kTile < lo || hi - j * kTile < kTile);
+                const int tj = tile_at(j);
+                const bool edge = side == 1 && (tj * kTile < lo || hi - tj * kTile < kTile);
                 uint4 x[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -596,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     widen4<PAGE>(x[i].y, y[2], y[3]);
                     widen4<PAGE>(x[i].z, y[4], y[5]);
                     widen4<PAGE>(x[i].w, y[6], y[7]);
-                    const int t = j * kTile + r;
+                    const int t = tj * kTile + r;
                     if (edge && (t < lo || t >= hi)) {  // V rows no query sees
 #pragma unroll
                         for (int e = 0; e < 8; ++e) y[e] = 0;
@@ -624,35 +831,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int copies = kTile / box * L::kHalves;  // of a tile
         const int k = lane * L::kProducers + me, my_page = k / L::kHalves, my_half = k % L::kHalves;
         const bool mine = k < copies;
-        const int32_t* table = a.r.table + (int64_t)b * a.r.max_blocks;
+        const int32_t* table = a.r.table + (int64_t)names * a.r.max_blocks;
         auto seen = [&](int j) {
-            const int t = j * kTile + my_page * box;
+            const int t = tile_at(j) * kTile + my_page * box;
             return mine && j < T1 && t < hi && t + box > lo;
         };
         auto id_of = [&](int j) {
-            return seen(j) ? __ldg(table + (j * kTile + my_page * box) / bs) : -1;
+            return seen(j) ? __ldg(table + (tile_at(j) * kTile + my_page * box) / bs) : -1;
         };
         const uint32_t at = my_half * (kTile * 128) + my_page * box * 128;
         int id = id_of(T0);
         uint32_t slot = 0, turn = 0, patches = 0, n = 0;  // n: tiles into the ring so far
         bool live = true;
         for (int j = T0; j < T1 && live; ++j) {
-            const int next = id_of(j + 1);
+            const int next = id_of(j + 1), tj = tile_at(j);
             const bool ok = valid(a.r, id);
             const unsigned which = __ballot_sync(0xffffffffu, ok);
             const bool gone = seen(j) && !ok;
             if (__any_sync(0xffffffffu, gone)) {  // rare: the warp stays together beside it
                 if (gone) {
                     latch(a.r.err, PGD_ERR_BLOCK_ID);
-                    mark_lost(a, s, row0, j * kTile + my_page * box, box, lost);
+                    mark_lost(a, s, row0, tj * kTile + my_page * box, box, lost);
                 }
                 __syncwarp();
             }
             const uint32_t bytes = __popc(which) * box * 128;
             // rows no query sees, or that have no page, among this warp's copies
-            const bool patch = j * kTile < lo || hi - j * kTile < kTile ||
+            const bool patch = tj * kTile < lo || hi - tj * kTile < kTile ||
                                __any_sync(0xffffffffu, mine && !ok);
-            const int row = (j * kTile + my_page * box) % bs;
+            const int row = (tj * kTile + my_page * box) % bs;
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
                 if (live) live = warp_wait(bar_empty + 8 * slot, turn ^ 1, gave_up);
@@ -679,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint8_t* const col = smem + L::kRing + slot * L::kSlot +
                                              c % L::kHalves * (kTile * 128) + lane % 8 * 16;
                         for (int r = first + lane / 8; r < first + box; r += 4) {
-                            const int t = j * kTile + r;
+                            const int t = tj * kTile + r;
                             if (t < lo || t >= hi || !(which >> (c / L::kProducers) & 1))
                                 *reinterpret_cast<uint4*>(col + r * 128) = make_uint4(0, 0, 0, 0);
                         }
@@ -712,13 +919,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int bs = a.r.block_size, me = warp - 14;
         const int box = min(bs, kTile), pages = kTile / box;
         const int page = lane * L::kProducers + me;
-        const int32_t* table = a.r.table + (int64_t)b * a.r.max_blocks;
+        const int32_t* table = a.r.table + (int64_t)names * a.r.max_blocks;
         auto seen = [&](int j, int pg) {
-            const int t = j * kTile + pg * box;
+            const int t = tile_at(j) * kTile + pg * box;
             return pg < pages && j < T1 && t < hi && t + box > lo;
         };
         auto id_of = [&](int j, int pg) {
-            return seen(j, pg) ? __ldg(table + (j * kTile + pg * box) / bs) : -1;
+            return seen(j, pg) ? __ldg(table + (tile_at(j) * kTile + pg * box) / bs) : -1;
         };
         auto scale_of = [&](const float* scales, int id, float none) {
             return valid(a.r, id) ? __ldg(scales + (int64_t)id * a.hkv + head) : none;
@@ -768,11 +975,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool ok = seen(j, page);
             if (ok && !valid(a.r, id)) {
                 latch(a.r.err, PGD_ERR_BLOCK_ID);
-                mark_lost(a, s, row0, j * kTile + page * box, box, lost);
+                mark_lost(a, s, row0, tile_at(j) * kTile + page * box, box, lost);
                 id = -1;  // outside the tensor: zeros
             }
             const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * box * 128;
-            const int row = (j * kTile + page * box) % bs;
+            const int row = (tile_at(j) * kTile + page * box) % bs;
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
                 if (live) live = warp_wait(bar_raw_empty + 8 * raw, turn ^ 1, gave_up);
@@ -909,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t out_at = (int64_t)s.row0 * a.hq + (int64_t)head * a.group;  // head vectors
     // what the accumulator is to be multiplied with beside 1 / l
     const float by = !kQ8 ? 1.f : PB ? 1.f / vgain : __ldg(a.v_scale + head);
-    if (a.cluster == 1 && !paired) {
+    if (a.cluster == 1 && !paired && !prefix) {
         if (warp < 8) {
             const uint32_t to = tmem + (uint32_t(warp % 4 * 32) << 16) + 2 * kTile + blk * D;
             const float inv = failed ? NAN : l > 0.f ? by / l : l == 0.f ? 0.f : NAN;
@@ -990,7 +1197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr int kQuads = D / 4, kLines = 32 / kQuads;
             const int step = a.cluster * 8 * kLines;
             const int c = lane % kQuads, line = lane / kQuads;
-            const int from = (share * 8 + warp) * kLines;
+            const int from = ((prefix ? 0 : share) * 8 + warp) * kLines;
             Rows at(row0 + from + line, group, step);
             // kR rows with kP parts each are on their way together: four loads, and none for a
             // part that is not there (two parts loaded as four: 481 against 462 us for two
@@ -1040,6 +1247,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (r0 + u * step + line >= rows) continue;
                         // a row that sees a token has a sum of 1 or more; NaN where a part failed
                         const float inv = sum[u] == 0.f ? 0.f : __fdividef(1.f, sum[u]);
+                        if (prefix) {  // this CTA's part of the row
+                            const int64_t r = (int64_t)share * a.r.total * a.hq + out_at +
+                                              at.token * a.hq + at.head;
+                            *reinterpret_cast<float4*>(a.part_o + r * D + c * 4) =
+                                make_float4(o[u][0] * inv, o[u][1] * inv, o[u][2] * inv,
+                                            o[u][3] * inv);
+                            if (c == 0)
+                                a.part_lse[r] = sum[u] == 0.f ? -INFINITY
+                                                : sum[u] != sum[u]
+                                                    ? 0.f
+                                                    : top[u] + __log2f(sum[u]) -
+                                                          (kQ8 && !PB ? kLift : 0.f);
+                            continue;
+                        }
                         *reinterpret_cast<uint2*>(
                             a.out + (out_at + at.token * a.hq + at.head) * D + c * 4) =
                             make_uint2(bf16x2(o[u][0] * inv, o[u][1] * inv),

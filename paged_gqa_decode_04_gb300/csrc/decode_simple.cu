@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kSimpleThreads) decode_simple_kernel(DecodeArg
 
         for (int j = warp; j < G; j += kSimpleWarps) {
             const int h = kvh * G + j;
+            const float slope = a.slopes ? a.slopes[h] * 1.4426950408889634f : 0.f;
             float qf[DPL], o[DPL];
             const T* qrow = q + ((int64_t)b * a.hq + h) * D + lane * DPL;
 #pragma unroll
@@ -97,7 +98,10 @@ __global__ void __launch_bounds__(kSimpleThreads) decode_simple_kernel(DecodeArg
                 for (int e = 0; e < DPL; ++e) dot += qf[e] * ld_f(kp + row + e);
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-                const float s = dot * a.scale_log2;
+                float s = dot * a.scale_log2;
+                // tanhf: the float32 path's results hold to 1e-5
+                if (a.cap > 0.f) s = a.cap * tanhf(s * a.cap_inv);
+                s = fmaf(slope, (float)(t - (L - 1)), s);
                 const float m_new = fmaxf(m, s);
                 const float alpha = fast_exp2(m - m_new);
                 const float p = fast_exp2(s - m_new);

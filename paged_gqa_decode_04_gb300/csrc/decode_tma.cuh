@@ -61,6 +61,7 @@
 #include <mutex>
 
 #include "partition.cuh"
+#include "softcap.cuh"
 
 namespace pgd {
 namespace tma {
@@ -70,6 +71,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 // this many tiles per CTA: tiny calls then split runs into fewer pieces.
 constexpr int kMinTilesPerCta = 2;
 constexpr int kSmemBudget = 227 * 1024;
+constexpr float kLog2e = 1.4426950408889634f;  // slopes are given in natural units
 
 // ----------------------------------------------------------------- PTX wrappers
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -274,7 +276,7 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
 
 // ----------------------------------------------------------------- configuration
 template <int D_, int HG_, int MT_, int TG_, bool ROWS16_, bool FP8_ = false, int MV_ = 0,
-          bool INT8_ = false, bool PB_ = false>
+          bool INT8_ = false, bool PB_ = false, bool EX_ = false>
 struct Cfg {
     static constexpr int D = D_;
     static constexpr int HG = HG_;            // KV heads per unit of work
@@ -284,6 +286,9 @@ struct Cfg {
     static constexpr bool FP8 = FP8_;         // 8-bit K/V pages, f16 products
     static constexpr bool INT8 = INT8_;       // 8-bit pages hold int8 codes (else e4m3)
     static constexpr bool PB = PB_;           // 8-bit pages with a scale per block and KV head
+    // scores capped and with a distance bias (a.softcap, a.slopes), sequences walked from
+    // a.starts on, results for a later join (a.row_o): see DecodeArgs
+    static constexpr bool EX = EX_;
     // merge variant of split runs: 0 the last arriver merges with register
     // loads; 1 (SHARE, cooperative launch) all pieces' warps merge a share of
     // the rows; 2 (SEP) no merge here: pieces write partials, and a second
@@ -342,7 +347,7 @@ struct StageDesc {
     int n_b;            // tiles of the run
     int tok0;           // sequence position of the tile's first token
     int L;              // sequence length
-    int pad;
+    int start;          // EX: first token the sequence is walked from
 };
 
 // Offset (in elements) of query row r of KV head kvh of sequence b in q / out
@@ -504,9 +509,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         aborted = 0;
         fence_barrier_init();
     }
+    const int32_t* const starts = C::EX ? a.starts : nullptr;
     find_span_start(a.seq_lens, a.B, a.units, T, a.q_len, a.window, a.max_blocks, bs,
                     a.num_parts, a.auto_parts ? kMinTilesPerCta : 1, scratch, &ss,
-                    a.tile_base, a.run_cost);  // ends with __syncthreads
+                    a.tile_base, a.run_cost, starts);  // ends with __syncthreads
 
     // Sequences that own no tiles: length 0 gives zeros, an out-of-range length
     // gives NaN and latches PGD_ERR_SEQ_LEN.  CTA b % P writes sequence b.
@@ -526,7 +532,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (warp == C::NC) {
         // ============================================================ producer
         TileCursor cur = cursor_at(ss, a.seq_lens, a.units, T, a.q_len, a.window, a.max_blocks,
-                                   bs, W);
+                                   bs, W, starts);
         const uint64_t policy = policy_evict_first();
         const uint32_t box_bytes = (uint32_t)(C::HH * R * 128);
         // Block-id window: lane l holds block_table[win_b][win_lb + l]; the next
@@ -553,7 +559,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int npg = bs < T ? (n_valid + bs - 1) / bs : 1;
             // pages wholly before the earliest token any query reads are not
             // fetched (a windowed cache may have released them)
-            const int lo_min = a.window > 0 ? max(0, L - a.q_len - a.window + 1) : 0;
+            const int start = C::EX ? start_of(starts, cur.b, L) : 0;
+            int lo_min = a.window > 0 ? max(0, L - a.q_len - a.window + 1) : 0;
+            if constexpr (C::EX) lo_min = max(lo_min, start);
             const int skip = (bs < T && lo_min > tok0) ? (lo_min - tok0) / bs : 0;
             const int lb0 = tok0 / bs;
             const int slot0 = bs < T ? 0 : tok0 % bs;
@@ -600,7 +608,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const uint32_t fb = smem_u32(&full_bar[s]);
             if (lane == 0) {
                 desc[s] = StageDesc{cur.run_start, cur.b, cur.unit, n_valid, flags, cur.n_b,
-                                    tok0, L, 0};
+                                    tok0, L, start};
                 mbar_arrive_expect_tx(fb, (uint32_t)nok * box_bytes * 2u);
                 if (bad) latch_error(a.err, PGD_ERR_BLOCK_ID);
             }
@@ -625,7 +633,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (lane == 0) mbar_arrive(fb);  // second arrival: the scales are in place
             }
             cursor_next(cur, a.seq_lens, a.B, a.units, T, a.q_len, a.window, a.max_blocks, bs,
-                        W);
+                        W, starts);
         }
         // Do not leave while copies this CTA issued may still land.
         if (lane == 0) {
@@ -665,6 +673,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // int8 pages: the K bias term of each row's scores (1152 * sum_d q) and
     // the running sums of the f16 P values (for the V bias term); 0 otherwise
     float qc0 = 0.f, qc1 = 0.f, cp0 = 0.f, cp1 = 0.f;
+    float sl0 = 0.f, sl1 = 0.f;  // EX: distance slopes of the rows' heads (base-2 units)
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     bool seg_bad = false;
     uint32_t comb_phase = 0;
@@ -685,6 +694,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             qb + (row0_ok ? qrow_offset(a, q_seq, q_kvh, row0) : 0));
         const uint32_t* q1 = reinterpret_cast<const uint32_t*>(
             qb + (row1_ok ? qrow_offset(a, q_seq, q_kvh, row1) : 0));
+        if constexpr (C::EX) {
+            if (a.slopes) {
+                const float* sl = a.slopes + (int64_t)q_kvh * G;
+                sl0 = row0_ok ? __ldg(sl + row0 % G) * kLog2e : 0.f;
+                sl1 = row1_ok ? __ldg(sl + row1 % G) * kLog2e : 0.f;
+            }
+        }
         if constexpr (C::FP8) {
             // f16 fragments with the head dimension permuted inside each
             // 16-wide step: mma k-slots (2 tig, 2 tig + 1) and (2 tig + 8,
@@ -739,7 +755,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     int pre_seq = -1, pre_kvh = -1;
     {
         const TileCursor c0 = cursor_at(ss, a.seq_lens, a.units, T, a.q_len, a.window,
-                                        a.max_blocks, bs, W);
+                                        a.max_blocks, bs, W, starts);
         pre_seq = c0.b;
         pre_kvh = c0.unit * C::HG + hgi;
         load_q(pre_seq, pre_kvh);
@@ -787,7 +803,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // tile-local tokens before `v_lo` (pages not fetched: before every
         // query's window) or from n_valid on (past the end) hold tail slots or
         // stale data: zero their V rows so 0 * (NaN or Inf) never reaches O
-        const int lo_min = a.window > 0 ? max(0, dsc.L - a.q_len - a.window + 1) : 0;
+        const int start = C::EX ? dsc.start : 0;
+        int lo_min = a.window > 0 ? max(0, dsc.L - a.q_len - a.window + 1) : 0;
+        if constexpr (C::EX) lo_min = max(lo_min, start);
         const int v_lo = max(0, lo_min - dsc.tok0);
         const bool active = tw0 < n_valid && tw0 + C::TW > v_lo;
         // (both ends clamped to my slice: with several token groups or chunks
@@ -856,8 +874,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 // ---- mask (causal / window, per row), scale to base-2 units, running max
                 const int hi0 = dsc.L - a.q_len + qi0 + 1 - dsc.tok0;   // tile-local bounds
                 const int hi1 = dsc.L - a.q_len + qi1 + 1 - dsc.tok0;
-                const int lo0 = a.window > 0 ? hi0 - a.window : INT_MIN;
-                const int lo1 = a.window > 0 ? hi1 - a.window : INT_MIN;
+                int lo0 = a.window > 0 ? hi0 - a.window : INT_MIN;
+                int lo1 = a.window > 0 ? hi1 - a.window : INT_MIN;
+                if constexpr (C::EX) {
+                    lo0 = max(lo0, start - dsc.tok0);
+                    lo1 = max(lo1, start - dsc.tok0);
+                }
                 float mx0 = -INFINITY, mx1 = -INFINITY;
                 // logit multiplier of each n-tile (8 tokens, one page): with
                 // per-block scales, times the K scale of the tile's page
@@ -872,7 +894,30 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 // every row sees all of this warp's tokens (the usual case): no mask
                 const bool full = c0 + C::CH <= dsc.L - a.q_len + 1 - dsc.tok0 &&
                                   (a.window == 0 || c0 >= dsc.L - a.window - dsc.tok0);
-                if (full) {
+                if constexpr (C::EX) {
+                    // capped, and less slope * distance: the row's own position is hi - 1
+                    auto shape = [&](float s, float slope, int from) {
+                        if (a.cap > 0.f) s = capped(s, a.cap, a.cap_inv);
+                        return fmaf(slope, (float)from, s);
+                    };
+#pragma unroll
+                    for (int j = 0; j < C::CH / 8; ++j) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int tok = c0 + j * 8 + tig * 2 + e;
+                            const float s0 = shape(fmaf(sc[j][e], smj[j], -qc0 * smj[j]), sl0,
+                                                   tok - (hi0 - 1));
+                            sc[j][e] = tok < hi0 && tok >= lo0 ? s0 : -INFINITY;
+                            mx0 = fmaxf(mx0, sc[j][e]);
+                            if (C::ROWS16) {
+                                const float s1 = shape(fmaf(sc[j][2 + e], smj[j], -qc1 * smj[j]),
+                                                       sl1, tok - (hi1 - 1));
+                                sc[j][2 + e] = tok < hi1 && tok >= lo1 ? s1 : -INFINITY;
+                                mx1 = fmaxf(mx1, sc[j][2 + e]);
+                            }
+                        }
+                    }
+                } else if (full) {
 #pragma unroll
                     for (int j = 0; j < C::CH / 8; ++j) {
 #pragma unroll
@@ -1137,6 +1182,30 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // a query before the sequence start) has l = 0: zeros, lse = -inf
         const float inv0 = seg_bad ? NAN : (lt0 > 0.f ? v_mul / lt0 : 0.f);
         const float inv1 = seg_bad ? NAN : (lt1 > 0.f ? v_mul / lt1 : 0.f);
+        if (C::EX && a.row_o && !(dsc.flags & kSegPartial)) {
+            // whole run, to be joined with its prefix: rows in float32 and their lse
+            auto put = [&](bool ok, int row, int at, float inv, float m, float lt) {
+                if (!ok) return;
+                const int64_t r = qrow_offset(a, dsc.b, kvh, row);
+                if constexpr (C::FP8) {
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c)
+                        *reinterpret_cast<float4*>(a.row_o + r + 16 * c + 4 * tig) = make_float4(
+                            o[2 * c][at] * inv, o[2 * c + 1][at] * inv, o[2 * c][at + 1] * inv,
+                            o[2 * c + 1][at + 1] * inv);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n)
+                        *reinterpret_cast<float2*>(a.row_o + r + n * 8 + tig * 2) =
+                            make_float2(o[n][at] * inv, o[n][at + 1] * inv);
+                }
+                if (tig == 0)
+                    a.row_lse[r / D] = seg_bad ? 0.f : lt > 0.f ? m + fast_log2(lt) : -INFINITY;
+            };
+            put(row0_ok, row0, 0, inv0, m0, lt0);
+            put(row1_ok, row1, 2, inv1, m1, lt1);
+            continue;
+        }
         if (!(dsc.flags & kSegPartial)) {
             __nv_bfloat16* o0 = static_cast<__nv_bfloat16*>(a.out) +
                                 (row0_ok ? qrow_offset(a, dsc.b, kvh, row0) : 0);
@@ -1212,6 +1281,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
         }
         if constexpr (C::SEP) continue;  // merged by the run-merge kernel after this one
+        if (C::EX && a.join) continue;   // joined by the kernel after this one
         // Publish the partial and count it; the warp that brings the count to
         // the number of pieces sets it back to zero and flips the run's flag
         // bit.  Shared merge (cooperative launch, a merge of more than six
@@ -1368,24 +1438,24 @@ constexpr int token_groups(int t, int hg, int mt) {
     return by_tokens < by_warps ? by_tokens : by_warps;
 }
 
-template <int D, int HG, int MT, bool R16, bool FP8, int MV, bool INT8, bool PB>
+template <int D, int HG, int MT, bool R16, bool FP8, int MV, bool INT8, bool PB, bool EX>
 cudaError_t launch_hg(const DecodeArgs& a, const Pool& p, cudaStream_t s) {
     constexpr int TG = token_groups((FP8 ? 256 : 128) / HG, HG, MT);
     const int idx = HG == 1 ? 0 : HG == 2 ? 1 : HG == 4 ? 2 : 3;
-    return launch_cfg<Cfg<D, HG, MT, TG, R16, FP8, MV, INT8, PB>>(
+    return launch_cfg<Cfg<D, HG, MT, TG, R16, FP8, MV, INT8, PB, EX>>(
         a, p.tmap_k[idx], p.tmap_v[idx], p.num_sms, p.device, s);
 }
 
-template <int D, int MT, bool R16, bool FP8, int MV, bool INT8, bool PB>
+template <int D, int MT, bool R16, bool FP8, int MV, bool INT8, bool PB, bool EX>
 cudaError_t launch_mt(const DecodeArgs& a, const Pool& p, cudaStream_t s) {
     switch (a.hg) {
-        case 1: return launch_hg<D, 1, MT, R16, FP8, MV, INT8, PB>(a, p, s);
-        case 2: return launch_hg<D, 2, MT, R16, FP8, MV, INT8, PB>(a, p, s);
+        case 1: return launch_hg<D, 1, MT, R16, FP8, MV, INT8, PB, EX>(a, p, s);
+        case 2: return launch_hg<D, 2, MT, R16, FP8, MV, INT8, PB, EX>(a, p, s);
         case 4:
-            if constexpr (MT <= 2) return launch_hg<D, 4, MT, R16, FP8, MV, INT8, PB>(a, p, s);
+            if constexpr (MT <= 2) return launch_hg<D, 4, MT, R16, FP8, MV, INT8, PB, EX>(a, p, s);
             break;
         case 8:
-            if constexpr (MT == 1) return launch_hg<D, 8, MT, R16, FP8, MV, INT8, PB>(a, p, s);
+            if constexpr (MT == 1) return launch_hg<D, 8, MT, R16, FP8, MV, INT8, PB, EX>(a, p, s);
             break;
     }
     return cudaErrorInvalidValue;
@@ -1395,14 +1465,14 @@ cudaError_t launch_mt(const DecodeArgs& a, const Pool& p, cudaStream_t s) {
 // PB: with a scale per block and KV head (else per KV head).
 // MV: merge variant (see Cfg).  The shared variant (1) returns
 // cudaErrorCooperativeLaunchTooLarge when the grid cannot be resident at once.
-template <int D, bool FP8, int MV, bool INT8 = false, bool PB = false>
+template <int D, bool FP8, int MV, bool INT8 = false, bool PB = false, bool EX = false>
 cudaError_t launch_tma_d(const DecodeArgs& a, const Pool& p, cudaStream_t s) {
     const int rows = a.q_len * a.group;  // query rows per KV head
-    if (rows <= 8) return launch_mt<D, 1, false, FP8, MV, INT8, PB>(a, p, s);
-    if (rows <= 16) return launch_mt<D, 1, true, FP8, MV, INT8, PB>(a, p, s);
-    if (rows <= 32) return launch_mt<D, 2, true, FP8, MV, INT8, PB>(a, p, s);
-    if (rows <= 48) return launch_mt<D, 3, true, FP8, MV, INT8, PB>(a, p, s);
-    return launch_mt<D, 4, true, FP8, MV, INT8, PB>(a, p, s);
+    if (rows <= 8) return launch_mt<D, 1, false, FP8, MV, INT8, PB, EX>(a, p, s);
+    if (rows <= 16) return launch_mt<D, 1, true, FP8, MV, INT8, PB, EX>(a, p, s);
+    if (rows <= 32) return launch_mt<D, 2, true, FP8, MV, INT8, PB, EX>(a, p, s);
+    if (rows <= 48) return launch_mt<D, 3, true, FP8, MV, INT8, PB, EX>(a, p, s);
+    return launch_mt<D, 4, true, FP8, MV, INT8, PB, EX>(a, p, s);
 }
 
 }  // namespace tma

@@ -1,0 +1,10 @@
+// The TMA decode kernel for int8 pages with a scale per block and KV head, with shaped scores (softcap,
+// distance bias), sequences walked from a start and results left for a join.
+#include "decode_tma.cuh"
+
+namespace pgd {
+namespace tma {
+template cudaError_t launch_tma_d<128, true, 0, true, true, true>(const DecodeArgs&, const Pool&,
+                                                                  cudaStream_t);
+}  // namespace tma
+}  // namespace pgd

@@ -45,6 +45,15 @@ inline int check_ragged(const Pool& p, int total, const int32_t* cu, int B, cons
     return PGD_OK;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The soft cap and the slopes of a call with shaped scores.  The cap and its inverse stay far
+// inside float32's range.
+inline int check_shaping(float softcap, const float* slopes) {
+    if (softcap != 0.f && !(softcap >= 0x1p-64f && softcap <= 0x1p64f)) return PGD_ERR_ARG;
+    return is_aligned(slopes, 4) ? PGD_OK : PGD_ERR_ALIGN;
+}
+
 // A packed tensor of rows of `width` elements, `stride` elements apart.
 inline int check_rows(const void* p, int64_t stride, int64_t width, int elt) {
     if (!p) return PGD_ERR_ARG;

@@ -53,12 +53,23 @@ __device__ __forceinline__ int first_tile_of(int L, int T, int q_len, int window
     return lo > 0 ? lo / T : 0;
 }
 
-// Tiles of T tokens a sequence of length L walks (0 for L == 0 or a length out
+// The same with `starts` (null: all zeros): sequence b is walked from token starts[b]
+// on, at most its length (decode with shared prefixes: what lies before is attended to
+// for a whole group at once).
+__device__ __forceinline__ int start_of(const int32_t* starts, int b, int L) {
+    return starts ? min(max(starts[b], 0), max(L, 0)) : 0;
+}
+__device__ __forceinline__ int first_tile_at(int L, int T, int q_len, int window,
+                                             const int32_t* starts, int b) {
+    return max(first_tile_of(L, T, q_len, window), start_of(starts, b, L) / T);
+}
+
+// Tiles of T tokens sequence b of length L walks (0 for L == 0 or a length out
 // of range).
 __device__ __forceinline__ int tiles_of(int L, int max_blocks, int block_size, int T, int q_len,
-                                        int window) {
+                                        int window, const int32_t* starts = nullptr, int b = 0) {
     if (!seq_len_ok(L, max_blocks, block_size) || L == 0) return 0;
-    return (L + T - 1) / T - first_tile_of(L, T, q_len, window);
+    return (L + T - 1) / T - first_tile_at(L, T, q_len, window, starts, b);
 }
 
 __device__ __forceinline__ int64_t span_begin(int64_t c, int64_t N, int64_t P) {
@@ -118,7 +129,8 @@ __device__ inline void find_span_start(const int32_t* __restrict__ seq_lens, int
                                        int T, int q_len, int window, int max_blocks,
                                        int block_size, int64_t parts, int min_tiles,
                                        int64_t* scratch, SpanStart* out,
-                                       int64_t* __restrict__ tile_base_out, int run_cost = 0) {
+                                       int64_t* __restrict__ tile_base_out, int run_cost = 0,
+                                       const int32_t* starts = nullptr) {
     const int nt = blockDim.x;  // a multiple of 32
     const int tid = threadIdx.x;
     const int lane = tid & 31, warp = tid >> 5, nwarps = nt >> 5;
@@ -128,10 +140,13 @@ __device__ inline void find_span_start(const int32_t* __restrict__ seq_lens, int
     // tiles per unit of this thread's sequences (the first one kept: one
     // sequence per thread whenever B <= blockDim.x)
     const int n_first =
-        b_lo < b_hi ? tiles_of(seq_lens[b_lo], max_blocks, block_size, T, q_len, window) : 0;
+        b_lo < b_hi
+            ? tiles_of(seq_lens[b_lo], max_blocks, block_size, T, q_len, window, starts, b_lo)
+            : 0;
     auto tiles_at = [&](int b) {
         return b == b_lo ? n_first
-                         : tiles_of(seq_lens[b], max_blocks, block_size, T, q_len, window);
+                         : tiles_of(seq_lens[b], max_blocks, block_size, T, q_len, window,
+                                    starts, b);
     };
     // both prefixes in one scan: real tiles, and virtual tiles with the cost
     int64_t real_loc = 0, virt_loc = 0;
@@ -267,13 +282,14 @@ __device__ inline TileCursor cursor_at_tile(int64_t x, int b, int64_t b_base,
 // Cursor at the span's first real tile (the position find_span_start found).
 __device__ inline TileCursor cursor_at(const SpanStart& s, const int32_t* seq_lens, int units,
                                        int T, int q_len, int window, int max_blocks,
-                                       int block_size, int run_cost = 0) {
+                                       int block_size, int run_cost = 0,
+                                       const int32_t* starts = nullptr) {
     (void)units;
     TileCursor c;
     c.b = s.b;
     const int L = seq_lens[s.b];
-    c.n_b = tiles_of(L, max_blocks, block_size, T, q_len, window);
-    c.first = first_tile_of(L, T, q_len, window);
+    c.n_b = tiles_of(L, max_blocks, block_size, T, q_len, window, starts, s.b);
+    c.first = first_tile_at(L, T, q_len, window, starts, s.b);
     c.unit = s.unit;
     c.i = s.i;
     c.run_start = s.b_base + (int64_t)s.unit * (c.n_b + run_cost) + run_cost;
@@ -285,7 +301,7 @@ __device__ inline TileCursor cursor_at(const SpanStart& s, const int32_t* seq_le
 // starts run_cost virtual slots after this run's end.
 __device__ inline void cursor_next(TileCursor& c, const int32_t* seq_lens, int B, int units,
                                    int T, int q_len, int window, int max_blocks, int block_size,
-                                   int run_cost = 0) {
+                                   int run_cost = 0, const int32_t* starts = nullptr) {
     if (++c.i < c.n_b) return;
     c.run_start += c.n_b + run_cost;
     c.i = 0;
@@ -293,11 +309,11 @@ __device__ inline void cursor_next(TileCursor& c, const int32_t* seq_lens, int B
     c.unit = 0;
     int nb = 0;
     while (++c.b < B) {
-        nb = tiles_of(seq_lens[c.b], max_blocks, block_size, T, q_len, window);
+        nb = tiles_of(seq_lens[c.b], max_blocks, block_size, T, q_len, window, starts, c.b);
         if (nb > 0) break;
     }
     c.n_b = nb;
-    if (c.b < B) c.first = first_tile_of(seq_lens[c.b], T, q_len, window);
+    if (c.b < B) c.first = first_tile_at(seq_lens[c.b], T, q_len, window, starts, c.b);
 }
 
 // Segment flags for the piece of (b, unit) a CTA holds.

@@ -99,6 +99,18 @@ struct DecodeArgs {
                            // in use and the run cost
     float* part_o;         // [num_parts][2][hg * group][d] normalised partial outputs
     float* part_lse;       // [num_parts][2][hg * group]    partial log2-sum-exp
+    // shaped scores and shared prefixes (the EX kernels; null or 0 where not asked for)
+    float cap, cap_inv;    // soft cap of the scores in base-2 units, and 1 over it; 0: none
+    const float* slopes;   // [hq] natural units a token of distance, device
+    const int32_t* starts; // [B] token that a sequence is walked from (its shared prefix
+                           // lies before), device
+    int join;              // split runs are left to launch_join
+    float* row_o;          // [B * q_len * hq][d] and [B * q_len * hq]: runs that were not
+    float* row_lse;        // split, for launch_join; null: they are written to out
+    // parts of the shared prefixes, for launch_join: prefix_parts(start, prefix_splits) a row
+    int prefix_splits;
+    const float* pre_o;    // [prefix_splits][B * q_len * hq][d]
+    const float* pre_lse;  // [prefix_splits][B * q_len * hq]
 };
 
 // The launch plan of a decode call, from shapes alone.
@@ -127,6 +139,18 @@ int check_decode(const Pool& p, const void* q, int B, int q_len, int Hq,
                  float scale, const void* out, const void* workspace, size_t workspace_bytes,
                  int num_splits, Plan* plan, WorkspaceLayout* wl);
 
+// The kernels' arguments of a call that check_decode passed (softcap 0 and slopes null: plain
+// scores).
+DecodeArgs decode_args(const Pool& p, const void* q, int B, int q_len, int Hq,
+                       const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
+                       int window, float scale, float softcap, const float* slopes, void* out,
+                       void* workspace, int num_splits, const Plan& plan,
+                       const WorkspaceLayout& wl);
+
+// Spans num_splits = 0 resolves to, and the next multiple of a.
+int resolve_parts(const Pool& p, int num_splits);
+inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
 // KV heads per unit of work for this pool and rows per KV head.
 int choose_hg(const Pool& p, int rows);
 
@@ -138,5 +162,8 @@ cudaError_t launch_decode_simple(const DecodeArgs& a, int dtype, cudaStream_t s)
 cudaError_t launch_decode_tma(const DecodeArgs& a, const Pool& p, cudaStream_t s);
 cudaError_t launch_merge(const DecodeArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_merge_runs(const DecodeArgs& a, cudaStream_t s);
+// Decode with shaped scores or shared prefixes, and the join of what it leaves.
+cudaError_t launch_decode_ex(const DecodeArgs& a, const Pool& p, cudaStream_t s);
+cudaError_t launch_join(const DecodeArgs& a, cudaStream_t s);
 
 }  // namespace pgd

@@ -1,0 +1,28 @@
+// The soft cap of attention scores, c tanh(s / c), for scores in any unit.
+//
+// Below half the cap an odd polynomial in x = s / c, whose relative error is 2^-23 (a fit of
+// tanh(x) / x in x^2 on [0, 1/4], smallest largest relative error, by exchange: 2^-26 before
+// its coefficients are rounded), above it 1 - 2 / (1 + e^2|x|), whose error of 2^-22 is that of
+// a value of 0.46 or more.  So the result is within a few 2^-22 of its own size, however
+// large the cap; a NaN stays one.
+#pragma once
+
+#include <stdint.h>
+
+namespace pgd {
+
+__device__ __forceinline__ float capped(float s, float cap, float inv) {
+    const float x = s * inv, z = x * x;
+    float p = fmaf(z, 0.017135007f, -0.052986074f);
+    p = fmaf(p, z, 0.13324779f);
+    p = fmaf(p, z, -0.33333069f);
+    p = fmaf(p * z, x, x);
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(x) * 2.8853900817779268f));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    const float big = copysignf(fmaf(-2.f, r, 1.f), x);
+    return cap * (fabsf(x) < 0.5f ? p : big);
+}
+
+}  // namespace pgd

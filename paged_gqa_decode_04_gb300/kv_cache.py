@@ -181,6 +181,16 @@ def _empty_on(pool, stream, shape):
         return torch.empty(shape, dtype=pool.q_dtype, device=pool.device)
 
 
+def _zeros_on(pool, stream, nbytes):
+    """A zero-filled workspace allocated and cleared on the launching stream."""
+    if stream is None:
+        return torch.zeros(nbytes, dtype=torch.uint8, device=pool.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=pool.device)
+    with torch.cuda.stream(stream):
+        return torch.zeros(nbytes, dtype=torch.uint8, device=pool.device)
+
+
 def paged_kv_write(pool, k, v, cu_seqlens, block_table, seq_lens, stream=None):
     """Store the new tokens of a ragged batch in the pages, quantised as they are
     written.
@@ -281,8 +291,21 @@ def paged_qk_norm_rope_write(pool, q, k, v, cu_seqlens, block_table, seq_lens, q
     return q_out
 
 
+def _slopes_ptr(pool, slopes, heads):
+    """The pointer of distance slopes [Hq], or None."""
+    if slopes is None:
+        return None
+    if slopes.dim() != 1 or slopes.shape[0] != heads or not slopes.is_contiguous():
+        raise ValueError("slopes must be a contiguous [%d]" % heads)
+    if slopes.dtype is not torch.float32:
+        raise TypeError("slopes must be float32")
+    if slopes.get_device() != pool.device.index:
+        raise ValueError("slopes must be on the pool's device")
+    return slopes.data_ptr() if heads else None
+
+
 def paged_gqa_attend(pool, q, cu_seqlens, block_table, seq_lens, scale, causal=True, window=0,
-                     out=None, stream=None):
+                     out=None, stream=None, softcap=0.0, slopes=None, visible=None):
     """Attention of a ragged batch of query tokens over the pages.
 
     q [total, Hq, D] bfloat16 (rows may be a view of a packed projection): rows
@@ -292,6 +315,11 @@ def paged_gqa_attend(pool, q, cu_seqlens, block_table, seq_lens, scale, causal=T
     attends to all seq_lens[b] cached tokens: cross attention.  Returns out
     [total, Hq, D]; rows past cu_seqlens[B] are left as they were.  Sums are float32, the
     weights that V is multiplied with bfloat16 (f16 over 8-bit pages, see paged_gqa.h).
+
+    Shaped scores: softcap > 0 takes s to softcap * tanh(s / softcap); slopes [Hq] float32
+    then subtract slopes[h] * |p - t| (query i of n at p = seq_lens[b] - n + i); visible
+    [total, 2] int32 lets a row see tokens [first, end) alone, of those it would see without
+    (packed documents; with causal=False a prefix that all rows see: [0, max(p + 1, prefix))).
     """
     B = _check_tables(pool, cu_seqlens, block_table, seq_lens)
     if q.dim() != 3:
@@ -304,8 +332,79 @@ def paged_gqa_attend(pool, q, cu_seqlens, block_table, seq_lens, scale, causal=T
     if not out.is_contiguous():
         raise ValueError("out must be contiguous")
     window = min(max(int(window), -1), 2 ** 31 - 1)   # none there is longer; C takes an int
-    _check(_lib.load().paged_gqa_attend(
+    v_ptr = None
+    if visible is not None:
+        if visible.dim() != 2 or tuple(visible.shape) != (total, 2) or \
+                not visible.is_contiguous():
+            raise ValueError("visible must be a contiguous [total, 2]")
+        if visible.dtype is not torch.int32:
+            raise TypeError("visible must be int32")
+        if visible.get_device() != pool.device.index:
+            raise ValueError("visible must be on the pool's device")
+        v_ptr = visible.data_ptr() if total else None
+    _check(_lib.load().paged_gqa_attend_shaped(
         pool.handle, q.data_ptr(), qs, total, Hq, cu_seqlens.data_ptr(), B,
         block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), int(bool(causal)),
-        window, float(scale), out.data_ptr(), _stream_on(pool, stream)), "paged_gqa_attend")
+        window, float(scale), float(softcap), _slopes_ptr(pool, slopes, Hq), v_ptr,
+        out.data_ptr(), _stream_on(pool, stream)), "paged_gqa_attend")
+    return out
+
+
+def paged_gqa_workspace_size_shared(pool, B, q_len, Hq, num_groups):
+    n = ctypes.c_size_t()
+    _check(_lib.load().paged_gqa_workspace_size_shared(
+        pool.handle, int(B), int(q_len), int(Hq), int(num_groups), ctypes.byref(n)),
+        "paged_gqa_workspace_size_shared")
+    return n.value
+
+
+def alloc_workspace_shared(pool, B, q_len, Hq, num_groups):
+    """A zero-filled workspace for paged_gqa_decode_shared, reusable call after call."""
+    n = paged_gqa_workspace_size_shared(pool, B, q_len, Hq, num_groups)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=pool.device)
+
+
+def paged_gqa_decode_shared(pool, q, cu_groups, shared_lens, block_table, seq_lens, scale,
+                            softcap=0.0, slopes=None, out=None, workspace=None, stream=None):
+    """Decode of sequences that share prefixes in groups, as forks of one prompt do.
+
+    q [B, Hq, D] or [B, q_len, Hq, D] bfloat16: the last tokens of each sequence, as for
+    paged_gqa_decode_ex.  Sequences cu_groups[g] .. cu_groups[g+1]-1 (int32 [groups + 1])
+    are group g; their first shared_lens[g] (int32 [groups]) cached tokens are the same, and
+    are read once for the group, through the table row of one of its sequences.  softcap and
+    slopes as for paged_gqa_attend.  Returns out, shaped like q.
+    """
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [B, Hq, D] or [B, q_len, Hq, D]")
+    if q.dtype is not pool.q_dtype:
+        raise TypeError("q must be %s for this pool" % pool.q_dtype)
+    B, Hq, q_len = q.shape[0], q.shape[-2], q.shape[1] if q.dim() == 4 else 1
+    for name, t, dims in (("cu_groups", cu_groups, 1), ("shared_lens", shared_lens, 1),
+                          ("block_table", block_table, 2), ("seq_lens", seq_lens, 1)):
+        if t.dim() != dims or t.dtype is not torch.int32 or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous int32 tensor of %d dimensions"
+                             % (name, dims))
+    groups = shared_lens.shape[0]
+    if (q.shape[-1] != pool.head_dim or cu_groups.shape[0] != groups + 1 or
+            block_table.shape[0] != B or seq_lens.shape[0] != B):
+        raise ValueError("shape mismatch between q, groups, tables and pool")
+    if out is None:
+        out = _empty_on(pool, stream, tuple(q.shape))
+    if out.shape != q.shape or out.dtype is not q.dtype:
+        raise ValueError("out must be shaped and typed like q")
+    for t in (q, out, cu_groups, shared_lens, block_table, seq_lens):
+        if t.get_device() != pool.device.index or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous and on the pool's device")
+    sl = _slopes_ptr(pool, slopes, Hq)
+    if workspace is None:
+        workspace = _zeros_on(pool, stream, max(paged_gqa_workspace_size_shared(
+            pool, B, q_len, Hq, groups), 256))
+    if workspace.get_device() != pool.device.index or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the pool's device")
+    _check(_lib.load().paged_gqa_decode_shared(
+        pool.handle, q.data_ptr(), B, q_len, Hq, cu_groups.data_ptr(), shared_lens.data_ptr(),
+        groups, block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), float(scale),
+        float(softcap), sl, out.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_on(pool, stream)),
+        "paged_gqa_decode_shared")
     return out
