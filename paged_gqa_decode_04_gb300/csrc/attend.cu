@@ -91,8 +91,7 @@ extern "C" int paged_gqa_attend_shaped(pgd_pool_t pool, const void* q, int64_t q
     t.pieces = int(pieces);
     t.k_scale = p.k_scale;
     t.v_scale = p.v_scale;
-    t.cap = softcap * kLog2e;
-    t.cap_inv = softcap > 0.f ? 1.f / t.cap : 0.f;
+    attend::set_cap(t, softcap * kLog2e);
     t.slopes = slopes;
     t.visible = reinterpret_cast<const int2*>(visible);
     const bool shaped = softcap > 0.f || slopes || visible;

@@ -66,8 +66,10 @@ cudaError_t launch_shaped(Args& a, const Pool& p, const PageMaps& maps, cudaStre
     if (a.slopes)
         return a.cap > 0.f ? launch<D, PAGE, PB, kShaped | kCap | kBias>(a, p, maps, s)
                            : launch<D, PAGE, PB, kShaped | kBias>(a, p, maps, s);
-    return a.cap > 0.f ? launch<D, PAGE, PB, kShaped | kCap>(a, p, maps, s)
-                       : launch<D, PAGE, PB, kShaped>(a, p, maps, s);
+    if (a.cap == 0.f) return launch<D, PAGE, PB, kShaped>(a, p, maps, s);
+    if constexpr (PAGE == PGD_BF16)
+        if (a.cap <= kFixedMost) return launch<D, PAGE, PB, kShaped | kCap | kFixed>(a, p, maps, s);
+    return launch<D, PAGE, PB, kShaped | kCap>(a, p, maps, s);
 }
 
 // launch or launch_shaped for the pool's pages.

@@ -116,6 +116,7 @@ struct Args {
     const float* v_scale;
     // kShaped kernels
     float cap, cap_inv;     // soft cap of the scores in base-2 units, and 1 over it
+    float2 cap_poly[6];     // cap tanh(x) / x as a polynomial in x^2 (set_cap), each term twice
     const float* slopes;    // [hq], natural units a token of distance
     const int2* visible;    // [total] tokens [first, end) that a row may see; null: all
     // shared prefixes: r.cu, r.B, r.total are groups of sequences (cu[g] .. cu[g+1] - 1 are
@@ -130,7 +131,12 @@ struct Args {
 
 // What a kernel does beside the plain attention: kShaped rows with a visible range of their own
 // and shared prefixes; with kCap and kBias besides, scores capped and less slope * distance.
-constexpr int kShaped = 1, kCap = 2, kBias = 4;
+// kFixed: capped, and weights relative to a quarter of the cap instead of the row's maximum, which
+// then need not be found (4 prompts of up to 4096, 32/8 heads: 480 -> 400 us).  For bfloat16 pages
+// and caps up to kFixedMost base-2 units: weights are between 2^-100 and 2^60, where bfloat16 and
+// float32 are as precise as near 1, and sums over 2^31 tokens stay finite for values below 2^36.
+constexpr int kShaped = 1, kCap = 2, kBias = 4, kFixed = 8;
+constexpr float kFixedMost = 80.f;
 
 template <int D, int PAGE, bool PB>
 struct Layout {
@@ -156,6 +162,21 @@ struct Layout {
     static constexpr int kProducers = kQ8 ? 2 : 4;
     static constexpr int kColumns = kQ8 ? 1 : kHalves;
 };
+
+// A polynomial P with x P(x^2) = tanh(x) to 6.7e-7 of its size for |x| below 1: a fit of
+// smallest largest relative error, by exchange, with P(0) = 1 so that small scores stay what they
+// are.  A score under a cap of 50 is off by 4e-5 in units of log 2 at most.  (Three terms do
+// below 0.32 and take 416 us instead of 480, but choosing between the two tile by tile 617: the
+// loop's code has to stay one.  4 prompts of up to 4096, 32/8 heads.)
+constexpr int kTerms = 6;
+inline void set_cap(Args& a, float cap) {
+    const double c[kTerms] = {1, -0.33330279671319310, 0.13288490272548903,
+                              -0.051768285513206420, 0.016906408736806840,
+                              -0.0031265776866605624};
+    a.cap = cap;
+    a.cap_inv = cap > 0.f ? 1.f / cap : 0.f;
+    for (int i = 0; i < kTerms; ++i) a.cap_poly[i].x = a.cap_poly[i].y = float(c[i] * cap);
+}
 
 // The keys a block of rows sees: tiles [t0, t1), and which of them every row sees whole.
 struct Span {
@@ -260,13 +281,14 @@ __device__ __forceinline__ bool valid(const Ragged& r, int id) {
 // A page, tokens [t, t + n), has a block id out of range: the rows of the piece that see it are
 // marked in `lost`, a bit a row, to become NaN.  Apart from the kernel's own code, whose loops it
 // would slow down (2048 of 8192 tokens over bfloat16 pages, 64/8 heads: 337 -> 356 us).
-static __device__ __noinline__ void mark_lost(const Args& a, const Seq& s, int row0, int t, int n,
+template <bool kRanges>
+__device__ __noinline__ void mark_lost(const Args& a, const Seq& s, int row0, int t, int n,
                                        uint32_t* lost) {
     for (int r = 0; r < 1 << kRowShift; ++r) {
         const int pos = s.len - s.n + (row0 + r) / a.group;
         int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
         int hi = a.causal ? pos + 1 : s.len;
-        if (a.visible) {
+        if (kRanges && a.visible) {
             const int2 v = (row0 + r) / a.group < s.n ? row_range(a, s, row0 + r) : make_int2(0, 0);
             lo = v.x, hi = v.y;
         }
@@ -297,6 +319,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
     return m;
 }
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float m;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+__device__ __forceinline__ float max8_abs(const uint32_t* x) {
+    const float a =
+        max3_abs(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+    const float b =
+        max3_abs(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
+    return max3_abs(max3_abs(a, b, __uint_as_float(x[6])), __uint_as_float(x[7]), 0.f);
+}
 __device__ __forceinline__ float max8(const uint32_t* x) {
     const float a = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
     const float b = max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
@@ -313,6 +347,11 @@ __device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -594,7 +633,281 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (PB) wait_st();  // a tile may rescale twice, for the gain and for the maximum
             };
             const int first = p.t0 + (paired ? blk : 0), by = paired ? 2 : 1;  // its tiles
+            // weights of half h of a tile, over the scores that they came from
+            auto hand_over = [&](int h, const uint32_t (&w)[kTile / 4]) {
+                tmem_st32(ts + h * (kTile / 4), w);
+                wait_st();
+                fence_before();
+                warp_arrive(bar_p + 16 * blk + 8 * h);
+            };
             constexpr bool kShape = (MOD & (kCap | kBias)) != 0;
+            // cap tanh(x) + add for a pair, |x| < 1
+            auto capped2 = [&](uint64_t x, uint64_t add) {
+                const uint64_t z = mul2(x, x);
+                uint64_t p = pair(a.cap_poly[kTerms - 1].x, a.cap_poly[kTerms - 1].y);
+#pragma unroll
+                for (int i = kTerms - 2; i >= 0; --i)
+                    p = fma2(p, z, pair(a.cap_poly[i].x, a.cap_poly[i].y));
+                return fma2(x, p, add);
+            };
+            // the whole tile in place, for scores beyond the cap
+            auto cap_in_place = [&](uint32_t (&x)[kTile], const float4* sc) {
+#pragma unroll
+                for (int i = 0; i < kTile; ++i)
+                    x[i] = __float_as_uint(capped(
+                        __uint_as_float(x[i]) * (PB ? sc[i / 8].x : scale), a.cap, a.cap_inv));
+            };
+            // all of the warp's scores are below the cap (NaN counts as beyond)
+            auto reaches = [&](float big) { return __all_sync(0xffffffffu, big < 1.f); };
+            // the row's maximum has grown too far in some row: the reference moves
+            auto move_reference = [&](float now, bool any) {
+                const bool over = now > m + kGrow;
+                const bool grown = __any_sync(0xffffffffu, over);
+                if (grown) {
+                    float keep = 1.f;
+                    if (over) {
+                        keep = m == -INFINITY ? 0.f : ex2(m - now);
+                        l *= keep;
+                        m = now;
+                    }
+                    if (any) rescale(keep);
+                }
+                return grown;
+            };
+            // sums and 16 bits of 8 weights
+            auto take = [&](int h, int g, const uint32_t* x, uint32_t* w, uint64_t* sum,
+                            const float4* sc) {
+                uint64_t part = 0;
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float e0 = __uint_as_float(x[i]), e1 = __uint_as_float(x[i + 1]);
+                    if (PB)
+                        part = i == 0 ? pair(e0, e1) : add2(part, pair(e0, e1));
+                    else
+                        sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(e0, e1));
+                    w[g * 4 + i / 2] = operand2<PAGE>(e0, e1);
+                }
+                if (PB) {
+                    const float over = sc[h * 8 + g].z;
+                    sum[g & 1] = fma2(part, pair(over, over), sum[g & 1]);
+                }
+            };
+            auto scores_of = [&](uint32_t (&x)[kTile]) {
+#pragma unroll
+                for (int i = 0; i < kTile; i += 32) tmem_ld32(ts + i, x + i);
+                wait_ld();
+#pragma unroll
+                for (int i = 0; i < kTile; i += 32) keep32(x + i);
+            };
+            // A tile of capped scores.  Relative to the row's maximum (the cap keeps the scores'
+            // order), that and the largest magnitude are found first, so that nothing is done
+            // twice; relative to a fixed reference the magnitude along with the first half, which
+            // is done again where a score is beyond the cap.
+            // Limit: of the 1024 cycles that the products leave each of a quarter's two warps a
+            // tile, the polynomial takes 2 multiplications and 6 multiply-adds of 2 to 3 cycles
+            // each for a pair of elements, the reference being the last one's addend.
+            auto capped_tile = [&](int j, auto edge, uint32_t (&x)[kTile],
+                                   uint32_t (&w)[kTile / 4], uint64_t (&sum)[2],
+                                   const float4* sc) {
+                constexpr bool kEdge = decltype(edge)::value;
+                constexpr bool kFix = (MOD & kFixed) != 0;
+                const int t0 = tile_at(j) * kTile, from = my_lo - t0, until = my_hi - t0;
+                auto hidden = [&](int i) { return kEdge && (i < from || i >= until); };
+                auto seen = [&](int i, float none) {
+                    return hidden(i) ? none : __uint_as_float(x[i]);
+                };
+                scores_of(x);
+                bool below = true;
+                if constexpr (!kFix) {
+                    float tops[4], bigs[4];
+#pragma unroll
+                    for (int g = 0; g < kTile / 8; ++g) {
+                        const float mul = PB ? sc[g].x : 1.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int k = g * 8 + i;
+                            tops[i] = max3(g == 0 ? -INFINITY : tops[i],
+                                           seen(k, -INFINITY) * mul, seen(k + 4, -INFINITY) * mul);
+                            bigs[i] = max3_abs(g == 0 ? 0.f : bigs[i], seen(k, 0.f) * mul,
+                                               seen(k + 4, 0.f) * mul);
+                        }
+                    }
+                    const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
+                    const float by = PB ? 1.f : scale;
+                    below = reaches(max3(fmaxf(bigs[0], bigs[1]), bigs[2], bigs[3]) *
+                                    (by * a.cap_inv));
+                    move_reference(top == -INFINITY ? top : capped(top * by, a.cap, a.cap_inv),
+                                   j > first);
+                }
+                float off = kFix ? -0.25f * a.cap : m == -INFINITY ? 0.f : -m;
+                if (kQ8 && !PB) off += kLift;
+                float big = 0.f;
+                // the weights of half h
+                auto weigh = [&](int h, auto exponents) {
+                    float bigs[4];
+#pragma unroll
+                    for (int g = 0; g <= 8; ++g) {
+                        const int at = h * (kTile / 2) + g * 8;
+                        if (g < 8) {
+                            if (kFix && h == 0) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    bigs[i % 4] =
+                                        max3_abs(g == 0 && i < 4 ? 0.f : bigs[i % 4],
+                                                 seen(at + i, 0.f), seen(kTile / 2 + at + i, 0.f));
+                            }
+                            const float mul = PB ? sc[at / 8].x : scale;
+                            const float add = PB ? off + sc[at / 8].y : off;
+#pragma unroll
+                            for (int i = at; i < at + 8; i += 2) {
+                                float e0, e1;
+                                unpair(exponents(pair(__uint_as_float(x[i]),
+                                                      __uint_as_float(x[i + 1])),
+                                                 mul * a.cap_inv, pair(add, add)),
+                                       e0, e1);
+                                x[i] = hidden(i) ? 0 : __float_as_uint(ex2(e0));
+                                x[i + 1] = hidden(i + 1) ? 0 : __float_as_uint(ex2(e1));
+                            }
+                        }
+                        if (g > 0) take(h, g - 1, x + at - 8, w, sum, sc);
+                    }
+                    if (kFix && h == 0)
+                        big = max3(fmaxf(bigs[0], bigs[1]), bigs[2], bigs[3]) *
+                              (scale * a.cap_inv);
+                };
+                auto by_polynomial = [&](uint64_t y, float k, uint64_t add) {
+                    return capped2(mul2(y, pair(k, k)), add);
+                };
+                auto as_they_are = [&](uint64_t y, float, uint64_t add) { return add2(y, add); };
+                sum[0] = sum[1] = 0;
+                if (below) {
+                    weigh(0, by_polynomial);
+                    below = !kFix || reaches(big);
+                    if (below) {
+                        hand_over(0, w);
+                        weigh(1, by_polynomial);
+                        hand_over(1, w);
+                    } else {
+                        scores_of(x);
+                    }
+                }
+                if (!below) {
+                    cap_in_place(x, sc);
+                    sum[0] = sum[1] = 0;
+                    weigh(0, as_they_are);
+                    hand_over(0, w);
+                    weigh(1, as_they_are);
+                    hand_over(1, w);
+                }
+                if (kFix) m = 0.25f * a.cap;
+            };
+            // A tile of scores with a bias: the second half's exponents are formed along with the
+            // first half's weights, so that the largest of all is known before any weight is
+            // handed over.  For tokens before the row's own the bias is a straight line,
+            // slope * i + c, with the reference in c.
+            auto biased_tile = [&](int j, auto edge, uint32_t (&x)[kTile],
+                                   uint32_t (&w)[kTile / 4], uint64_t (&sum)[2],
+                                   const float4* sc) {
+                constexpr bool kEdge = decltype(edge)::value;
+                const int t0 = tile_at(j) * kTile, from = my_lo - t0, until = my_hi - t0;
+                const float far = float(t0 - pos);
+                float top, big;
+                auto turn_to_weights = [&](int at) {
+#pragma unroll
+                    for (int i = at; i < at + 8; ++i)
+                        x[i] = __float_as_uint(ex2(__uint_as_float(x[i])));
+                };
+                auto first_half = [&](auto polynomial, auto straight) {
+                    constexpr bool kPoly = decltype(polynomial)::value;
+                    float off = m == -INFINITY ? 0.f : -m;
+                    if (kQ8 && !PB) off += kLift;
+                    const float c = fmaf(slope, far, off);
+                    top = -INFINITY;
+                    if (kPoly) big = 0.f;
+                    uint64_t line[4];  // slope times 0 .. 7
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        line[i] = pair(slope * float(2 * i), slope * float(2 * i + 1));
+                    auto exponents_of = [&](int at) {  // of the 8 scores from `at` on
+                        const float mul = PB ? sc[at / 8].x : scale;
+                        const float k = kPoly ? mul * a.cap_inv : mul;
+                        const float lift = PB ? sc[at / 8].y : 0.f;
+                        if (kPoly) {
+                            const float u = max8_abs(x + at);
+                            big = fmaxf(big, PB ? u * mul : u);
+                        }
+                        const float cl = fmaf(slope, float(at), c) + lift, ol = off + lift;
+                        const uint64_t kk = pair(k, k), cc = pair(cl, cl);
+#pragma unroll
+                        for (int i = at; i < at + 8; i += 2) {
+                            const uint64_t r = pair(__uint_as_float(x[i]),
+                                                    __uint_as_float(x[i + 1]));
+                            const uint64_t b =
+                                decltype(straight)::value
+                                    ? add2(line[(i - at) / 2], cc)
+                                    : pair(fmaf(-slope, fabsf(far + float(i)), ol),
+                                           fmaf(-slope, fabsf(far + float(i + 1)), ol));
+                            float y0, y1;
+                            if constexpr (kPoly)
+                                unpair(capped2(mul2(r, kk), b), y0, y1);
+                            else if constexpr ((MOD & kCap) != 0)  // capped before
+                                unpair(add2(r, b), y0, y1);
+                            else
+                                unpair(fma2(r, kk, b), y0, y1);
+                            if (kEdge && (i < from || i >= until)) y0 = -INFINITY;
+                            if (kEdge && (i + 1 < from || i + 1 >= until)) y1 = -INFINITY;
+                            x[i] = __float_as_uint(y0);
+                            x[i + 1] = __float_as_uint(y1);
+                        }
+                        const float u = max8(x + at);
+                        top = fmaxf(top, PB ? u - lift : u);
+                    };
+#pragma unroll
+                    for (int g = 0; g <= 8; ++g) {
+                        if (g < 8) {
+                            exponents_of(g * 8);
+                            exponents_of(kTile / 2 + g * 8);
+                            turn_to_weights(g * 8);
+                        }
+                        if (g > 0) take(0, g - 1, x + g * 8 - 8, w, sum, sc);
+                    }
+                    if (kPoly) big *= PB ? a.cap_inv : scale * a.cap_inv;
+                    top -= off;
+                };
+                [[maybe_unused]] bool below = true;
+                for (;;) {
+                    scores_of(x);
+                    if (kEdge && (MOD & kCap)) {  // what a row does not see need not be below
+#pragma unroll
+                        for (int i = 0; i < kTile; ++i)
+                            if (i < from || i >= until) x[i] = 0;
+                    }
+                    sum[0] = sum[1] = 0;
+                    if constexpr ((MOD & kCap) != 0) {
+                        if (below) {
+                            first_half(std::true_type(), std::false_type());
+                            below = reaches(big);
+                            if (!below) continue;
+                        } else {
+                            cap_in_place(x, sc);
+                            first_half(std::false_type(), std::false_type());
+                        }
+                    } else if (__all_sync(0xffffffffu, a.causal || t0 + kTile - 1 <= pos)) {
+                        first_half(std::false_type(), std::true_type());
+                    } else {
+                        first_half(std::false_type(), std::false_type());
+                    }
+                    if (!move_reference(top, j > first)) break;
+                }
+                hand_over(0, w);
+#pragma unroll
+                for (int g = 0; g <= 8; ++g) {
+                    const int at = kTile / 2 + g * 8;
+                    if (g < 8) turn_to_weights(at);
+                    if (g > 0) take(1, g - 1, x + at - 8, w, sum, sc);
+                }
+                hand_over(1, w);
+            };
             // One tile of scores; `edge`: some row does not see all of it.
             auto tile = [&](int j, auto edge) {
                 uint32_t x[kTile], w[kTile / 4];
@@ -621,12 +934,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int g = 0; g <= 8; ++g) {
                         const int at = h * (kTile / 2) + g * 8;
-                        const float mul = kShape ? 1.f : PB && g < 8 ? sc[h * 8 + g].x : scale;
+                        const float mul = PB && g < 8 ? sc[h * 8 + g].x : scale;
                         const float add = PB && g < 8 ? off + sc[h * 8 + g].y : off;
                         const uint64_t cc = pair(mul, mul), mm = pair(add, add);
                         if (g < 8) {
-                            if (kShape) {  // the maximum is known
-                            } else if (h == 0 && PB) {
+                            if (h == 0 && PB) {
                                 float u = max8(x + g * 8) * sc[g].x;
                                 float v = max8(x + kTile / 2 + g * 8) * sc[8 + g].x;
                                 top[0] = g == 0 ? fmaxf(u, v) : max3(top[0], u, v);
@@ -672,42 +984,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // found; the tile is read again where that has grown too far.
                 bool grown;
                 if constexpr (kShape) {
-                    // Scores as they are asked for come first, then their maximum: the tile
-                    // would have to be shaped again if that were found with the weights.
-#pragma unroll
-                    for (int i = 0; i < kTile; i += 32) tmem_ld32(ts + i, x + i);
-                    wait_ld();
-#pragma unroll
-                    for (int i = 0; i < kTile; i += 32) keep32(x + i);
-                    const int t0 = tile_at(j) * kTile, from = my_lo - t0, until = my_hi - t0;
-                    const float far = float(t0 - pos);
-#pragma unroll
-                    for (int g = 0; g < kTile / 8; ++g) {
-                        const float mul = PB ? sc[g].x : scale;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int i = g * 8 + e;
-                            float y = __uint_as_float(x[i]) * mul;
-                            if (MOD & kCap) y = capped(y, a.cap, a.cap_inv);
-                            if (MOD & kBias) y = fmaf(-slope, fabsf(far + float(i)), y);
-                            if (decltype(edge)::value && (i < from || i >= until)) y = -INFINITY;
-                            x[i] = __float_as_uint(y);
-                        }
-                        const float u = max8(x + g * 8);
-                        top[0] = g == 0 ? u : fmaxf(top[0], u);
-                    }
-                    const bool over = top[0] > m + kGrow;
-                    if (__any_sync(0xffffffffu, over)) {
-                        float keep = 1.f;
-                        if (over) {
-                            keep = m == -INFINITY ? 0.f : ex2(m - top[0]);
-                            l *= keep;
-                            m = top[0];
-                        }
-                        if (j > first) rescale(keep);
-                    }
-                    sum[0] = sum[1] = 0;
-                    weigh(0);
+                    if constexpr ((MOD & kBias) != 0)
+                        biased_tile(j, edge, x, w, sum, sc);
+                    else
+                        capped_tile(j, edge, x, w, sum, sc);
                     grown = false;
                 } else do {
 #pragma unroll
@@ -740,16 +1020,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (j > first) rescale(keep);
                     }
                 } while (grown);
-                // the first half's product runs while the second half is computed
-                tmem_st32(ts, w);
-                wait_st();
-                fence_before();
-                warp_arrive(bar_p + 16 * blk);
-                weigh(1);
-                tmem_st32(ts + kTile / 4, w);
-                wait_st();
-                fence_before();
-                warp_arrive(bar_p + 16 * blk + 8);
+                if constexpr (!kShape) {
+                    // the first half's product runs while the second half is computed
+                    hand_over(0, w);
+                    weigh(1);
+                    hand_over(1, w);
+                }
                 float s0, s1;
                 unpair(add2(sum[0], sum[1]), s0, s1);
                 l += s0 + s1;
@@ -851,7 +1127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (__any_sync(0xffffffffu, gone)) {  // rare: the warp stays together beside it
                 if (gone) {
                     latch(a.r.err, PGD_ERR_BLOCK_ID);
-                    mark_lost(a, s, row0, tj * kTile + my_page * box, box, lost);
+                    mark_lost<MOD != 0>(a, s, row0, tj * kTile + my_page * box, box, lost);
                 }
                 __syncwarp();
             }
@@ -975,7 +1251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool ok = seen(j, page);
             if (ok && !valid(a.r, id)) {
                 latch(a.r.err, PGD_ERR_BLOCK_ID);
-                mark_lost(a, s, row0, tile_at(j) * kTile + page * box, box, lost);
+                mark_lost<MOD != 0>(a, s, row0, tile_at(j) * kTile + page * box, box, lost);
                 id = -1;  // outside the tensor: zeros
             }
             const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * box * 128;

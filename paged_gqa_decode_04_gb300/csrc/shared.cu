@@ -110,8 +110,7 @@ extern "C" int paged_gqa_decode_shared(pgd_pool_t pool, const void* q, int B, in
         t.pieces = int(pieces);
         t.k_scale = p.k_scale;
         t.v_scale = p.v_scale;
-        t.cap = a.cap;
-        t.cap_inv = a.cap_inv;
+        attend::set_cap(t, a.cap);
         t.slopes = slopes;
         t.shared = shared_lens;
         t.starts = starts;
