@@ -41,8 +41,14 @@ cudaError_t launch(Args& a, const Pool& p, const PageMaps& maps, cudaStream_t s)
         }
         fits[p.device].store(known);
     }
+    auto step = [&](int rows) { return make_int2(rows / a.group, rows % a.group); };
+    a.inv_group = 1.f / float(a.group);
+    a.q_step = step(kBlock / (D / 8));
+    a.o_step = step(32 / (D / 8));
+    auto join_step = [&]() { return step(a.cluster * 8 * (32 / (D / 4))); };
     if (MOD != 0 && a.shared) {  // one more CTA for the starts
         a.cluster = 1;
+        a.join_step = join_step();
         cfg.gridDim = dim3(1 + unsigned(a.pieces) * a.hkv * a.splits);
         cfg.numAttrs = 0;
         return cudaLaunchKernelEx(&cfg, attend_kernel<D, PAGE, PB, MOD>, a, maps.k, maps.v);
@@ -54,6 +60,7 @@ cudaError_t launch(Args& a, const Pool& p, const PageMaps& maps, cudaStream_t s)
     const double tile = PAGE == PGD_BF16 ? 1.2 : PB ? 1.75 : 1.5;
     a.cluster = choose_cluster(fit, (int64_t)a.pieces * a.hkv,
                                piece_tiles(a.r.max_len, a.window, a.group), few, tile);
+    a.join_step = join_step();
     attr[0].val.clusterDim.x = a.cluster;
     cfg.gridDim = dim3(unsigned(a.pieces) * a.hkv * a.cluster);
     cfg.numAttrs = a.cluster > 1 ? 1 : 0;

@@ -115,6 +115,9 @@ struct Args {
     const float* k_scale;   // 8-bit pages: [hkv], or [num_blocks][hkv]
     const float* v_scale;
     // kShaped kernels
+    float inv_group;        // 1 / group
+    int2 q_step, o_step;    // tokens and heads of the rows between two of a thread's
+    int2 join_step;
     float cap, cap_inv;     // soft cap of the scores in base-2 units, and 1 over it
     float2 cap_poly[6];     // cap tanh(x) / x as a polynomial in x^2 (set_cap), each term twice
     const float* slopes;    // [hq], natural units a token of distance
@@ -205,9 +208,41 @@ __device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int first, 
     return p;
 }
 
-// Tokens [x, y) that row R of a sequence sees, (0, 0) where that is none.
-__device__ __forceinline__ int2 row_range(const Args& a, const Seq& s, int R) {
-    const int i = R / a.group, pos = s.len - s.n + i;
+// Rows are counted (token, head of the group) from the piece's first, which is head `rem` of the
+// group of token `token`: the same for row r.  Exact: the sum is below 2^21, half a step off any
+// whole quotient, and the product's error is below that.
+struct First {
+    int token, rem;
+};
+__device__ __forceinline__ First row_at(const Args& a, const First& f, int r) {
+    const int x = f.rem + r, t = int((float(x) + 0.5f) * a.inv_group);
+    return {f.token + t, x - t * a.group};
+}
+// Where row r's vector is among rows of tokens `stride` elements apart, and the same for every
+// row a constant step further: no division and no product on the way.  (A softmax warp meets
+// this with one other on its quarter of the SM, so that each dependent operation counts.)
+struct Walk {
+    int64_t at, inc, wrap;
+    int head, group, dh;
+    __device__ __forceinline__ Walk(const Args& a, const First& f, int r, int2 step, int D,
+                                    int64_t stride)
+        : group(a.group), dh(step.y) {
+        const First x = row_at(a, f, r);
+        head = x.rem;
+        at = x.token * stride + head * D;
+        inc = step.x * stride + step.y * D;
+        wrap = stride - group * D;
+    }
+    __device__ __forceinline__ void next() {
+        at += inc;
+        head += dh;
+        if (head >= group) head -= group, at += wrap;
+    }
+};
+
+// Tokens [x, y) that the rows of token i of a sequence see, (0, 0) where that is none.
+__device__ __forceinline__ int2 row_range(const Args& a, const Seq& s, int i) {
+    const int pos = s.len - s.n + i;
     int lo = 0, hi = a.causal ? pos + 1 : s.len;
     if (a.window > 0) lo = max(0, pos - a.window + 1);
     if (a.visible) {
@@ -221,11 +256,11 @@ __device__ __forceinline__ int2 row_range(const Args& a, const Seq& s, int R) {
 // The same as span_of from the ranges of the rows themselves, which a warp looks at: rows
 // [first, first + 32) of the piece that are below `rows`.  A row that sees nothing does not
 // count; its scores are left as they come and the row becomes zeros at the end.
-__device__ __forceinline__ int4 range_of_warp(const Args& a, const Seq& s, int row0, int first,
-                                              int rows) {
+__device__ __forceinline__ int4 range_of_warp(const Args& a, const Seq& s, const First& f,
+                                              int first, int rows) {
     const int r = first + (threadIdx.x & 31);
     int2 v = make_int2(0, 0);
-    if (r < rows && s.ok) v = row_range(a, s, row0 + r);
+    if (r < rows && s.ok) v = row_range(a, s, row_at(a, f, r).token);
     const bool sees = v.y > v.x;
     return make_int4(__reduce_min_sync(0xffffffffu, sees ? v.x : INT32_MAX),
                      __reduce_max_sync(0xffffffffu, sees ? v.y : 0),
@@ -289,7 +324,8 @@ __device__ __noinline__ void mark_lost(const Args& a, const Seq& s, int row0, in
         int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
         int hi = a.causal ? pos + 1 : s.len;
         if (kRanges && a.visible) {
-            const int2 v = (row0 + r) / a.group < s.n ? row_range(a, s, row0 + r) : make_int2(0, 0);
+            const int i = (row0 + r) / a.group;
+            const int2 v = i < s.n ? row_range(a, s, i) : make_int2(0, 0);
             lo = v.x, hi = v.y;
         }
         if (lo < t + n && hi > t) atomicOr(lost + r / 32, 1u << r % 32);
@@ -486,11 +522,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rows = min(n * a.group - row0, 1 << kRowShift);
     if (rows <= 0) return;
 
+    First f = {0, 0};  // token and head of the piece's first row
+    if (MOD != 0) {
+        f.token = row0 / a.group;
+        f.rem = row0 - f.token * a.group;
+    }
     Span sp[2];
     if (MOD != 0 && a.visible) {
         int4* const of_warp = reinterpret_cast<int4*>(smem);  // before the queries come there
         if (warp < 8) {
-            const int4 v = range_of_warp(a, s, row0, warp * 32, rows);
+            const int4 v = range_of_warp(a, s, f, warp * 32, rows);
             if (lane == 0) of_warp[warp] = v;
         }
         __syncthreads();
@@ -556,6 +597,237 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int my_row = threadIdx.x % kBlock;
     const int at_row = (paired ? 0 : blk * kBlock) + my_row;  // in the piece
 
+    // Rows that are not shared by anyone are written as they are.  The others go through shared
+    // memory, unnormalised, and every CTA of the cluster joins a share of them.  Plain kernels
+    // do this with all warps, the others in the softmax warps, whose registers it needs: with
+    // those that all warps have left, 48, a piece's results took 6000 cycles.
+    const bool joins = a.cluster > 1 || paired || prefix;
+    auto results = [&]() {
+    const bool failed = *gave_up || !s.ok || (warp < 8 && lost[at_row / 32] >> lane & 1);
+    if (*gave_up && threadIdx.x == 0) latch(a.r.err, PGD_ERR_TIMEOUT);
+
+    // -------------------------------------------------------------------- results
+    const int64_t out_at = (int64_t)s.row0 * a.hq + (int64_t)head * a.group;  // head vectors
+    // what the accumulator is to be multiplied with beside 1 / l
+    const float by = !kQ8 ? 1.f : PB ? 1.f / vgain : __ldg(a.v_scale + head);
+    if (!joins) {
+        if (warp < 8) {
+            const uint32_t to = tmem + (uint32_t(warp % 4 * 32) << 16) + 2 * kTile + blk * D;
+            const float inv = failed ? NAN : l > 0.f ? by / l : l == 0.f ? 0.f : NAN;
+            const bool have = blk ? sp[1].t1 > sp[1].t0 : sp[0].t1 > sp[0].t0;
+            uint8_t* const rowp = smem + (blk * kBlock + my_row) * (D * 2);
+            if constexpr (MOD != 0) {
+                // a row that saw nothing, or that failed: its accumulator is not used
+                const bool none = l == 0.f && !failed, lost_row = inv != inv;
+#pragma unroll
+                for (int i = 0; i < D; i += 64) {
+                    uint32_t o[64];
+                    if (have) {
+                        tmem_ld32(to + i, o);
+                        tmem_ld32(to + i + 32, o + 32);
+                        wait_ld();
+                        keep32(o);
+                        keep32(o + 32);
+                    }
+                    const float by_row = none || lost_row ? 0.f : inv;
+                    const uint32_t fill = lost_row ? 0x7fc07fc0u : 0u;
+                    const bool whole = !(none || lost_row);
+#pragma unroll
+                    for (int e = 0; e < 64; e += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t y =
+                                bf16x2(__uint_as_float(o[e + 2 * k]) * by_row,
+                                       __uint_as_float(o[e + 2 * k + 1]) * by_row);
+                            w[k] = whole ? y : fill;
+                        }
+                        const int c = (i + e) / 8;
+                        *reinterpret_cast<uint4*>(rowp + ((c ^ my_row) & (D / 8 - 1)) * 16) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            } else
+#pragma unroll
+            for (int i = 0; i < D; i += 32) {
+                uint32_t o[32];
+                if (have) {
+                    tmem_ld32(to + i, o);
+                    wait_ld();
+                    keep32(o);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float y0 = __uint_as_float(o[e + 2 * k]) * inv;
+                        const float y1 = __uint_as_float(o[e + 2 * k + 1]) * inv;
+                        w[k] = l == 0.f && !failed ? 0u : inv != inv ? 0x7fc07fc0u : bf16x2(y0, y1);
+                    }
+                    const int c = (i + e) / 8;
+                    *reinterpret_cast<uint4*>(rowp + ((c ^ my_row) & (D / 8 - 1)) * 16) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            __syncwarp();
+            constexpr int kVecs = D / 8, kStep = 32 / kVecs;
+            const int c = lane % kVecs;
+            if constexpr (MOD != 0) {
+                const int r0 = warp * 32 + lane / kVecs;
+                Walk at(a, f, r0, a.o_step, D, (int64_t)a.hq * D);
+                __nv_bfloat16* const out = a.out + out_at * D + c * 8;
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i, at.next()) {
+                    const int r = r0 + i * kStep;
+                    if (r < rows)
+                        *reinterpret_cast<uint4*>(out + at.at) = *reinterpret_cast<const uint4*>(
+                            smem + r * (D * 2) + ((c ^ r) & (kVecs - 1)) * 16);
+                }
+            } else {
+                Rows at(row0 + warp * 32 + lane / kVecs, group, kStep);
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i, at.next()) {
+                    const int r = warp * 32 + lane / kVecs + i * kStep;
+                    if (r < rows)
+                        *reinterpret_cast<uint4*>(
+                            a.out + (out_at + at.token * a.hq + at.head) * D + c * 8) =
+                            *reinterpret_cast<const uint4*>(smem + r * (D * 2) +
+                                                            ((c ^ r) & (kVecs - 1)) * 16);
+                }
+            }
+        }
+    } else {
+        // unnormalised rows, maxima and sums to shared memory, then every CTA of the
+        // cluster joins a share of the rows
+        float2* const stat = reinterpret_cast<float2*>(smem);  // of the 256 rows
+        if (warp < 8) {
+            const uint32_t to = tmem + (uint32_t(warp % 4 * 32) << 16) + 2 * kTile + blk * D;
+            const bool have = blk ? sp[1].t1 > sp[1].t0 : sp[0].t1 > sp[0].t0;
+            const int r = blk * kBlock + my_row;
+            stat[r] = make_float2(m, failed ? NAN : l);
+            if (have && at_row - lane < rows) {
+#pragma unroll MOD == 0 ? D / 32 : 1
+                for (int i = 0; i < D; i += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(to + i, o);
+                    wait_ld();
+                    keep32(o);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const int c = (i + e) / 4;
+                        *reinterpret_cast<uint4*>(smem + L::kRing + r * (D * 4) +
+                                                  ((c ^ r) & (D / 4 - 1)) * 16) =
+                            make_uint4(__float_as_uint(__uint_as_float(o[e]) * by),
+                                       __float_as_uint(__uint_as_float(o[e + 1]) * by),
+                                       __float_as_uint(__uint_as_float(o[e + 2]) * by),
+                                       __float_as_uint(__uint_as_float(o[e + 3]) * by));
+                    }
+                }
+            }
+        }
+        cluster_sync();
+        if (warp < 8) {
+            // part k of a row: CTA k of the cluster, or with paired blocks block k % 2 of CTA k / 2
+            const int parts = paired ? 2 * a.cluster : a.cluster;
+            auto cta_of = [&](int k) { return paired ? k / 2 : k; };
+            auto row_of = [&](int r, int k) { return paired ? r + k % 2 * kBlock : r; };
+            // four columns a thread, kLines rows of a warp at once
+            constexpr int kQuads = D / 4, kLines = 32 / kQuads;
+            const int step = a.cluster * 8 * kLines;
+            const int c = lane % kQuads, line = lane / kQuads;
+            const int from = ((prefix ? 0 : share) * 8 + warp) * kLines;
+            auto start = [&]() {
+                if constexpr (MOD != 0)
+                    return Walk(a, f, from + line, a.join_step, 1, a.hq);
+                else
+                    return Rows(row0 + from + line, group, step);
+            };
+            auto at = start();
+            auto vector = [&]() {  // of out, from the piece's head on
+                if constexpr (MOD != 0)
+                    return out_at + at.at;
+                else
+                    return out_at + at.token * a.hq + at.head;
+            };
+            // kR rows with kP parts each are on their way together: four loads, and none for a
+            // part that is not there (two parts loaded as four: 481 against 462 us for two
+            // chunks of 1400 tokens, 10k cached each; four rows of two spill, 513)
+            auto join = [&](auto some_rows, auto some_parts) {
+                constexpr int kR = decltype(some_rows)::value, kP = decltype(some_parts)::value;
+                for (int r0 = from; r0 < rows; r0 += kR * step) {
+                    float o[kR][4], sum[kR], top[kR];
+#pragma unroll
+                    for (int u = 0; u < kR; ++u) {
+                        o[u][0] = o[u][1] = o[u][2] = o[u][3] = sum[u] = 0.f;
+                        top[u] = -INFINITY;
+                    }
+                    for (int k0 = 0; k0 < parts; k0 += kP) {
+                        float2 st[kR][kP];
+                        float4 v[kR][kP];
+#pragma unroll
+                        for (int u = 0; u < kR; ++u)
+#pragma unroll
+                            for (int k = 0; k < kP; ++k) {
+                                const int part = min(k0 + k, parts - 1);
+                                const int r = row_of(min(r0 + u * step + line, rows - 1), part);
+                                st[u][k] = peer_ld2(peer_addr(base + r * 8, cta_of(part)));
+                                v[u][k] = peer_ld4(peer_addr(
+                                    base + L::kRing + r * (D * 4) + ((c ^ r) & (kQuads - 1)) * 16,
+                                    cta_of(part)));
+                            }
+#pragma unroll
+                        for (int u = 0; u < kR; ++u)
+#pragma unroll
+                            for (int k = 0; k < kP; ++k) {
+                                // a part without a tile of the row left nothing there
+                                const float2 x = st[u][k];
+                                if (k0 + k >= parts || x.y == 0.f) continue;
+                                const float now = fmaxf(top[u], x.x);
+                                const float keep = ex2(top[u] - now), w = ex2(x.x - now);
+                                top[u] = now;
+                                sum[u] = fmaf(w, x.y, sum[u] * keep);
+                                o[u][0] = fmaf(w, v[u][k].x, o[u][0] * keep);
+                                o[u][1] = fmaf(w, v[u][k].y, o[u][1] * keep);
+                                o[u][2] = fmaf(w, v[u][k].z, o[u][2] * keep);
+                                o[u][3] = fmaf(w, v[u][k].w, o[u][3] * keep);
+                            }
+                    }
+#pragma unroll
+                    for (int u = 0; u < kR; ++u, at.next()) {
+                        if (r0 + u * step + line >= rows) continue;
+                        // a row that sees a token has a sum of 1 or more; NaN where a part failed
+                        const float inv = sum[u] == 0.f ? 0.f : __fdividef(1.f, sum[u]);
+                        if (prefix) {  // this CTA's part of the row
+                            const int64_t r = (int64_t)share * a.r.total * a.hq + vector();
+                            *reinterpret_cast<float4*>(a.part_o + r * D + c * 4) =
+                                make_float4(o[u][0] * inv, o[u][1] * inv, o[u][2] * inv,
+                                            o[u][3] * inv);
+                            if (c == 0)
+                                a.part_lse[r] = sum[u] == 0.f ? -INFINITY
+                                                : sum[u] != sum[u]
+                                                    ? 0.f
+                                                    : top[u] + __log2f(sum[u]) -
+                                                          (kQ8 && !PB ? kLift : 0.f);
+                            continue;
+                        }
+                        *reinterpret_cast<uint2*>(
+                            a.out + vector() * D + c * 4) =
+                            make_uint2(bf16x2(o[u][0] * inv, o[u][1] * inv),
+                                       bf16x2(o[u][2] * inv, o[u][3] * inv));
+                    }
+                }
+            };
+            using std::integral_constant;
+            if (parts > 2)
+                join(integral_constant<int, 1>(), integral_constant<int, 4>());
+            else
+                join(integral_constant<int, 2>(), integral_constant<int, 2>());
+        }
+        cluster_sync();  // shared memory stays until every CTA has read it
+    }
+    };
+
     if (warp < 8) {
         // ---------------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -567,14 +839,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const __nv_bfloat16* q =
                 a.q + (int64_t)s.row0 * a.q_stride + (int64_t)head * a.group * D + c * 8;
             const int first_row = at_row - my_row + my_row / kVecs;
-            Rows at(row0 + first_row, group, kStep);
             uint4 x[kVecs];
+            if constexpr (MOD != 0) {
+                Walk at(a, f, first_row, a.q_step, D, a.q_stride);
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i, at.next()) {  // all loads, then all stores
-                x[i] = make_uint4(0, 0, 0, 0);
-                if (first_row + i * kStep < rows)
-                    x[i] = __ldg(reinterpret_cast<const uint4*>(q + at.token * a.q_stride +
-                                                                at.head * D));
+                for (int i = 0; i < kVecs; ++i, at.next()) {  // all loads, then all stores
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    if (first_row + i * kStep < rows)
+                        x[i] = __ldg(reinterpret_cast<const uint4*>(q + at.at));
+                }
+            } else {
+                Rows at(row0 + first_row, group, kStep);
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i, at.next()) {
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    if (first_row + i * kStep < rows)
+                        x[i] = __ldg(reinterpret_cast<const uint4*>(q + at.token * a.q_stride +
+                                                                    at.head * D));
+                }
             }
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
@@ -593,12 +875,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_smem_async();
             warp_arrive(bar_q + 8 * blk);
 
-            const uint32_t R = row0 + at_row;
             int my_lo = 0, my_hi = 0;
+            const First mine = MOD != 0 ? row_at(a, f, at_row) : First{0, 0};
             if (MOD != 0 && at_row < rows) {
-                const int2 v = row_range(a, s, R);
+                const int2 v = row_range(a, s, mine.token);
                 my_lo = v.x, my_hi = v.y;
             } else if (at_row < rows) {
+                const uint32_t R = row0 + at_row;
                 const int pos = s.len - s.n + int(R / group);
                 my_hi = a.causal ? pos + 1 : s.len;
                 if (a.window > 0) my_lo = max(0, pos - a.window + 1);
@@ -606,8 +889,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float slope = 0.f;  // in base-2 units
             int pos = 0;        // of the row's token
             if ((MOD & kBias) && at_row < rows) {
-                const int i = int(R / group);
-                slope = __ldg(a.slopes + head * a.group + R % group) * 1.4426950408889634f;
+                const int i = mine.token;
+                slope = __ldg(a.slopes + head * a.group + mine.rem) * 1.4426950408889634f;
                 pos = s.len - s.n + i;
                 if (prefix)
                     pos = __ldg(a.r.lens + (s.row0 + i) / a.q_len) - a.q_len + i % a.q_len;
@@ -619,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float scale =
                 kQ8 && !PB ? fmaxf(a.scale_log2 * __ldg(a.k_scale + head), 1e-30f) : a.scale_log2;
             auto rescale = [&](float keep) {  // the block's accumulator
-#pragma unroll
+#pragma unroll MOD == 0 ? D / 32 : 1
                 for (int i = 0; i < D; i += 32) {
                     uint32_t o[32];
                     tmem_ld32(to + i, o);
@@ -633,280 +916,235 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (PB) wait_st();  // a tile may rescale twice, for the gain and for the maximum
             };
             const int first = p.t0 + (paired ? blk : 0), by = paired ? 2 : 1;  // its tiles
-            // weights of half h of a tile, over the scores that they came from
-            auto hand_over = [&](int h, const uint32_t (&w)[kTile / 4]) {
-                tmem_st32(ts + h * (kTile / 4), w);
-                wait_st();
-                fence_before();
-                warp_arrive(bar_p + 16 * blk + 8 * h);
-            };
-            constexpr bool kShape = (MOD & (kCap | kBias)) != 0;
-            // cap tanh(x) + add for a pair, |x| < 1
-            auto capped2 = [&](uint64_t x, uint64_t add) {
-                const uint64_t z = mul2(x, x);
-                uint64_t p = pair(a.cap_poly[kTerms - 1].x, a.cap_poly[kTerms - 1].y);
+            // One tile of scores in the kernels with kShaped, half by half and with loops that are
+            // not unrolled: what such a kernel does beside the products is long enough for its
+            // instructions to be fetched again and again.  The largest score is found before any
+            // weight is computed (the cap keeps the scores' order), so that nothing is done
+            // twice; relative to a fixed reference that falls away.
+            //   cap   below it tanh is a polynomial: two multiplications and six multiply-adds a
+            //         pair of elements, 2 to 3 cycles each, where the products leave each of a
+            //         quarter's two warps 1024 cycles a tile.  Where some score of the warp is
+            //         beyond the cap the tile's scores are capped in place before, and the
+            //         polynomial is that of a straight line;
+            //   bias  for tokens before the row's own a straight line too, slope * i + c.
+            // (`straight`: whether all are; decided tile by tile for the bias alone.)
+            uint64_t steps[4];  // slope times 0 .. 7
+            if (MOD & kBias) {
 #pragma unroll
-                for (int i = kTerms - 2; i >= 0; --i)
-                    p = fma2(p, z, pair(a.cap_poly[i].x, a.cap_poly[i].y));
-                return fma2(x, p, add);
-            };
-            // the whole tile in place, for scores beyond the cap
-            auto cap_in_place = [&](uint32_t (&x)[kTile], const float4* sc) {
-#pragma unroll
-                for (int i = 0; i < kTile; ++i)
-                    x[i] = __float_as_uint(capped(
-                        __uint_as_float(x[i]) * (PB ? sc[i / 8].x : scale), a.cap, a.cap_inv));
-            };
-            // all of the warp's scores are below the cap (NaN counts as beyond)
-            auto reaches = [&](float big) { return __all_sync(0xffffffffu, big < 1.f); };
-            // the row's maximum has grown too far in some row: the reference moves
-            auto move_reference = [&](float now, bool any) {
-                const bool over = now > m + kGrow;
-                const bool grown = __any_sync(0xffffffffu, over);
-                if (grown) {
-                    float keep = 1.f;
-                    if (over) {
-                        keep = m == -INFINITY ? 0.f : ex2(m - now);
-                        l *= keep;
-                        m = now;
-                    }
-                    if (any) rescale(keep);
-                }
-                return grown;
-            };
-            // sums and 16 bits of 8 weights
-            auto take = [&](int h, int g, const uint32_t* x, uint32_t* w, uint64_t* sum,
-                            const float4* sc) {
-                uint64_t part = 0;
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const float e0 = __uint_as_float(x[i]), e1 = __uint_as_float(x[i + 1]);
-                    if (PB)
-                        part = i == 0 ? pair(e0, e1) : add2(part, pair(e0, e1));
-                    else
-                        sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(e0, e1));
-                    w[g * 4 + i / 2] = operand2<PAGE>(e0, e1);
-                }
-                if (PB) {
-                    const float over = sc[h * 8 + g].z;
-                    sum[g & 1] = fma2(part, pair(over, over), sum[g & 1]);
-                }
-            };
-            auto scores_of = [&](uint32_t (&x)[kTile]) {
-#pragma unroll
-                for (int i = 0; i < kTile; i += 32) tmem_ld32(ts + i, x + i);
-                wait_ld();
-#pragma unroll
-                for (int i = 0; i < kTile; i += 32) keep32(x + i);
-            };
-            // A tile of capped scores.  Relative to the row's maximum (the cap keeps the scores'
-            // order), that and the largest magnitude are found first, so that nothing is done
-            // twice; relative to a fixed reference the magnitude along with the first half, which
-            // is done again where a score is beyond the cap.
-            // Limit: of the 1024 cycles that the products leave each of a quarter's two warps a
-            // tile, the polynomial takes 2 multiplications and 6 multiply-adds of 2 to 3 cycles
-            // each for a pair of elements, the reference being the last one's addend.
-            auto capped_tile = [&](int j, auto edge, uint32_t (&x)[kTile],
-                                   uint32_t (&w)[kTile / 4], uint64_t (&sum)[2],
-                                   const float4* sc) {
+                for (int i = 0; i < 4; ++i)
+                    steps[i] = pair(slope * float(2 * i), slope * float(2 * i + 1));
+            }
+            auto shaped_tile = [&](int j, auto edge, auto straight) {
                 constexpr bool kEdge = decltype(edge)::value;
+                constexpr bool kLine = decltype(straight)::value;
+                constexpr bool kCapped = (MOD & kCap) != 0, kBiased = (MOD & kBias) != 0;
                 constexpr bool kFix = (MOD & kFixed) != 0;
-                const int t0 = tile_at(j) * kTile, from = my_lo - t0, until = my_hi - t0;
-                auto hidden = [&](int i) { return kEdge && (i < from || i >= until); };
-                auto seen = [&](int i, float none) {
-                    return hidden(i) ? none : __uint_as_float(x[i]);
-                };
-                scores_of(x);
-                bool below = true;
-                if constexpr (!kFix) {
-                    float tops[4], bigs[4];
-#pragma unroll
-                    for (int g = 0; g < kTile / 8; ++g) {
-                        const float mul = PB ? sc[g].x : 1.f;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int k = g * 8 + i;
-                            tops[i] = max3(g == 0 ? -INFINITY : tops[i],
-                                           seen(k, -INFINITY) * mul, seen(k + 4, -INFINITY) * mul);
-                            bigs[i] = max3_abs(g == 0 ? 0.f : bigs[i], seen(k, 0.f) * mul,
-                                               seen(k + 4, 0.f) * mul);
-                        }
-                    }
-                    const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
-                    const float by = PB ? 1.f : scale;
-                    below = reaches(max3(fmaxf(bigs[0], bigs[1]), bigs[2], bigs[3]) *
-                                    (by * a.cap_inv));
-                    move_reference(top == -INFINITY ? top : capped(top * by, a.cap, a.cap_inv),
-                                   j > first);
-                }
-                float off = kFix ? -0.25f * a.cap : m == -INFINITY ? 0.f : -m;
-                if (kQ8 && !PB) off += kLift;
-                float big = 0.f;
-                // the weights of half h
-                auto weigh = [&](int h, auto exponents) {
-                    float bigs[4];
-#pragma unroll
-                    for (int g = 0; g <= 8; ++g) {
-                        const int at = h * (kTile / 2) + g * 8;
-                        if (g < 8) {
-                            if (kFix && h == 0) {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    bigs[i % 4] =
-                                        max3_abs(g == 0 && i < 4 ? 0.f : bigs[i % 4],
-                                                 seen(at + i, 0.f), seen(kTile / 2 + at + i, 0.f));
-                            }
-                            const float mul = PB ? sc[at / 8].x : scale;
-                            const float add = PB ? off + sc[at / 8].y : off;
-#pragma unroll
-                            for (int i = at; i < at + 8; i += 2) {
-                                float e0, e1;
-                                unpair(exponents(pair(__uint_as_float(x[i]),
-                                                      __uint_as_float(x[i + 1])),
-                                                 mul * a.cap_inv, pair(add, add)),
-                                       e0, e1);
-                                x[i] = hidden(i) ? 0 : __float_as_uint(ex2(e0));
-                                x[i + 1] = hidden(i + 1) ? 0 : __float_as_uint(ex2(e1));
-                            }
-                        }
-                        if (g > 0) take(h, g - 1, x + at - 8, w, sum, sc);
-                    }
-                    if (kFix && h == 0)
-                        big = max3(fmaxf(bigs[0], bigs[1]), bigs[2], bigs[3]) *
-                              (scale * a.cap_inv);
-                };
-                auto by_polynomial = [&](uint64_t y, float k, uint64_t add) {
-                    return capped2(mul2(y, pair(k, k)), add);
-                };
-                auto as_they_are = [&](uint64_t y, float, uint64_t add) { return add2(y, add); };
-                sum[0] = sum[1] = 0;
-                if (below) {
-                    weigh(0, by_polynomial);
-                    below = !kFix || reaches(big);
-                    if (below) {
-                        hand_over(0, w);
-                        weigh(1, by_polynomial);
-                        hand_over(1, w);
-                    } else {
-                        scores_of(x);
+                constexpr int kHalf = kTile / 2;
+                const float4* const sc = reinterpret_cast<const float4*>(
+                    smem + L::kScales + (PB ? (j - T0) % L::kScaleTiles * L::kScaleBytes : 0));
+                if (PB) {
+                    const float gain = sc[kTile / 8].x;
+                    if (gain != vgain) {
+                        if (j > first) rescale(gain / vgain);
+                        vgain = gain;
                     }
                 }
-                if (!below) {
-                    cap_in_place(x, sc);
-                    sum[0] = sum[1] = 0;
-                    weigh(0, as_they_are);
-                    hand_over(0, w);
-                    weigh(1, as_they_are);
-                    hand_over(1, w);
-                }
-                if (kFix) m = 0.25f * a.cap;
-            };
-            // A tile of scores with a bias: the second half's exponents are formed along with the
-            // first half's weights, so that the largest of all is known before any weight is
-            // handed over.  For tokens before the row's own the bias is a straight line,
-            // slope * i + c, with the reference in c.
-            auto biased_tile = [&](int j, auto edge, uint32_t (&x)[kTile],
-                                   uint32_t (&w)[kTile / 4], uint64_t (&sum)[2],
-                                   const float4* sc) {
-                constexpr bool kEdge = decltype(edge)::value;
-                const int t0 = tile_at(j) * kTile, from = my_lo - t0, until = my_hi - t0;
+                const int t0 = tile_at(j) * kTile;
                 const float far = float(t0 - pos);
-                float top, big;
-                auto turn_to_weights = [&](int at) {
-#pragma unroll
-                    for (int i = at; i < at + 8; ++i)
-                        x[i] = __float_as_uint(ex2(__uint_as_float(x[i])));
+                uint32_t x[kHalf];
+                auto load = [&](int h) {
+                    tmem_ld32(ts + h * kHalf, x);
+                    tmem_ld32(ts + h * kHalf + 32, x + 32);
+                    wait_ld();
+                    keep32(x);
+                    keep32(x + 32);
                 };
-                auto first_half = [&](auto polynomial, auto straight) {
-                    constexpr bool kPoly = decltype(polynomial)::value;
-                    float off = m == -INFINITY ? 0.f : -m;
-                    if (kQ8 && !PB) off += kLift;
-                    const float c = fmaf(slope, far, off);
-                    top = -INFINITY;
-                    if (kPoly) big = 0.f;
-                    uint64_t line[4];  // slope times 0 .. 7
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        line[i] = pair(slope * float(2 * i), slope * float(2 * i + 1));
-                    auto exponents_of = [&](int at) {  // of the 8 scores from `at` on
-                        const float mul = PB ? sc[at / 8].x : scale;
-                        const float k = kPoly ? mul * a.cap_inv : mul;
-                        const float lift = PB ? sc[at / 8].y : 0.f;
-                        if (kPoly) {
-                            const float u = max8_abs(x + at);
-                            big = fmaxf(big, PB ? u * mul : u);
-                        }
-                        const float cl = fmaf(slope, float(at), c) + lift, ol = off + lift;
-                        const uint64_t kk = pair(k, k), cc = pair(cl, cl);
-#pragma unroll
-                        for (int i = at; i < at + 8; i += 2) {
-                            const uint64_t r = pair(__uint_as_float(x[i]),
-                                                    __uint_as_float(x[i + 1]));
-                            const uint64_t b =
-                                decltype(straight)::value
-                                    ? add2(line[(i - at) / 2], cc)
-                                    : pair(fmaf(-slope, fabsf(far + float(i)), ol),
-                                           fmaf(-slope, fabsf(far + float(i + 1)), ol));
-                            float y0, y1;
-                            if constexpr (kPoly)
-                                unpair(capped2(mul2(r, kk), b), y0, y1);
-                            else if constexpr ((MOD & kCap) != 0)  // capped before
-                                unpair(add2(r, b), y0, y1);
-                            else
-                                unpair(fma2(r, kk, b), y0, y1);
-                            if (kEdge && (i < from || i >= until)) y0 = -INFINITY;
-                            if (kEdge && (i + 1 < from || i + 1 >= until)) y1 = -INFINITY;
-                            x[i] = __float_as_uint(y0);
-                            x[i + 1] = __float_as_uint(y1);
-                        }
-                        const float u = max8(x + at);
-                        top = fmaxf(top, PB ? u - lift : u);
-                    };
-#pragma unroll
-                    for (int g = 0; g <= 8; ++g) {
-                        if (g < 8) {
-                            exponents_of(g * 8);
-                            exponents_of(kTile / 2 + g * 8);
-                            turn_to_weights(g * 8);
-                        }
-                        if (g > 0) take(0, g - 1, x + g * 8 - 8, w, sum, sc);
-                    }
-                    if (kPoly) big *= PB ? a.cap_inv : scale * a.cap_inv;
-                    top -= off;
+                auto hidden = [&](int h, int i) {  // element i of half h
+                    const int t = t0 + h * kHalf;
+                    return kEdge && (i < my_lo - t || i >= my_hi - t);
                 };
-                [[maybe_unused]] bool below = true;
-                for (;;) {
-                    scores_of(x);
-                    if (kEdge && (MOD & kCap)) {  // what a row does not see need not be below
+                // largest magnitude of a half before the cap: where all are below, x P(x^2) is
+                // tanh(x); else the scores are replaced by tanh(x), and P is 1
+                uint64_t poly[kTerms];
+                bool below = true;
+                auto choose = [&]() {
 #pragma unroll
-                        for (int i = 0; i < kTile; ++i)
-                            if (i < from || i >= until) x[i] = 0;
+                    for (int i = 0; i < kTerms; ++i) {
+                        const float c = below || i == 0 ? a.cap_poly[i].x : 0.f;
+                        poly[i] = pair(c, c);
                     }
-                    sum[0] = sum[1] = 0;
-                    if constexpr ((MOD & kCap) != 0) {
-                        if (below) {
-                            first_half(std::true_type(), std::false_type());
-                            below = reaches(big);
-                            if (!below) continue;
+                };
+                auto magnitude = [&](int h) {
+                    float big = 0.f;
+#pragma unroll
+                    for (int g = 0; g < kHalf / 8; ++g) {
+                        float y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            y[i] = hidden(h, g * 8 + i) ? 0.f : __uint_as_float(x[g * 8 + i]);
+                        const float u = max3_abs(max3_abs(y[0], y[1], y[2]),
+                                                 max3_abs(y[3], y[4], y[5]), max3_abs(y[6], y[7], 0.f));
+                        big = fmaxf(big, PB ? u * sc[h * 8 + g].x : u);
+                    }
+                    return big * (PB ? a.cap_inv : scale * a.cap_inv);
+                };
+                auto cap_in_place = [&](int h0, int h1) {
+#pragma unroll 1
+                    for (int q = h0 * 2; q < h1 * 2; ++q) {
+                        uint32_t y[32];
+                        tmem_ld32(ts + q * 32, y);
+                        wait_ld();
+                        keep32(y);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float mul = PB ? sc[q * 4 + i / 8].x : scale;
+                            y[i] = __float_as_uint(
+                                capped(__uint_as_float(y[i]) * mul * a.cap_inv, 1.f, 1.f));
+                        }
+                        tmem_st32(ts + q * 32, y);
+                        wait_st();
+                    }
+                };
+                // base-2 exponents of 8 elements: the shaped scores plus `add`
+                auto exponents = [&](int h, int g, float add, uint64_t (&e)[4]) {
+                    const float mul = PB ? sc[h * 8 + g].x : scale;
+                    const float k = !kCapped ? mul : below ? mul * a.cap_inv : 1.f;
+                    const float at = far + float(h * kHalf + g * 8);
+                    const uint64_t kk = pair(k, k);
+                    const float c = kBiased ? fmaf(slope, at, add) : add;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint64_t r = pair(__uint_as_float(x[g * 8 + 2 * i]),
+                                                __uint_as_float(x[g * 8 + 2 * i + 1]));
+                        uint64_t b = pair(c, c);
+                        if (kBiased && kLine)
+                            b = add2(steps[i], b);
+                        else if (kBiased)
+                            b = pair(fmaf(-slope, fabsf(at + float(2 * i)), add),
+                                     fmaf(-slope, fabsf(at + float(2 * i + 1)), add));
+                        if constexpr (kCapped) {
+                            const uint64_t y = mul2(r, kk), z = mul2(y, y);
+                            uint64_t p = poly[kTerms - 1];
+#pragma unroll
+                            for (int q = kTerms - 2; q >= 0; --q) p = fma2(p, z, poly[q]);
+                            e[i] = fma2(y, p, b);
                         } else {
-                            cap_in_place(x, sc);
-                            first_half(std::false_type(), std::false_type());
+                            e[i] = fma2(r, kk, b);
                         }
-                    } else if (__all_sync(0xffffffffu, a.causal || t0 + kTile - 1 <= pos)) {
-                        first_half(std::false_type(), std::true_type());
-                    } else {
-                        first_half(std::false_type(), std::false_type());
                     }
-                    if (!move_reference(top, j > first)) break;
+                };
+                if (kCapped && !kFix) {
+                    float big = 0.f;
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        load(h);
+                        big = fmaxf(big, magnitude(h));
+                    }
+                    below = __all_sync(0xffffffffu, big < 1.f);  // (NaN counts as beyond)
+                    if (!below) cap_in_place(0, 2);
+                    choose();
                 }
-                hand_over(0, w);
+                if (!kFix) {
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        load(h);
 #pragma unroll
-                for (int g = 0; g <= 8; ++g) {
-                    const int at = kTile / 2 + g * 8;
-                    if (g < 8) turn_to_weights(at);
-                    if (g > 0) take(1, g - 1, x + at - 8, w, sum, sc);
+                        for (int g = 0; g < kHalf / 8; ++g) {
+                            float y[8];
+                            if constexpr (kBiased) {
+                                uint64_t e[4];
+                                exponents(h, g, 0.f, e);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) unpair(e[i], y[2 * i], y[2 * i + 1]);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(x[g * 8 + i]);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (hidden(h, g * 8 + i)) y[i] = -INFINITY;
+                            const float u = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[5]),
+                                                 fmaxf(y[6], y[7]));
+                            top = fmaxf(top, kBiased || !PB || !below ? u : u * sc[h * 8 + g].x);
+                        }
+                    }
+                    if (!kBiased && top != -INFINITY) {
+                        if (kCapped)
+                            top = below ? capped(PB ? top : top * scale, a.cap, a.cap_inv)
+                                        : top * a.cap;
+                        else if (!PB)
+                            top *= scale;
+                    }
+                    const bool over = top > m + kGrow;
+                    if (__any_sync(0xffffffffu, over)) {
+                        float keep = 1.f;
+                        if (over) {
+                            keep = m == -INFINITY ? 0.f : ex2(m - top);
+                            l *= keep;
+                            m = top;
+                        }
+                        if (j > first) rescale(keep);
+                    }
+                } else {
+                    m = 0.25f * a.cap;
                 }
-                hand_over(1, w);
+                float off = m == -INFINITY ? 0.f : -m;
+                if (kQ8 && !PB) off += kLift;
+                uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    load(h);
+                    if (kFix) {
+                        below = __all_sync(0xffffffffu, magnitude(h) < 1.f);
+                        if (!below) {
+                            cap_in_place(h, h + 1);
+                            load(h);
+                        }
+                        choose();
+                    }
+                    uint32_t w[kHalf / 2];
+#pragma unroll
+                    for (int g = 0; g <= kHalf / 8; ++g) {
+                        if (g < kHalf / 8) {
+                            uint64_t e[4];
+                            exponents(h, g, PB ? off + sc[h * 8 + g].y : off, e);
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) {
+                                float y0, y1;
+                                unpair(e[i / 2], y0, y1);
+                                x[g * 8 + i] = hidden(h, g * 8 + i) ? 0 : __float_as_uint(ex2(y0));
+                                x[g * 8 + i + 1] =
+                                    hidden(h, g * 8 + i + 1) ? 0 : __float_as_uint(ex2(y1));
+                            }
+                        }
+                        if (g > 0) {  // sums and 16 bits of the group before
+                            uint64_t part = 0;
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) {
+                                const float e0 = __uint_as_float(x[g * 8 - 8 + i]);
+                                const float e1 = __uint_as_float(x[g * 8 - 8 + i + 1]);
+                                if (PB)
+                                    part = i == 0 ? pair(e0, e1) : add2(part, pair(e0, e1));
+                                else
+                                    sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(e0, e1));
+                                w[g * 4 - 4 + i / 2] = operand2<PAGE>(e0, e1);
+                            }
+                            if (PB) {
+                                const float over = sc[h * 8 + g - 1].z;
+                                sum[g & 1] = fma2(part, pair(over, over), sum[g & 1]);
+                            }
+                        }
+                    }
+                    // the first half's product runs while the second half is computed
+                    tmem_st32(ts + h * (kTile / 4), w);
+                    wait_st();
+                    fence_before();
+                    warp_arrive(bar_p + 16 * blk + 8 * h);
+                }
+                float s0, s1;
+                unpair(add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
             };
             // One tile of scores; `edge`: some row does not see all of it.
             auto tile = [&](int j, auto edge) {
@@ -983,20 +1221,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The first half's weights are relative to the old maximum while the new one is
                 // found; the tile is read again where that has grown too far.
                 bool grown;
-                if constexpr (kShape) {
-                    if constexpr ((MOD & kBias) != 0)
-                        biased_tile(j, edge, x, w, sum, sc);
-                    else
-                        capped_tile(j, edge, x, w, sum, sc);
-                    grown = false;
-                } else do {
+                do {
 #pragma unroll
                     for (int i = 0; i < kTile; i += 32) tmem_ld32(ts + i, x + i);
                     wait_ld();
 #pragma unroll
                     for (int i = 0; i < kTile; i += 32) keep32(x + i);
                     if (decltype(edge)::value) {
-                        const int t0 = tile_at(j) * kTile, from = my_lo - t0, until = my_hi - t0;
+                        const int from = my_lo - j * kTile, until = my_hi - j * kTile;
 #pragma unroll
                         for (int i = 0; i < kTile; ++i)
                             if (i < from || i >= until) x[i] = 0xff800000u;  // -infinity
@@ -1020,12 +1252,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (j > first) rescale(keep);
                     }
                 } while (grown);
-                if constexpr (!kShape) {
-                    // the first half's product runs while the second half is computed
-                    hand_over(0, w);
-                    weigh(1);
-                    hand_over(1, w);
-                }
+                // the first half's product runs while the second half is computed
+                tmem_st32(ts, w);
+                wait_st();
+                fence_before();
+                warp_arrive(bar_p + 16 * blk);
+                weigh(1);
+                tmem_st32(ts + kTile / 4, w);
+                wait_st();
+                fence_before();
+                warp_arrive(bar_p + 16 * blk + 8);
                 float s0, s1;
                 unpair(add2(sum[0], sum[1]), s0, s1);
                 l += s0 + s1;
@@ -1034,16 +1270,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = first; j < p.t1; j += by, phase ^= 1) {
                 if (!warp_wait(bar_s + 8 * blk, phase, gave_up)) break;
                 fence_after();
+                auto one = [&](auto edge) {
+                    if constexpr (MOD == 0) {
+                        tile(j, edge);
+                    } else if constexpr ((MOD & kBias) != 0 && (MOD & kCap) == 0) {
+                        if (__all_sync(0xffffffffu,
+                                       a.causal || tile_at(j) * kTile + kTile - 1 <= pos))
+                            shaped_tile(j, edge, std::true_type());
+                        else
+                            shaped_tile(j, edge, std::false_type());
+                    } else {
+                        shaped_tile(j, edge, std::false_type());
+                    }
+                };
                 if (tile_at(j) * kTile < p.lo_all || p.hi_all - tile_at(j) * kTile < kTile)
-                    tile(j, std::true_type());
+                    one(std::true_type());
                 else
-                    tile(j, std::false_type());
+                    one(std::false_type());
             }
             warp_wait(bar_o + 8 * blk, 0, gave_up);
             if (MOD != 0 && my_hi <= my_lo) {  // a row that sees nothing
                 m = -INFINITY;
                 l = 0.f;
             }
+        }
+        if constexpr (MOD != 0) {
+            fence_after();
+            if (joins) asm volatile("bar.sync 1, 320;" ::: "memory");
+            results();
         }
     } else if (kQ8 && warp < 12) {
         // ---------------------------------------------------------- widening (8-bit pages)
@@ -1381,178 +1635,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         volatile int never = 0;
         bar_wait(bar_o + 8 * i, 0, &never);
     }
+    if constexpr (MOD == 0) {
+        __syncwarp();
+        fence_before();
+        __syncthreads();
+        fence_after();
+        results();
+    } else if (warp >= 8) {
+        // the join's shared memory is free once both blocks' products are over, and every
+        // thread of a cluster takes part in its barriers
+        if (warp == 12 || warp == 13) asm volatile("bar.arrive 1, 320;" ::: "memory");
+        if (joins) {
+            cluster_sync();
+            cluster_sync();
+        }
+    }
     __syncwarp();
     fence_before();
     __syncthreads();
-    fence_after();
-    const bool failed = *gave_up || !s.ok || (warp < 8 && lost[at_row / 32] >> lane & 1);
-    if (*gave_up && threadIdx.x == 0) latch(a.r.err, PGD_ERR_TIMEOUT);
-
-    // -------------------------------------------------------------------- results
-    const int64_t out_at = (int64_t)s.row0 * a.hq + (int64_t)head * a.group;  // head vectors
-    // what the accumulator is to be multiplied with beside 1 / l
-    const float by = !kQ8 ? 1.f : PB ? 1.f / vgain : __ldg(a.v_scale + head);
-    if (a.cluster == 1 && !paired && !prefix) {
-        if (warp < 8) {
-            const uint32_t to = tmem + (uint32_t(warp % 4 * 32) << 16) + 2 * kTile + blk * D;
-            const float inv = failed ? NAN : l > 0.f ? by / l : l == 0.f ? 0.f : NAN;
-            const bool have = blk ? sp[1].t1 > sp[1].t0 : sp[0].t1 > sp[0].t0;
-            uint8_t* const rowp = smem + (blk * kBlock + my_row) * (D * 2);
-#pragma unroll
-            for (int i = 0; i < D; i += 32) {
-                uint32_t o[32];
-                if (have) {
-                    tmem_ld32(to + i, o);
-                    wait_ld();
-                    keep32(o);
-                }
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float y0 = __uint_as_float(o[e + 2 * k]) * inv;
-                        const float y1 = __uint_as_float(o[e + 2 * k + 1]) * inv;
-                        w[k] = l == 0.f && !failed ? 0u : inv != inv ? 0x7fc07fc0u : bf16x2(y0, y1);
-                    }
-                    const int c = (i + e) / 8;
-                    *reinterpret_cast<uint4*>(rowp + ((c ^ my_row) & (D / 8 - 1)) * 16) =
-                        make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
-            __syncwarp();
-            constexpr int kVecs = D / 8, kStep = 32 / kVecs;
-            const int c = lane % kVecs;
-            Rows at(row0 + warp * 32 + lane / kVecs, group, kStep);
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i, at.next()) {
-                const int r = warp * 32 + lane / kVecs + i * kStep;
-                if (r < rows)
-                    *reinterpret_cast<uint4*>(
-                        a.out + (out_at + at.token * a.hq + at.head) * D + c * 8) =
-                        *reinterpret_cast<const uint4*>(smem + r * (D * 2) +
-                                                        ((c ^ r) & (kVecs - 1)) * 16);
-            }
-        }
-    } else {
-        // unnormalised rows, maxima and sums to shared memory, then every CTA of the
-        // cluster joins a share of the rows
-        float2* const stat = reinterpret_cast<float2*>(smem);  // of the 256 rows
-        if (warp < 8) {
-            const uint32_t to = tmem + (uint32_t(warp % 4 * 32) << 16) + 2 * kTile + blk * D;
-            const bool have = blk ? sp[1].t1 > sp[1].t0 : sp[0].t1 > sp[0].t0;
-            const int r = blk * kBlock + my_row;
-            stat[r] = make_float2(m, failed ? NAN : l);
-            if (have && at_row - lane < rows) {
-#pragma unroll
-                for (int i = 0; i < D; i += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(to + i, o);
-                    wait_ld();
-                    keep32(o);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const int c = (i + e) / 4;
-                        *reinterpret_cast<uint4*>(smem + L::kRing + r * (D * 4) +
-                                                  ((c ^ r) & (D / 4 - 1)) * 16) =
-                            make_uint4(__float_as_uint(__uint_as_float(o[e]) * by),
-                                       __float_as_uint(__uint_as_float(o[e + 1]) * by),
-                                       __float_as_uint(__uint_as_float(o[e + 2]) * by),
-                                       __float_as_uint(__uint_as_float(o[e + 3]) * by));
-                    }
-                }
-            }
-        }
-        cluster_sync();
-        if (warp < 8) {
-            // part k of a row: CTA k of the cluster, or with paired blocks block k % 2 of CTA k / 2
-            const int parts = paired ? 2 * a.cluster : a.cluster;
-            auto cta_of = [&](int k) { return paired ? k / 2 : k; };
-            auto row_of = [&](int r, int k) { return paired ? r + k % 2 * kBlock : r; };
-            // four columns a thread, kLines rows of a warp at once
-            constexpr int kQuads = D / 4, kLines = 32 / kQuads;
-            const int step = a.cluster * 8 * kLines;
-            const int c = lane % kQuads, line = lane / kQuads;
-            const int from = ((prefix ? 0 : share) * 8 + warp) * kLines;
-            Rows at(row0 + from + line, group, step);
-            // kR rows with kP parts each are on their way together: four loads, and none for a
-            // part that is not there (two parts loaded as four: 481 against 462 us for two
-            // chunks of 1400 tokens, 10k cached each; four rows of two spill, 513)
-            auto join = [&](auto some_rows, auto some_parts) {
-                constexpr int kR = decltype(some_rows)::value, kP = decltype(some_parts)::value;
-                for (int r0 = from; r0 < rows; r0 += kR * step) {
-                    float o[kR][4], sum[kR], top[kR];
-#pragma unroll
-                    for (int u = 0; u < kR; ++u) {
-                        o[u][0] = o[u][1] = o[u][2] = o[u][3] = sum[u] = 0.f;
-                        top[u] = -INFINITY;
-                    }
-                    for (int k0 = 0; k0 < parts; k0 += kP) {
-                        float2 st[kR][kP];
-                        float4 v[kR][kP];
-#pragma unroll
-                        for (int u = 0; u < kR; ++u)
-#pragma unroll
-                            for (int k = 0; k < kP; ++k) {
-                                const int part = min(k0 + k, parts - 1);
-                                const int r = row_of(min(r0 + u * step + line, rows - 1), part);
-                                st[u][k] = peer_ld2(peer_addr(base + r * 8, cta_of(part)));
-                                v[u][k] = peer_ld4(peer_addr(
-                                    base + L::kRing + r * (D * 4) + ((c ^ r) & (kQuads - 1)) * 16,
-                                    cta_of(part)));
-                            }
-#pragma unroll
-                        for (int u = 0; u < kR; ++u)
-#pragma unroll
-                            for (int k = 0; k < kP; ++k) {
-                                // a part without a tile of the row left nothing there
-                                const float2 x = st[u][k];
-                                if (k0 + k >= parts || x.y == 0.f) continue;
-                                const float now = fmaxf(top[u], x.x);
-                                const float keep = ex2(top[u] - now), w = ex2(x.x - now);
-                                top[u] = now;
-                                sum[u] = fmaf(w, x.y, sum[u] * keep);
-                                o[u][0] = fmaf(w, v[u][k].x, o[u][0] * keep);
-                                o[u][1] = fmaf(w, v[u][k].y, o[u][1] * keep);
-                                o[u][2] = fmaf(w, v[u][k].z, o[u][2] * keep);
-                                o[u][3] = fmaf(w, v[u][k].w, o[u][3] * keep);
-                            }
-                    }
-#pragma unroll
-                    for (int u = 0; u < kR; ++u, at.next()) {
-                        if (r0 + u * step + line >= rows) continue;
-                        // a row that sees a token has a sum of 1 or more; NaN where a part failed
-                        const float inv = sum[u] == 0.f ? 0.f : __fdividef(1.f, sum[u]);
-                        if (prefix) {  // this CTA's part of the row
-                            const int64_t r = (int64_t)share * a.r.total * a.hq + out_at +
-                                              at.token * a.hq + at.head;
-                            *reinterpret_cast<float4*>(a.part_o + r * D + c * 4) =
-                                make_float4(o[u][0] * inv, o[u][1] * inv, o[u][2] * inv,
-                                            o[u][3] * inv);
-                            if (c == 0)
-                                a.part_lse[r] = sum[u] == 0.f ? -INFINITY
-                                                : sum[u] != sum[u]
-                                                    ? 0.f
-                                                    : top[u] + __log2f(sum[u]) -
-                                                          (kQ8 && !PB ? kLift : 0.f);
-                            continue;
-                        }
-                        *reinterpret_cast<uint2*>(
-                            a.out + (out_at + at.token * a.hq + at.head) * D + c * 4) =
-                            make_uint2(bf16x2(o[u][0] * inv, o[u][1] * inv),
-                                       bf16x2(o[u][2] * inv, o[u][3] * inv));
-                    }
-                }
-            };
-            using std::integral_constant;
-            if (parts > 2)
-                join(integral_constant<int, 1>(), integral_constant<int, 4>());
-            else
-                join(integral_constant<int, 2>(), integral_constant<int, 2>());
-        }
-        cluster_sync();  // shared memory stays until every CTA has read it
-    }
-    __syncthreads();
+    if (MOD != 0 && *gave_up && threadIdx.x == 0) latch(a.r.err, PGD_ERR_TIMEOUT);
     if (warp == 12) tmem_free(tmem, 512);
 }
 
