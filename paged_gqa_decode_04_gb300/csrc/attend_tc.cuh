@@ -527,9 +527,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         f.token = row0 / a.group;
         f.rem = row0 - f.token * a.group;
     }
+    // Queries of bfloat16 pages go to shared memory by asynchronous copies as soon as their rows
+    // are known, while the rest is found out; 128 rows or fewer are for both blocks.
+    const bool early = MOD != 0 && !kQ8 && a.q_and == 0xffffffffu && a.q_xor == 0;
+    if (early && warp < 8) {
+        constexpr int kVecs = D / 8, kStep = kBlock / kVecs;  // 16-byte pieces; rows at once
+        const int r0 = threadIdx.x % kBlock, c = r0 % kVecs;
+        const int first_row = (rows <= kBlock ? 0 : warp / 4 * kBlock) + r0 / kVecs;
+        const __nv_bfloat16* q =
+            a.q + (int64_t)s.row0 * a.q_stride + (int64_t)head * a.group * D + c * 8;
+        Walk at(a, f, first_row, a.q_step, D, a.q_stride);
+        const uint32_t to = base + warp / 4 * L::kQ + c / 8 * (kBlock * 128);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i, at.next()) {
+            const int r = r0 / kVecs + i * kStep;
+            const bool there = first_row + i * kStep < rows;
+            copy16(to + r * 128 + ((c ^ r) & 7) * 16, there ? q + at.at : a.q, there);
+        }
+    }
     Span sp[2];
     if (MOD != 0 && a.visible) {
-        int4* const of_warp = reinterpret_cast<int4*>(smem);  // before the queries come there
+        // (before the tiles come there)
+        int4* const of_warp = reinterpret_cast<int4*>(smem + L::kRing);
         if (warp < 8) {
             const int4 v = range_of_warp(a, s, f, warp * 32, rows);
             if (lane == 0) of_warp[warp] = v;
@@ -833,44 +852,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const Span p = blk ? sp[1] : sp[0];
         if (p.t1 > p.t0) {
-            // the block's queries into shared memory, swizzled
-            constexpr int kVecs = D / 8, kStep = kBlock / kVecs;  // 16-byte pieces; rows at once
-            const int c = my_row % kVecs;
-            const __nv_bfloat16* q =
-                a.q + (int64_t)s.row0 * a.q_stride + (int64_t)head * a.group * D + c * 8;
-            const int first_row = at_row - my_row + my_row / kVecs;
-            uint4 x[kVecs];
-            if constexpr (MOD != 0) {
-                Walk at(a, f, first_row, a.q_step, D, a.q_stride);
-#pragma unroll
-                for (int i = 0; i < kVecs; ++i, at.next()) {  // all loads, then all stores
-                    x[i] = make_uint4(0, 0, 0, 0);
-                    if (first_row + i * kStep < rows)
-                        x[i] = __ldg(reinterpret_cast<const uint4*>(q + at.at));
-                }
+            if (early) {
+                copies_landed();
             } else {
-                Rows at(row0 + first_row, group, kStep);
-#pragma unroll
-                for (int i = 0; i < kVecs; ++i, at.next()) {
-                    x[i] = make_uint4(0, 0, 0, 0);
-                    if (first_row + i * kStep < rows)
-                        x[i] = __ldg(reinterpret_cast<const uint4*>(q + at.token * a.q_stride +
-                                                                    at.head * D));
+                // the block's queries into shared memory, swizzled
+                constexpr int kVecs = D / 8, kStep = kBlock / kVecs;  // 16-byte pieces; rows at once
+                const int c = my_row % kVecs;
+                const __nv_bfloat16* q =
+                    a.q + (int64_t)s.row0 * a.q_stride + (int64_t)head * a.group * D + c * 8;
+                const int first_row = at_row - my_row + my_row / kVecs;
+                uint4 x[kVecs];
+                if constexpr (MOD != 0) {
+                    Walk at(a, f, first_row, a.q_step, D, a.q_stride);
+    #pragma unroll
+                    for (int i = 0; i < kVecs; ++i, at.next()) {  // all loads, then all stores
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (first_row + i * kStep < rows)
+                            x[i] = __ldg(reinterpret_cast<const uint4*>(q + at.at));
+                    }
+                } else {
+                    Rows at(row0 + first_row, group, kStep);
+    #pragma unroll
+                    for (int i = 0; i < kVecs; ++i, at.next()) {
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (first_row + i * kStep < rows)
+                            x[i] = __ldg(reinterpret_cast<const uint4*>(q + at.token * a.q_stride +
+                                                                        at.head * D));
+                    }
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const int r = my_row / kVecs + i * kStep;
-                auto operand = [&](uint32_t two) {
-                    two = (two & a.q_and) ^ a.q_xor;
-                    return kQ8 ? f16x2(__uint_as_float(two << 16),
-                                       __uint_as_float(two & 0xffff0000u))
-                               : two;
-                };
-                *reinterpret_cast<uint4*>(smem + blk * L::kQ + c / 8 * (kBlock * 128) + r * 128 +
-                                          ((c ^ r) & 7) * 16) =
-                    make_uint4(operand(x[i].x), operand(x[i].y), operand(x[i].z),
-                               operand(x[i].w));
+    #pragma unroll
+                for (int i = 0; i < kVecs; ++i) {
+                    const int r = my_row / kVecs + i * kStep;
+                    auto operand = [&](uint32_t two) {
+                        two = (two & a.q_and) ^ a.q_xor;
+                        return kQ8 ? f16x2(__uint_as_float(two << 16),
+                                           __uint_as_float(two & 0xffff0000u))
+                                   : two;
+                    };
+                    *reinterpret_cast<uint4*>(smem + blk * L::kQ + c / 8 * (kBlock * 128) + r * 128 +
+                                              ((c ^ r) & 7) * 16) =
+                        make_uint4(operand(x[i].x), operand(x[i].y), operand(x[i].z),
+                                   operand(x[i].w));
+                }
             }
             fence_smem_async();
             warp_arrive(bar_q + 8 * blk);

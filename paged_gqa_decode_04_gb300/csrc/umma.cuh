@@ -85,6 +85,15 @@ __device__ __forceinline__ void fence_smem_async() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// 16 bytes from global to shared memory without registers in between, or zeros; and the wait for
+// all such copies of this thread.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                             int x, int y, int z, int w) {
