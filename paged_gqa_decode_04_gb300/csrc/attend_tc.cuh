@@ -1011,6 +1011,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     return big * (PB ? a.cap_inv : scale * a.cap_inv);
                 };
+                // largest score of a half, before the logit multiplier where that is one for all
+                auto largest = [&](int h) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int g = 0; g < kHalf / 8; ++g) {
+                        float y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            y[i] = hidden(h, g * 8 + i) ? -INFINITY
+                                                        : __uint_as_float(x[g * 8 + i]);
+                        const float u = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[5]),
+                                             fmaxf(y[6], y[7]));
+                        top = fmaxf(top, PB ? u * sc[h * 8 + g].x : u);
+                    }
+                    return top;
+                };
                 auto cap_in_place = [&](int h0, int h1) {
 #pragma unroll 1
                     for (int q = h0 * 2; q < h1 * 2; ++q) {
@@ -1056,48 +1072,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 };
+                float top = -INFINITY;
                 if (kCapped && !kFix) {
                     float big = 0.f;
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         load(h);
                         big = fmaxf(big, magnitude(h));
+                        if (!kBiased) top = fmaxf(top, largest(h));
                     }
+                    if (top != -INFINITY) top = capped(PB ? top : top * scale, a.cap, a.cap_inv);
                     below = __all_sync(0xffffffffu, big < 1.f);  // (NaN counts as beyond)
                     if (!below) cap_in_place(0, 2);
                     choose();
                 }
                 if (!kFix) {
-                    float top = -INFINITY;
+                    if (!kCapped || kBiased) {
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        load(h);
-#pragma unroll
-                        for (int g = 0; g < kHalf / 8; ++g) {
-                            float y[8];
+                        for (int h = 0; h < 2; ++h) {
+                            load(h);
                             if constexpr (kBiased) {
-                                uint64_t e[4];
-                                exponents(h, g, 0.f, e);
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) unpair(e[i], y[2 * i], y[2 * i + 1]);
+                                for (int g = 0; g < kHalf / 8; ++g) {
+                                    float y[8];
+                                    uint64_t e[4];
+                                    exponents(h, g, 0.f, e);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) unpair(e[i], y[2 * i], y[2 * i + 1]);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i)
+                                        if (hidden(h, g * 8 + i)) y[i] = -INFINITY;
+                                    top = fmaxf(top, max3(max3(y[0], y[1], y[2]),
+                                                          max3(y[3], y[4], y[5]),
+                                                          fmaxf(y[6], y[7])));
+                                }
                             } else {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(x[g * 8 + i]);
+                                top = fmaxf(top, largest(h));
                             }
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (hidden(h, g * 8 + i)) y[i] = -INFINITY;
-                            const float u = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[5]),
-                                                 fmaxf(y[6], y[7]));
-                            top = fmaxf(top, kBiased || !PB || !below ? u : u * sc[h * 8 + g].x);
                         }
-                    }
-                    if (!kBiased && top != -INFINITY) {
-                        if (kCapped)
-                            top = below ? capped(PB ? top : top * scale, a.cap, a.cap_inv)
-                                        : top * a.cap;
-                        else if (!PB)
-                            top *= scale;
+                        if (!kBiased && !PB) top *= scale;  // (-infinity stays that)
                     }
                     const bool over = top > m + kGrow;
                     if (__any_sync(0xffffffffu, over)) {
