@@ -45,6 +45,7 @@ cudaError_t launch(Args& a, const Pool& p, const PageMaps& maps, cudaStream_t s)
     a.inv_group = 1.f / float(a.group);
     a.q_step = step(kBlock / (D / 8));
     a.o_step = step(32 / (D / 8));
+    a.part_step = step(32 / (D / 8));
     auto join_step = [&]() { return step(a.cluster * 8 * (32 / (D / 4))); };
     if (MOD != 0 && a.shared) {  // one more CTA for the starts
         a.cluster = 1;

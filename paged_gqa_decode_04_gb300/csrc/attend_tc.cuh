@@ -117,7 +117,7 @@ struct Args {
     // kShaped kernels
     float inv_group;        // 1 / group
     int2 q_step, o_step;    // tokens and heads of the rows between two of a thread's
-    int2 join_step;
+    int2 join_step, part_step;
     float cap, cap_inv;     // soft cap of the scores in base-2 units, and 1 over it
     float2 cap_poly[6];     // cap tanh(x) / x as a polynomial in x^2 (set_cap), each term twice
     const float* slopes;    // [hq], natural units a token of distance
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // memory, unnormalised, and every CTA of the cluster joins a share of them.  Plain kernels
     // do this with all warps, the others in the softmax warps, whose registers it needs: with
     // those that all warps have left, 48, a piece's results took 6000 cycles.
-    const bool joins = a.cluster > 1 || paired || prefix;
+    const bool joins = a.cluster > 1 || paired;
     auto results = [&]() {
     const bool failed = *gave_up || !s.ok || (warp < 8 && lost[at_row / 32] >> lane & 1);
     if (*gave_up && threadIdx.x == 0) latch(a.r.err, PGD_ERR_TIMEOUT);
@@ -629,7 +629,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t out_at = (int64_t)s.row0 * a.hq + (int64_t)head * a.group;  // head vectors
     // what the accumulator is to be multiplied with beside 1 / l
     const float by = !kQ8 ? 1.f : PB ? 1.f / vgain : __ldg(a.v_scale + head);
-    if (!joins) {
+    if (MOD != 0 && prefix && !joins) {
+        // this CTA's part of its rows, half of the columns at a time through the place that the
+        // block's queries had
+        if (warp < 8) {
+            constexpr int kCols = D / 2, kQuads = kCols / 4, kLines = 32 / kQuads;
+            static_assert(4 * 32 * kCols * 4 == L::kQ, "the warps' places");
+            const uint32_t to = tmem + (uint32_t(warp % 4 * 32) << 16) + 2 * kTile + blk * D;
+            const float inv = failed ? NAN : l > 0.f ? by / l : l == 0.f ? 0.f : NAN;
+            const bool have = blk ? sp[1].t1 > sp[1].t0 : sp[0].t1 > sp[0].t0;
+            const bool whole = inv == inv && l != 0.f;
+            const float fill = inv != inv ? NAN : 0.f;
+            uint8_t* const place = smem + blk * L::kQ + warp % 4 * (32 * kCols * 4);
+            const int line = lane / kQuads, c = lane % kQuads;  // kLines rows of a warp at once
+            const Walk from(a, f, warp * 32 + line, a.part_step, 1, a.hq);
+            const int64_t part = (int64_t)share * a.r.total * a.hq + out_at;
+            if (at_row < rows) {
+                const First x = row_at(a, f, at_row);
+                a.part_lse[part + (int64_t)x.token * a.hq + x.rem] =
+                    inv != inv ? 0.f
+                    : l == 0.f ? -INFINITY
+                               : m + __log2f(l) - (kQ8 && !PB ? kLift : 0.f);
+            }
+            if (warp * 32 < rows) {
+#pragma unroll 1
+                for (int i = 0; i < D; i += kCols) {
+                    uint32_t o[kCols];
+                    if (have) {
+#pragma unroll
+                        for (int e = 0; e < kCols; e += 32) tmem_ld32(to + i + e, o + e);
+                        wait_ld();
+#pragma unroll
+                        for (int e = 0; e < kCols; e += 32) keep32(o + e);
+                    }
+#pragma unroll
+                    for (int e = 0; e < kCols; e += 4) {
+                        float y[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            y[k] = whole ? __uint_as_float(o[e + k]) * inv : fill;
+                        *reinterpret_cast<float4*>(place + lane * (kCols * 4) +
+                                                   ((e / 4 ^ lane) & (kQuads - 1)) * 16) =
+                            make_float4(y[0], y[1], y[2], y[3]);
+                    }
+                    __syncwarp();
+                    Walk at = from;
+#pragma unroll
+                    for (int k = 0; k < 32 / kLines; ++k, at.next()) {
+                        const int r = line + k * kLines;  // of the warp's
+                        if (warp * 32 + r < rows)
+                            *reinterpret_cast<float4*>(a.part_o + (part + at.at) * D + i + c * 4) =
+                                *reinterpret_cast<const float4*>(place + r * (kCols * 4) +
+                                                                 ((c ^ r) & (kQuads - 1)) * 16);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    } else if (!joins) {
         if (warp < 8) {
             const uint32_t to = tmem + (uint32_t(warp % 4 * 32) << 16) + 2 * kTile + blk * D;
             const float inv = failed ? NAN : l > 0.f ? by / l : l == 0.f ? 0.f : NAN;
