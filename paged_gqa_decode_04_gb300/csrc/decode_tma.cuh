@@ -896,22 +896,43 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                   (a.window == 0 || c0 >= dsc.L - a.window - dsc.tok0);
                 if constexpr (C::EX) {
                     // capped, and less slope * distance: the row's own position is hi - 1
-                    auto shape = [&](float s, float slope, int from) {
-                        if (a.cap > 0.f) s = capped(s, a.cap, a.cap_inv);
-                        return fmaf(slope, (float)from, s);
-                    };
+                    constexpr int kRowsOf = C::ROWS16 ? 4 : 2;  // values of a lane's rows in use
+                    float big = 0.f;
+#pragma unroll
+                    for (int j = 0; j < C::CH / 8; ++j) {
+#pragma unroll
+                        for (int e = 0; e < kRowsOf; ++e) {
+                            sc[j][e] = fmaf(sc[j][e], smj[j], (e < 2 ? -qc0 : -qc1) * smj[j]);
+                            big = fmaxf(big, fabsf(sc[j][e]));
+                        }
+                    }
+                    // the polynomial alone where it does for the whole warp (a NaN stays one)
+                    const bool near = __all_sync(0xffffffffu, big * a.cap_inv < 0.5f);
+                    if (a.cap > 0.f && near) {
+#pragma unroll
+                        for (int j = 0; j < C::CH / 8; ++j) {
+#pragma unroll
+                            for (int e = 0; e < kRowsOf; ++e)
+                                sc[j][e] = a.cap * tanh_near(sc[j][e] * a.cap_inv);
+                        }
+                    } else if (a.cap > 0.f) {
+#pragma unroll
+                        for (int j = 0; j < C::CH / 8; ++j) {
+#pragma unroll
+                            for (int e = 0; e < kRowsOf; ++e)
+                                sc[j][e] = capped(sc[j][e], a.cap, a.cap_inv);
+                        }
+                    }
 #pragma unroll
                     for (int j = 0; j < C::CH / 8; ++j) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int tok = c0 + j * 8 + tig * 2 + e;
-                            const float s0 = shape(fmaf(sc[j][e], smj[j], -qc0 * smj[j]), sl0,
-                                                   tok - (hi0 - 1));
+                            const float s0 = fmaf(sl0, (float)(tok - (hi0 - 1)), sc[j][e]);
                             sc[j][e] = tok < hi0 && tok >= lo0 ? s0 : -INFINITY;
                             mx0 = fmaxf(mx0, sc[j][e]);
                             if (C::ROWS16) {
-                                const float s1 = shape(fmaf(sc[j][2 + e], smj[j], -qc1 * smj[j]),
-                                                       sl1, tok - (hi1 - 1));
+                                const float s1 = fmaf(sl1, (float)(tok - (hi1 - 1)), sc[j][2 + e]);
                                 sc[j][2 + e] = tok < hi1 && tok >= lo1 ? s1 : -INFINITY;
                                 mx1 = fmaxf(mx1, sc[j][2 + e]);
                             }

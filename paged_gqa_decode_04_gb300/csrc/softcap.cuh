@@ -11,12 +11,15 @@
 
 namespace pgd {
 
-__device__ __forceinline__ float capped(float s, float cap, float inv) {
-    const float x = s * inv, z = x * x;
+__device__ __forceinline__ float tanh_near(float x) {  // |x| < 1/2
+    const float z = x * x;
     float p = fmaf(z, 0.017135007f, -0.052986074f);
     p = fmaf(p, z, 0.13324779f);
     p = fmaf(p, z, -0.33333069f);
-    p = fmaf(p * z, x, x);
+    return fmaf(p * z, x, x);
+}
+__device__ __forceinline__ float capped(float s, float cap, float inv) {
+    const float x = s * inv, p = tanh_near(x);
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(x) * 2.8853900817779268f));
     float r;
