@@ -135,9 +135,10 @@ struct Args {
 // What a kernel does beside the plain attention: kShaped rows with a visible range of their own
 // and shared prefixes; with kCap and kBias besides, scores capped and less slope * distance.
 // kFixed: capped, and weights relative to a quarter of the cap instead of the row's maximum, which
-// then need not be found (4 prompts of up to 4096, 32/8 heads: 480 -> 400 us).  For bfloat16 pages
-// and caps up to kFixedMost base-2 units: weights are between 2^-100 and 2^60, where bfloat16 and
-// float32 are as precise as near 1, and sums over 2^31 tokens stay finite for values below 2^36.
+// then need not be found (4 prompts of up to 4096, 32/8 heads: 480 -> 400 us).  For caps up to
+// kFixedMost base-2 units, and with bfloat16 operands over 8-bit pages too (in which codes are
+// exact): weights are between 2^-100 and 2^60, where bfloat16 and float32 are as precise as near
+// 1, and sums over 2^31 tokens stay finite for values below 2^36.
 constexpr int kShaped = 1, kCap = 2, kBias = 4, kFixed = 8;
 constexpr float kFixedMost = 80.f;
 
@@ -410,6 +411,11 @@ template <int PAGE>
 __device__ __forceinline__ uint32_t operand2(float lo, float hi) {
     return PAGE == PGD_BF16 ? bf16x2(lo, hi) : f16x2(lo, hi);
 }
+// Exact for codes: 8 bits or fewer.
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t two) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+    return bf16x2(f.x, f.y);
+}
 // Four codes to two pairs of f16.
 template <int PAGE>
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
@@ -438,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap map_v) {
     using L = Layout<D, PAGE, PB>;
     constexpr bool kQ8 = L::kQ8;
+    constexpr bool kF16 = kQ8 && !(MOD & kFixed);  // the products' operands: f16, else bfloat16
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
@@ -529,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Queries of bfloat16 pages go to shared memory by asynchronous copies as soon as their rows
     // are known, while the rest is found out; 128 rows or fewer are for both blocks.
-    const bool early = MOD != 0 && !kQ8 && a.q_and == 0xffffffffu && a.q_xor == 0;
+    const bool early = MOD != 0 && !kF16 && a.q_and == 0xffffffffu && a.q_xor == 0;
     if (early && warp < 8) {
         constexpr int kVecs = D / 8, kStep = kBlock / kVecs;  // 16-byte pieces; rows at once
         const int r0 = threadIdx.x % kBlock, c = r0 % kVecs;
@@ -649,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 a.part_lse[part + (int64_t)x.token * a.hq + x.rem] =
                     inv != inv ? 0.f
                     : l == 0.f ? -INFINITY
-                               : m + __log2f(l) - (kQ8 && !PB ? kLift : 0.f);
+                               : m + __log2f(l) - (kF16 && !PB ? kLift : 0.f);
             }
             if (warp * 32 < rows) {
 #pragma unroll 1
@@ -884,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                 : sum[u] != sum[u]
                                                     ? 0.f
                                                     : top[u] + __log2f(sum[u]) -
-                                                          (kQ8 && !PB ? kLift : 0.f);
+                                                          (kF16 && !PB ? kLift : 0.f);
                             continue;
                         }
                         *reinterpret_cast<uint2*>(
@@ -942,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int r = my_row / kVecs + i * kStep;
                     auto operand = [&](uint32_t two) {
                         two = (two & a.q_and) ^ a.q_xor;
-                        return kQ8 ? f16x2(__uint_as_float(two << 16),
+                        return kF16 ? f16x2(__uint_as_float(two << 16),
                                            __uint_as_float(two & 0xffff0000u))
                                    : two;
                     };
@@ -1183,7 +1190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m = 0.25f * a.cap;
                 }
                 float off = m == -INFINITY ? 0.f : -m;
-                if (kQ8 && !PB) off += kLift;
+                if (kF16 && !PB) off += kLift;
                 uint64_t sum[2] = {0, 0};
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
@@ -1221,7 +1228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     part = i == 0 ? pair(e0, e1) : add2(part, pair(e0, e1));
                                 else
                                     sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(e0, e1));
-                                w[g * 4 - 4 + i / 2] = operand2<PAGE>(e0, e1);
+                                w[g * 4 - 4 + i / 2] = kF16 ? f16x2(e0, e1) : bf16x2(e0, e1);
                             }
                             if (PB) {
                                 const float over = sc[h * 8 + g - 1].z;
@@ -1238,6 +1245,97 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float s0, s1;
                 unpair(add2(sum[0], sum[1]), s0, s1);
                 l += s0 + s1;
+            };
+            // A tile with a bias and no cap that every row sees whole and all behind itself: the
+            // first half's weights are computed against the reference so far while the largest
+            // score is looked for.  That and the bias at the nearer end bound what the tile
+            // brings; where it might be too much (false) nothing was handed over.  (2048 of 8192
+            // tokens, 64/8 heads: 400 us, 459 with shaped_tile alone; packed documents without a
+            // bias gain nothing, 314 against 306.)
+            auto settled_tile = [&](int j) {
+                uint32_t x[kTile], w[kTile / 4];
+                uint64_t sum[2] = {0, 0};
+                float tops[4];
+                const float4* const sc = reinterpret_cast<const float4*>(
+                    smem + L::kScales + (PB ? (j - T0) % L::kScaleTiles * L::kScaleBytes : 0));
+                if (PB && sc[kTile / 8].x != vgain) return false;
+                const float far = float(tile_at(j) * kTile - pos);
+                float off = m == -INFINITY ? 0.f : -m;
+                if (kF16 && !PB) off += kLift;
+                const float c = fmaf(slope, far, off);
+#pragma unroll
+                for (int i = 0; i < kTile; i += 32) tmem_ld32(ts + i, x + i);
+                wait_ld();
+#pragma unroll
+                for (int i = 0; i < kTile; i += 32) keep32(x + i);
+                auto weigh = [&](int h) {
+#pragma unroll
+                    for (int g = 0; g <= 8; ++g) {
+                        const int at = h * (kTile / 2) + g * 8;
+                        if (g < 8) {
+                            if (h == 0) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    float u = __uint_as_float(x[g * 8 + i]);
+                                    float v = __uint_as_float(x[kTile / 2 + g * 8 + i]);
+                                    if (PB) u *= sc[g].x, v *= sc[8 + g].x;
+                                    tops[i % 4] = g == 0 && i < 4 ? fmaxf(u, v)
+                                                                  : max3(tops[i % 4], u, v);
+                                }
+                            }
+                            const float mul = PB ? sc[at / 8].x : scale;
+                            const float cl =
+                                fmaf(slope, float(at), c) + (PB ? sc[at / 8].y : 0.f);
+                            const uint64_t kk = pair(mul, mul), cc = pair(cl, cl);
+#pragma unroll
+                            for (int i = at; i < at + 8; i += 2) {
+                                float e0, e1;
+                                unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                            kk, add2(steps[(i - at) / 2], cc)),
+                                       e0, e1);
+                                x[i] = __float_as_uint(ex2(e0));
+                                x[i + 1] = __float_as_uint(ex2(e1));
+                            }
+                        }
+                        if (g > 0) {
+                            uint64_t part = 0;
+#pragma unroll
+                            for (int i = at - 8; i < at; i += 2) {
+                                const float e0 = __uint_as_float(x[i]);
+                                const float e1 = __uint_as_float(x[i + 1]);
+                                if (PB)
+                                    part = i == at - 8 ? pair(e0, e1) : add2(part, pair(e0, e1));
+                                else
+                                    sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(e0, e1));
+                                w[g * 4 - 4 + (i - at + 8) / 2] =
+                                    kF16 ? f16x2(e0, e1) : bf16x2(e0, e1);
+                            }
+                            if (PB) {
+                                const float over = sc[h * 8 + g - 1].z;
+                                sum[g & 1] = fma2(part, pair(over, over), sum[g & 1]);
+                            }
+                        }
+                    }
+                };
+                auto hand_over = [&](int h) {
+                    tmem_st32(ts + h * (kTile / 4), w);
+                    wait_st();
+                    fence_before();
+                    warp_arrive(bar_p + 16 * blk + 8 * h);
+                };
+                weigh(0);
+                float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
+                if (!PB) top *= scale;
+                top += fmaxf(slope * far, slope * (far + float(kTile - 1)));
+                // (a row that sees nothing is not looked at: it becomes zeros)
+                if (!__all_sync(0xffffffffu, top <= m + kGrow || my_hi <= my_lo)) return false;
+                hand_over(0);
+                weigh(1);
+                hand_over(1);
+                float s0, s1;
+                unpair(add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
+                return true;
             };
             // One tile of scores; `edge`: some row does not see all of it.
             auto tile = [&](int j, auto edge) {
@@ -1363,23 +1461,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = first; j < p.t1; j += by, phase ^= 1) {
                 if (!warp_wait(bar_s + 8 * blk, phase, gave_up)) break;
                 fence_after();
-                auto one = [&](auto edge) {
-                    if constexpr (MOD == 0) {
-                        tile(j, edge);
-                    } else if constexpr ((MOD & kBias) != 0 && (MOD & kCap) == 0) {
-                        if (__all_sync(0xffffffffu,
-                                       a.causal || tile_at(j) * kTile + kTile - 1 <= pos))
-                            shaped_tile(j, edge, std::true_type());
-                        else
-                            shaped_tile(j, edge, std::false_type());
-                    } else {
-                        shaped_tile(j, edge, std::false_type());
-                    }
-                };
-                if (tile_at(j) * kTile < p.lo_all || p.hi_all - tile_at(j) * kTile < kTile)
-                    one(std::true_type());
-                else
-                    one(std::false_type());
+                const int t = tile_at(j) * kTile;
+                const bool edge = t < p.lo_all || p.hi_all - t < kTile;
+                if constexpr (MOD == 0) {
+                    if (edge)
+                        tile(j, std::true_type());
+                    else
+                        tile(j, std::false_type());
+                } else if constexpr ((MOD & kCap) != 0 || !(MOD & kBias)) {
+                    if (edge)
+                        shaped_tile(j, std::true_type(), std::false_type());
+                    else
+                        shaped_tile(j, std::false_type(), std::false_type());
+                } else {
+                    // all that rows see of it is behind them: the bias is a line
+                    const bool behind =
+                        __all_sync(0xffffffffu, a.causal || t + kTile - 1 <= pos);
+                    if (!edge && behind && settled_tile(j)) continue;
+                    if (behind)
+                        shaped_tile(j, std::true_type(), std::true_type());
+                    else
+                        shaped_tile(j, std::true_type(), std::false_type());
+                }
             }
             warp_wait(bar_o + 8 * blk, 0, gave_up);
             if (MOD != 0 && my_hi <= my_lo) {  // a row that sees nothing
@@ -1426,6 +1529,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     widen4<PAGE>(x[i].y, y[2], y[3]);
                     widen4<PAGE>(x[i].z, y[4], y[5]);
                     widen4<PAGE>(x[i].w, y[6], y[7]);
+                    if (!kF16) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = f16x2_to_bf16x2(y[e]);
+                    }
                     const int t = tj * kTile + r;
                     if (edge && (t < lo || t >= hi)) {  // V rows no query sees
 #pragma unroll
@@ -1635,8 +1742,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if ((warp == 12 || warp == 13) && T1 > T0) {
         // --------------------------------------------------------------- products
-        constexpr uint32_t kQK = instruction(kBlock, kTile, !kQ8, 0);
-        constexpr uint32_t kPV = instruction(kBlock, D, !kQ8, 1);
+        constexpr uint32_t kQK = instruction(kBlock, kTile, !kF16, 0);
+        constexpr uint32_t kPV = instruction(kBlock, D, !kF16, 1);
         constexpr uint32_t kHi = operand_hi(1024);
         const int i = warp - 12;  // the block whose products this warp issues
         const int t0 = i ? sp[1].t0 : sp[0].t0, t1 = i ? sp[1].t1 : sp[0].t1;
