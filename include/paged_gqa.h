@@ -366,7 +366,11 @@ int paged_gqa_attend(pgd_pool_t pool, const void *q, int64_t q_stride, int total
  *
  * with p as in the plain call: Lb - n_b + i for query i of the n_b of a sequence (causal or
  * not), Lb - q_len + i in a decode.
- *   softcap      0 (none) or 2^-64 .. 2^64
+ *   softcap      0 (none) or 2^-64 .. 2^64.  tanh is taken to 2^-20 of its size or better.  An
+ *                attention with a cap up to 55 and no slopes keeps its weights relative to a
+ *                quarter of the cap, not of the row's largest score, and rounds them to bfloat16
+ *                (8-bit pages with scales per block: neither): cached values below 2^36 in
+ *                magnitude
  *   slopes       [Hq] float32, device, 4-byte aligned, finite, or NULL.  Scores and bias are
  *                summed in float32, in units of log 2: a bias of 2^k natural units has steps
  *                of about 2^(k-23)
@@ -377,6 +381,7 @@ int paged_gqa_attend(pgd_pool_t pool, const void *q, int64_t q_stride, int total
  *                values are fine; a row that sees nothing gets zeros.  Between the first and
  *                the last token that rows of a sequence see, its cached keys and values are
  *                expected to be finite and its block ids valid
+ * Hq / Hkv is at most 2^20 where anything is shaped.
  * With softcap 0, slopes NULL and visible NULL these are the plain calls.  Checks, errors,
  * workspace (decode: paged_gqa_workspace_size_ex) and everything else are theirs; the decode
  * also serves float32 pools (q_len 1, no window).
@@ -412,7 +417,8 @@ int paged_gqa_decode_shaped(pgd_pool_t pool, const void *q, int B, int q_len, in
  * within the batch or a negative shared length latch PGD_ERR_SEQ_LEN, and every sequence is
  * then read whole.  A block id out of range in a shared prefix makes the rows of its whole
  * group NaN.  bfloat16 and 8-bit pools (PGD_ERR_UNSUPPORTED for float32); over 8-bit pages the
- * limits of paged_gqa_attend hold for the prefix.  Three kernel launches.
+ * limits of paged_gqa_attend hold for the prefix, and with a cap those of
+ * paged_gqa_attend_shaped.  Three kernel launches.
  */
 int paged_gqa_decode_shared(pgd_pool_t pool, const void *q, int B, int q_len, int Hq,
                             const int32_t *cu_groups, const int32_t *shared_lens, int num_groups,

@@ -68,6 +68,8 @@ extern "C" int paged_gqa_attend_shaped(pgd_pool_t pool, const void* q, int64_t q
     if (window >= cap) window = 0;
     if (window > 0 && (int64_t)total + cap > INT32_MAX) return PGD_ERR_SHAPE;
     if ((int64_t)total * group > INT32_MAX / 2) return PGD_ERR_SHAPE;
+    const bool shaped = softcap > 0.f || slopes || visible;
+    if (shaped && group > attend::kMostGroup) return PGD_ERR_SHAPE;
     const int64_t pieces = max_pieces(total, B, group, attend::kRowShift, 1);
     if (pieces * p.hkv * 8 > INT32_MAX) return PGD_ERR_SHAPE;
     OnDevice dev(p.device);
@@ -94,7 +96,6 @@ extern "C" int paged_gqa_attend_shaped(pgd_pool_t pool, const void* q, int64_t q
     attend::set_cap(t, softcap * kLog2e);
     t.slopes = slopes;
     t.visible = reinterpret_cast<const int2*>(visible);
-    const bool shaped = softcap > 0.f || slopes || visible;
     const cudaError_t e = attend::launch_attend(t, p, page_maps(pool), shaped, s);
     return e == cudaSuccess ? PGD_OK : PGD_ERR_CUDA;
 }

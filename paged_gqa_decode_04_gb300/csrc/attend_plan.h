@@ -8,6 +8,9 @@ namespace attend {
 
 constexpr int kTile = 128;      // tokens of a key tile
 constexpr int kRowShift = 8;    // log2 of the rows of a CTA
+// Query heads of a KV head in the kernels with shaped scores: a row's place among them comes from
+// a float32 quotient, which is exact below 2^21.
+constexpr int kMostGroup = 1 << 20;
 
 // The most key tiles a piece of rows meets, when sequences have at most `max_len` tokens.  With
 // a window, its 256 rows (token, head of the group) lie in (254 + group) / group + 1 tokens or

@@ -64,6 +64,18 @@
 // with the softmax: 44% (scales per block).  ptxas spills 104 bytes of stores and 248 of loads
 // over bfloat16 pages, 180 and 416 to 200 and 464 over 8-bit ones.
 //
+// Shaped scores, visible ranges and shared prefixes are kernels of their own (MOD, kShaped and
+// the rest below) around the same pipeline:
+//     s = scale <q, k>;  s <- c tanh(s / c);  s <- s - slope |p - t|;  first <= t < end.
+// Their tiles are shaped_tile and settled_tile; tiles come from the last on where there is a bias;
+// results leave from the softmax warps.  Measured against the plain kernels on the same rows
+// (32/8 heads, 4 prompts of 2006 to 3900 tokens, scores up to +-20): 362 us under a cap of 50, 343
+// without; 2048 of 8192 tokens, 64/8 heads: 400 with a bias, 340 without.  A CTA's cycles on
+// documents of 1050 tokens packed into one of 16384 (6.7 tiles a piece, 44100): 3600 to find its
+// piece and send for the queries, 3200 for ranges, TMEM and the first barrier, 1000 and 3900 until
+// queries and first keys are there, 6400 for the first tile, 3100 for each other, 700 for the last
+// products, 4200 for the results.
+//
 // Every wait is bounded; one that gives up latches PGD_ERR_TIMEOUT and ends the CTA.
 #pragma once
 
@@ -135,7 +147,7 @@ struct Args {
 // What a kernel does beside the plain attention: kShaped rows with a visible range of their own
 // and shared prefixes; with kCap and kBias besides, scores capped and less slope * distance.
 // kFixed: capped, and weights relative to a quarter of the cap instead of the row's maximum, which
-// then need not be found (4 prompts of up to 4096, 32/8 heads: 480 -> 400 us).  For caps up to
+// then need not be found (the same prompts, at that stage 480 -> 400 us).  For caps up to
 // kFixedMost base-2 units, and with bfloat16 operands over 8-bit pages too (in which codes are
 // exact): weights are between 2^-100 and 2^60, where bfloat16 and float32 are as precise as near
 // 1, and sums over 2^31 tokens stay finite for values below 2^36.
@@ -169,9 +181,10 @@ struct Layout {
 
 // A polynomial P with x P(x^2) = tanh(x) to 6.7e-7 of its size for |x| below 1: a fit of
 // smallest largest relative error, by exchange, with P(0) = 1 so that small scores stay what they
-// are.  A score under a cap of 50 is off by 4e-5 in units of log 2 at most.  (Three terms do
-// below 0.32 and take 416 us instead of 480, but choosing between the two tile by tile 617: the
-// loop's code has to stay one.  4 prompts of up to 4096, 32/8 heads.)
+// are.  A score under a cap of 50 is off by 4e-5 in units of log 2 at most.  (At an earlier stage:
+// three terms, enough below 0.32, 416 us instead of 480, but chosen tile by tile 617, since the
+// loop's code has to stay one; one minus a quotient with an exponential 847.  4 prompts of up to
+// 4096, 32/8 heads.)
 constexpr int kTerms = 6;
 inline void set_cap(Args& a, float cap) {
     const double c[kTerms] = {1, -0.33330279671319310, 0.13288490272548903,
@@ -693,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (!joins) {
+    } else if (a.cluster == 1 && !paired) {
         if (warp < 8) {
             const uint32_t to = tmem + (uint32_t(warp % 4 * 32) << 16) + 2 * kTile + blk * D;
             const float inv = failed ? NAN : l > 0.f ? by / l : l == 0.f ? 0.f : NAN;
@@ -1844,8 +1857,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= 8) {
         // the join's shared memory is free once both blocks' products are over, and every
         // thread of a cluster takes part in its barriers
-        if (warp == 12 || warp == 13) asm volatile("bar.arrive 1, 320;" ::: "memory");
         if (joins) {
+            if (warp == 12 || warp == 13) asm volatile("bar.arrive 1, 320;" ::: "memory");
             cluster_sync();
             cluster_sync();
         }

@@ -26,9 +26,10 @@ def tail(b, decode):
 
 def check_rows(b, got, q, scale, decode=False, **kw):
     """Rows of a bfloat16 result against the definition.  The output's rounding, and the
-    weights', each half a bfloat16 step: 2^-8.  2^-12 for the rest: float32 sums, the cap's few
-    2^-22 of scores up to 72 in units of log 2, a bias' rounding of 2^-24 of up to 2^10, the
-    exponential's 2^-22, and parts joined in float32.  And the tail of weights in f16."""
+    weights', each half a bfloat16 step: 2^-8.  2^-12 for the rest: float32 sums, the cap's
+    6.7e-7 of scores up to 220 in units of log 2 (below a cap of 200, whose tanh is 0.77 there;
+    2^-21 beyond), a bias' rounding of 2^-24 of up to 2^10, the exponential's 2^-22, and parts
+    joined in float32.  And the tail of weights in f16."""
     want, size = ref.attend(q, b.k, b.v, b.k_scale, b.v_scale, b.cu, b.table, b.lens, scale, **kw)
     low = tail(b, decode) * max(b.lens)
     for row, y in want.items():

@@ -1,5 +1,9 @@
 """Attention with shaped scores (soft cap, distance bias, visible ranges) and decode with shared
 prefixes on the GPU, against their float64 definitions."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -204,6 +208,113 @@ def test_attend_masked_keys_may_hold_anything():
             if r != 60:
                 tol = 2.0 ** -8 * want[r].abs() + (2.0 ** -8 + 2.0 ** -12) * size[r]
                 assert torch.all((got[r].double() - want[r]).abs() <= tol)
+
+
+@pytest.mark.parametrize("pages,scales,d", FORMS)
+@pytest.mark.parametrize("cap", [2.0, 55.0, 56.0, 200.0])
+def test_attend_caps_and_where_scores_lie(cap, pages, scales, d):
+    """Caps on both sides of the one from which on weights are relative to the row's maximum;
+    scores far below the cap, about it and beyond it, in some rows and in all; rows whose scores
+    are all at the lower end of the cap."""
+    b = Batch([260, 140], [150, 140], hkv=1, d=d, pages=pages, scales=scales, seed=11)
+    q = b.rows(3).float()
+    size = torch.tensor([0.02, 1.0, 8.0, 60.0])[torch.arange(b.total) % 4]
+    size[200:] = 0.1
+    q = (q * size[:, None, None] * (2.0 if b.k_scale is None else 1.0)).to(torch.bfloat16)
+    check_attend(b, 3, q=q, scale=0.3, softcap=cap)
+    check_attend(b, 3, q=q, scale=0.3, softcap=cap, slopes=alibi(3), causal=False)
+    # every key the same: all scores of a row are equal, most at -cap or cap
+    b = Batch([130], [130], hkv=1, d=d, pages="bf16", seed=12)
+    b.k[:] = torch.where(b.k.isnan(), b.k, torch.ones((), dtype=b.k.dtype))
+    q = -torch.ones(130, 2, d, dtype=torch.bfloat16)
+    q[::3] = 0.01
+    check_attend(b, 2, q=q, scale=40.0, softcap=cap)
+
+
+def test_attend_values_of_any_usual_size():
+    """Values of 2^-20 and 2^30 keep their precision under a fixed reference."""
+    for size in (2.0 ** -20, 2.0 ** 30):
+        b = Batch([150], [150], hkv=1, seed=13)
+        b.v *= size
+        check_attend(b, 2, softcap=50.0)
+        check_attend(b, 2, softcap=50.0, causal=False)
+
+
+def test_attend_rows_of_a_wide_projection():
+    """Query rows as views, their stride not a power of two, and out given."""
+    b = Batch([90, 200], [90, 33], hkv=2, seed=14)
+    wide = torch.randn(b.total, 6 + 5, 128, generator=b.g).to(torch.bfloat16)
+    q = wide[:, 3:9]
+    out = torch.full((b.total, 6, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = check_attend(b, 6, q=q, softcap=4.0, slopes=alibi(6), out=out)
+    assert torch.equal(got, out.cpu())
+
+
+CAPTURED_FIRST = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+import paged_gqa_decode_04_gb300 as pgd
+from shaped_cases import alibi, group_tables, shared_batch
+groups, n = [(0, 3)], [300]
+b = shared_batch([20, 7, 64], groups, n, hkv=2, pages=%r, scales="block", seed=7)
+pool = b.pool()
+q = b.rows(4, packed=False).cuda()
+cu, table, lens = b.where()
+cg, shared = group_tables(groups, n)
+sl = alibi(4).cuda()
+ws, wd = pgd.alloc_workspace_shared(pool, 3, 1, 4, 1), pgd.alloc_workspace(pool, 3, 4)
+outs = [torch.zeros_like(q) for _ in range(4)]
+def step(s):
+    kw = dict(softcap=5.0, stream=s)
+    pgd.paged_gqa_attend(pool, q, cu, table, lens, 0.1, out=outs[0], **kw)
+    pgd.paged_gqa_attend(pool, q, cu, table, lens, 0.1, slopes=sl, out=outs[1], stream=s)
+    pgd.paged_gqa_decode_ex(pool, q.view(3, 1, 4, 128), table, lens, 0.1, slopes=sl, workspace=wd,
+                            out=outs[2].view(3, 1, 4, 128), **kw)
+    pgd.paged_gqa_decode_shared(pool, q, cg, shared, table, lens, 0.1, workspace=ws,
+                                out=outs[3], **kw)
+torch.cuda.synchronize()
+g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.graph(g, stream=s):
+    step(s)
+g.replay()
+torch.cuda.synchronize()
+first = [t.clone() for t in outs]
+for t in outs: t.zero_()
+torch.cuda.synchronize()
+step(s)
+s.synchronize()
+assert pgd.paged_gqa_get_error(pool) == 0
+for x, y in zip(first, outs):
+    assert x.abs().sum() > 0 and torch.equal(x, y)
+print("same")
+"""
+
+
+@pytest.mark.parametrize("pages", ["bf16", "e4m3"])
+def test_first_calls_of_a_process_are_captured(pages):
+    """The first calls of a process inside a graph capture, replayed: what eager calls give."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = CAPTURED_FIRST % (os.path.dirname(here), here, pages)
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240)
+    assert res.returncode == 0 and res.stdout.strip() == "same", res.stderr[-2000:]
+
+
+def test_many_groups_and_sequences():
+    """More groups than a warp looks at, of one to five sequences, some without tokens."""
+    g = torch.Generator().manual_seed(3)
+    groups, n, own, at = [], [], [], 0
+    for i in range(70):
+        size = i % 5 + 1
+        groups.append((at, at + size))
+        n.append(int(torch.randint(0, 60, (1,), generator=g)))
+        own += [(-1 if (at + k) % 13 == 5 else int(torch.randint(1, 30, (1,), generator=g)))
+                for k in range(size)]
+        at += size
+    b = shared_batch(own, groups, n, hkv=1, bs=8, seed=15)
+    q = b.rows(2, packed=False)
+    got = run_shared(b, q, groups, n, 1, 0.1)
+    check_rows(b, got, q, 0.1, decode=True)
 
 
 # ------------------------------------------------------------------------------- decode
