@@ -1,5 +1,6 @@
-// paged_gqa_attend, paged_gqa_attend_shaped: attention of a ragged batch of query tokens over the pages,
-// causal (prompts, chunks of prompts) or over all cached tokens (cross attention).
+// paged_gqa_attend, paged_gqa_attend_shaped: attention of a ragged batch of query tokens over
+// the pages, causal (prompts, chunks of prompts) or over all cached tokens (cross attention), with
+// plain scores or with capped and biased ones and ranges of visible tokens.
 // See include/paged_gqa.h for the contract.
 //
 //     out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale <q, k_t> - m), m = max_t,

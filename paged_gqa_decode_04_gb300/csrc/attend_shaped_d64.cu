@@ -1,4 +1,5 @@
-// The attention kernels with shaped scores and shared prefixes over bfloat16 pages, head_dim 64.
+// The attention kernels with shaped scores and shared prefixes:
+// bfloat16 pages, head_dim 64.
 #include "attend_launch.cuh"
 
 namespace pgd {

@@ -1,4 +1,5 @@
-// The attention kernels with shaped scores and shared prefixes over e4m3 pages with a scale per block.
+// The attention kernels with shaped scores and shared prefixes:
+// e4m3 pages with a scale per block.
 #include "attend_launch.cuh"
 
 namespace pgd {

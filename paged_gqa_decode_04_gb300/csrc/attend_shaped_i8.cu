@@ -1,4 +1,5 @@
-// The attention kernels with shaped scores and shared prefixes over int8 pages with a scale per KV head.
+// The attention kernels with shaped scores and shared prefixes:
+// int8 pages with a scale per KV head.
 #include "attend_launch.cuh"
 
 namespace pgd {

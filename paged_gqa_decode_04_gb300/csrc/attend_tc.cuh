@@ -374,13 +374,6 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
     asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
     return m;
 }
-__device__ __forceinline__ float max8_abs(const uint32_t* x) {
-    const float a =
-        max3_abs(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
-    const float b =
-        max3_abs(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
-    return max3_abs(max3_abs(a, b, __uint_as_float(x[6])), __uint_as_float(x[7]), 0.f);
-}
 __device__ __forceinline__ float max8(const uint32_t* x) {
     const float a = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
     const float b = max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
@@ -933,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 copies_landed();
             } else {
                 // the block's queries into shared memory, swizzled
-                constexpr int kVecs = D / 8, kStep = kBlock / kVecs;  // 16-byte pieces; rows at once
+                constexpr int kVecs = D / 8, kStep = kBlock / kVecs;  // as above
                 const int c = my_row % kVecs;
                 const __nv_bfloat16* q =
                     a.q + (int64_t)s.row0 * a.q_stride + (int64_t)head * a.group * D + c * 8;
@@ -941,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint4 x[kVecs];
                 if constexpr (MOD != 0) {
                     Walk at(a, f, first_row, a.q_step, D, a.q_stride);
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < kVecs; ++i, at.next()) {  // all loads, then all stores
                         x[i] = make_uint4(0, 0, 0, 0);
                         if (first_row + i * kStep < rows)
@@ -949,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 } else {
                     Rows at(row0 + first_row, group, kStep);
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < kVecs; ++i, at.next()) {
                         x[i] = make_uint4(0, 0, 0, 0);
                         if (first_row + i * kStep < rows)
@@ -957,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                         at.head * D));
                     }
                 }
-    #pragma unroll
+#pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
                     const int r = my_row / kVecs + i * kStep;
                     auto operand = [&](uint32_t two) {
@@ -966,8 +959,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            __uint_as_float(two & 0xffff0000u))
                                    : two;
                     };
-                    *reinterpret_cast<uint4*>(smem + blk * L::kQ + c / 8 * (kBlock * 128) + r * 128 +
-                                              ((c ^ r) & 7) * 16) =
+                    *reinterpret_cast<uint4*>(smem + blk * L::kQ + c / 8 * (kBlock * 128) +
+                                              r * 128 + ((c ^ r) & 7) * 16) =
                         make_uint4(operand(x[i].x), operand(x[i].y), operand(x[i].z),
                                    operand(x[i].w));
                 }
@@ -1083,7 +1076,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 8; ++i)
                             y[i] = hidden(h, g * 8 + i) ? 0.f : __uint_as_float(x[g * 8 + i]);
                         const float u = max3_abs(max3_abs(y[0], y[1], y[2]),
-                                                 max3_abs(y[3], y[4], y[5]), max3_abs(y[6], y[7], 0.f));
+                                                 max3_abs(y[3], y[4], y[5]),
+                                                 max3_abs(y[6], y[7], 0.f));
                         big = fmaxf(big, PB ? u * sc[h * 8 + g].x : u);
                     }
                     return big * (PB ? a.cap_inv : scale * a.cap_inv);
@@ -1159,7 +1153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!kBiased) top = fmaxf(top, largest(h));
                     }
                     if (top != -INFINITY) top = capped(PB ? top : top * scale, a.cap, a.cap_inv);
-                    below = __all_sync(0xffffffffu, big < 1.f);  // (NaN counts as beyond)
+                    below = __all_sync(0xffffffffu, big < 1.f);  // (NaN stay what they are)
                     if (!below) cap_in_place(0, 2);
                     choose();
                 }
@@ -1175,7 +1169,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     uint64_t e[4];
                                     exponents(h, g, 0.f, e);
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) unpair(e[i], y[2 * i], y[2 * i + 1]);
+                                    for (int i = 0; i < 4; ++i)
+                                        unpair(e[i], y[2 * i], y[2 * i + 1]);
 #pragma unroll
                                     for (int i = 0; i < 8; ++i)
                                         if (hidden(h, g * 8 + i)) y[i] = -INFINITY;

@@ -1,5 +1,6 @@
-// The TMA decode kernel for head_dim 64, with shaped scores (softcap,
-// distance bias), sequences walked from a start and results left for a join.
+// The TMA decode kernel for head_dim 64,
+// with shaped scores (softcap, distance bias), sequences walked from a start and results
+// left for a join.
 #include "decode_tma.cuh"
 
 namespace pgd {

@@ -1,5 +1,6 @@
-// The TMA decode kernel for e4m3 pages with a scale per block and KV head, with shaped scores (softcap,
-// distance bias), sequences walked from a start and results left for a join.
+// The TMA decode kernel for e4m3 pages with a scale per block and KV head,
+// with shaped scores (softcap, distance bias), sequences walked from a start and results
+// left for a join.
 #include "decode_tma.cuh"
 
 namespace pgd {

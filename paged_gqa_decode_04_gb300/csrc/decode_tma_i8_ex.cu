@@ -1,5 +1,6 @@
-// The TMA decode kernel for int8 pages with a scale per KV head, with shaped scores (softcap,
-// distance bias), sequences walked from a start and results left for a join.
+// The TMA decode kernel for int8 pages with a scale per KV head,
+// with shaped scores (softcap, distance bias), sequences walked from a start and results
+// left for a join.
 #include "decode_tma.cuh"
 
 namespace pgd {

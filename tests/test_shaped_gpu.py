@@ -417,7 +417,8 @@ def test_shared(pages, scales, d, shape, q_len):
 
 
 @pytest.mark.parametrize("pages,scales", [("bf16", "head"), ("e4m3", "block")])
-@pytest.mark.parametrize("B,hkv,group,prefix", [(40, 1, 8, 2500), (5, 8, 4, 1300), (100, 2, 4, 600)])
+@pytest.mark.parametrize("B,hkv,group,prefix",
+                         [(40, 1, 8, 2500), (5, 8, 4, 1300), (100, 2, 4, 600)])
 def test_shared_long(B, hkv, group, prefix, pages, scales):
     """Many parts of a prefix, paired blocks of rows and more than 256 rows."""
     g = torch.Generator().manual_seed(B)
