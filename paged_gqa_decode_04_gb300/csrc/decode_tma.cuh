@@ -286,7 +286,7 @@ struct Cfg {
     static constexpr bool FP8 = FP8_;         // 8-bit K/V pages, f16 products
     static constexpr bool INT8 = INT8_;       // 8-bit pages hold int8 codes (else e4m3)
     static constexpr bool PB = PB_;           // 8-bit pages with a scale per block and KV head
-    // scores capped and with a distance bias (a.softcap, a.slopes), sequences walked from
+    // scores capped and with a distance bias (a.cap, a.slopes), sequences walked from
     // a.starts on, results for a later join (a.row_o): see DecodeArgs
     static constexpr bool EX = EX_;
     // merge variant of split runs: 0 the last arriver merges with register
