@@ -15,7 +15,7 @@ from ._lib import PagedGQAError, STATUS_NAMES, strerror  # noqa: F401
 from .kv_cache import (KVBlockManager, alloc_workspace_shared, paged_gqa_attend,  # noqa: F401
                        paged_gqa_decode_shared, paged_gqa_workspace_size_shared,
                        paged_kv_append, paged_kv_copy_blocks, paged_kv_read, paged_kv_write,
-                       paged_qk_norm_rope_write, rope_table, _slopes_ptr)
+                       paged_qk_norm_rope_write, rope_table, _slopes_ptr, _stream_on)
 
 __all__ = [
     "PagedKVPool", "PagedGQAError", "paged_kv_pool_create", "paged_kv_pool_destroy",
@@ -229,7 +229,7 @@ def paged_gqa_decode_ex(pool, q, block_table, seq_lens, scale, window=0, out=Non
                                        seq_lens.data_ptr(), int(window), float(scale),
                                        float(softcap), _slopes_ptr(pool, slopes, Hq),
                                        out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                       int(num_splits), _stream_handle(stream)),
+                                       int(num_splits), _stream_on(pool, stream)),
            "paged_gqa_decode_ex")
     return out
 

@@ -433,9 +433,12 @@ int decode_ex_impl(pgd_pool_t pool, const void* q, int B, int q_len, int Hq,
         if (launch_decode_simple(a, p.dtype, s) != cudaSuccess) return PGD_ERR_CUDA;
         if (launch_merge(a, p.dtype, s) != cudaSuccess) return PGD_ERR_CUDA;
     } else if (softcap > 0.f || slopes) {
-        // where the plain decode shares or separates its merge the runs are long or many:
-        // joined by a second kernel
-        a.join = a.merge_variant != 0;
+        // Joined by a second kernel where the plain decode shares or separates its merge, and
+        // over heads of 64 (which have one merge in the plain decode, by the last arriver) where
+        // runs are no more than spans.  Measured, last arriver and join, in a graph: one sequence
+        // of 8192, 32/8 heads of 64: 61 and 21 us, 8/1 heads 20 and 13; 4 of 300, 8/2 heads 13 and
+        // 12; 64 of 2000, 32/8 heads 56 both.  256 of 600, heads of 128: 98 and 103.
+        a.join = a.merge_variant != 0 || (p.d == 64 && (int64_t)B * a.units <= a.num_parts);
         if (launch_decode_ex(a, p, s) != cudaSuccess) return PGD_ERR_CUDA;
         if (a.join && launch_join(a, s) != cudaSuccess) return PGD_ERR_CUDA;
     } else {

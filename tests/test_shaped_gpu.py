@@ -358,6 +358,20 @@ def test_decode_long_runs(B, hkv, group, pages):
         check_rows(b, got, q, 128 ** -0.5, decode=True, **kw)
 
 
+@pytest.mark.parametrize("B,hkv,group,q_len", [(1, 1, 8, 1), (2, 8, 4, 2), (30, 4, 3, 1),
+                                               (200, 2, 2, 1)])
+def test_decode_heads_of_64(B, hkv, group, q_len):
+    """Joined runs, long and short, and more runs than spans, which their last arriver merges."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(2, 1200 if B < 100 else 150, (B,), generator=g).tolist()
+    b = Batch(lens, [q_len] * B, hkv=hkv, d=64, seed=B)
+    q = b.rows(hkv * group, packed=False) * 2
+    for kw in (dict(softcap=20.0), dict(slopes=alibi(hkv * group))):
+        for splits in (0, 40):
+            got = run_decode(b, q, q_len, 0.125, num_splits=splits, **kw)
+            check_rows(b, got, q, 0.125, decode=True, **kw)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_decode_float32(d):
     """The float32 path: 1e-5 for values and weights near 1, as for plain scores."""
