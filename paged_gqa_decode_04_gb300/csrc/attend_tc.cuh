@@ -1497,6 +1497,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m = -INFINITY;
                 l = 0.f;
             }
+        } else if (early) {
+            // A block without a tile has no use for its queries, but results() writes to where
+            // they are on their way to: rows whose copies other threads of the block started.
+            copies_landed();
+            asm volatile("bar.sync %0, 128;" ::"r"(2 + blk) : "memory");
         }
         if constexpr (MOD != 0) {
             fence_after();

@@ -1,0 +1,117 @@
+"""Attention with shaped scores, decode and shared prefixes where they can go wrong: blocks of rows
+without a tile, steep and far biases, workspaces of many shapes, given streams, the C entry points."""
+import pytest
+import torch
+
+import paged_gqa_decode_04_gb300 as pgd
+from oracle import shaped
+from page_ops_cases import Batch
+from paged_gqa_decode_04_gb300 import _lib
+from shaped_cases import alibi, check_rows
+
+pytestmark = pytest.mark.gpu
+
+
+def ok(pool):
+    assert pgd.paged_gqa_get_error(pool) == 0
+
+
+def busy(n=1 << 26):
+    """A stream that reads and writes memory without a pause, as a call's neighbour."""
+    s = torch.cuda.Stream()
+    x = torch.zeros(n, device="cuda")
+    torch.cuda.synchronize()
+
+    def work():
+        with torch.cuda.stream(s):
+            for _ in range(3):
+                x.add_(1.0)
+    return work
+
+
+def check_again_and_again(b, heads, times=40, **kw):
+    """The call many times over on two streams beside other work: the first result against the
+    definition, every other one the same bits."""
+    q = b.rows(heads) * 3
+    scale = b.d ** -0.5
+    pool, dq, where = b.pool(), b.to(q), b.where()
+    dev = {k: v.cuda() if torch.is_tensor(v) else v for k, v in kw.items()}
+    outs = [torch.full((b.total, heads, b.d), 7.0, dtype=b.act, device="cuda")
+            for _ in range(times)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    work = busy()
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        work()
+        pgd.paged_gqa_attend(pool, dq, *where, scale, out=out, stream=streams[i % 2], **dev)
+    torch.cuda.synchronize()
+    ok(pool)
+    pool.close()
+    first = outs[0].cpu()
+    check_rows(b, first, q, scale, **kw)
+    assert torch.all(first[int(b.cu[-1]):] == 7)
+    for out in outs:
+        assert torch.equal(out, outs[0])
+    return first
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hide", [(0, 128), (100, 500), (200, 600), (472, 600)])
+def test_blocks_of_rows_that_see_nothing(hide, d):
+    """Hidden rows that fill blocks of 128 (32 tokens of 4 heads a group) at the beginning, inside
+    and at the end of a sequence, beside blocks that see something."""
+    b = Batch([600, 40], [600, 40], hkv=2, d=d, seed=hide[0], pad=2)
+    vis = torch.tensor([[0, 2 ** 31 - 1]], dtype=torch.int32).repeat(b.total, 1)
+    vis[hide[0]:hide[1], 1] = 0
+    for kw in ({}, dict(softcap=20.0), dict(softcap=100.0), dict(slopes=alibi(8))):
+        got = check_again_and_again(b, 8, visible=vis, **kw)
+        assert torch.all(got[hide[0]:hide[1]] == 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_cross_attention_to_nothing(d):
+    """Sequences without cached tokens beside one with many, every query of theirs zeros."""
+    b = Batch([0, 300, 0], [200, 100, 33], hkv=2, d=d, seed=1)
+    for kw in (dict(softcap=20.0), dict(slopes=alibi(8))):
+        got = check_again_and_again(b, 8, causal=False, **kw)
+        assert torch.all(got[:200] == 0) and torch.all(got[300:] == 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [1, 20, 200])
+def test_short_sequences_in_wide_clusters(rows, d):
+    """Sequences of one to three tiles behind a table for 512, whose width is what the cluster size
+    is chosen by: CTAs of a cluster without a tile, in calls of few and of many rows."""
+    b = Batch([max(rows, x) for x in (30, 128, 300, 1)], [rows, rows, rows, min(rows, 2)], hkv=1,
+              d=d, seed=rows)
+    wide = torch.full((4, 4096 - b.table.shape[1]), -1, dtype=torch.int32)
+    b.table = torch.cat([b.table, wide], 1).contiguous()
+    vis = torch.tensor([[0, 2 ** 31 - 1]], dtype=torch.int32).repeat(b.total, 1)
+    vis[::3, 1] = 10
+    for kw in (dict(softcap=20.0), dict(slopes=alibi(4)), dict(visible=vis)):
+        check_again_and_again(b, 4, **kw)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_sequences_of_impossible_length(d):
+    """Their rows are NaN, not what lay in shared memory; the others are right."""
+    b = Batch([200, 70], [200, 70], hkv=2, d=d, seed=2)
+    q = b.rows(8)
+    pool, dq = b.pool(), b.to(q)
+    cu, table, lens = b.where()
+    lens[0] = table.shape[1] * b.bs + 1
+    work = busy()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        work()
+        outs.append(pgd.paged_gqa_attend(pool, dq, cu, table, lens, 0.1, softcap=20.0))
+    torch.cuda.synchronize()
+    assert pgd.paged_gqa_get_error(pool) == _lib.PGD_ERR_SEQ_LEN
+    pool.close()
+    want, size = shaped.attend(q, b.k, b.v, None, None, b.cu, b.table, b.lens, 0.1, softcap=20.0)
+    for out in outs:
+        assert torch.all(out[:200].isnan()) and torch.equal(out[200:], outs[0][200:])
+    for row in range(200, 270):
+        tol = 2.0 ** -8 * want[row].abs() + (2.0 ** -8 + 2.0 ** -12) * size[row]
+        assert torch.all((outs[0][row].cpu().double() - want[row]).abs() <= tol)
