@@ -581,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sp[i].t1 = (v.y - 1) / kTile + 1;
             }
         }
+        fence_smem_async();  // before the tiles' copies write there
     } else {
         sp[0] = span_of(a, s, row0, row0 + min(rows, kBlock) - 1);
         sp[1] = span_of(a, s, row0 + kBlock, row0 + rows - 1);
