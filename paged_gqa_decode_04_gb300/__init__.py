@@ -15,7 +15,8 @@ from ._lib import PagedGQAError, STATUS_NAMES, strerror  # noqa: F401
 from .kv_cache import (KVBlockManager, alloc_workspace_shared, paged_gqa_attend,  # noqa: F401
                        paged_gqa_decode_shared, paged_gqa_workspace_size_shared,
                        paged_kv_append, paged_kv_copy_blocks, paged_kv_read, paged_kv_write,
-                       paged_qk_norm_rope_write, rope_table, _slopes_ptr, _stream_on)
+                       paged_qk_norm_rope_write, rope_table, _empty_on, _slopes_ptr,
+                       _stream_on, _zeros_on)
 
 __all__ = [
     "PagedKVPool", "PagedGQAError", "paged_kv_pool_create", "paged_kv_pool_destroy",
@@ -188,13 +189,14 @@ def paged_gqa_decode(pool, q, block_table, seq_lens, scale, out=None, workspace=
     _check_decode_args(pool, q, block_table, seq_lens, 3)
     B, Hq, D = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_on(pool, stream, tuple(q.shape))
     if workspace is None:
-        workspace = alloc_workspace(pool, B, Hq, num_splits)
+        workspace = _zeros_on(pool, stream, max(
+            paged_gqa_workspace_size(pool, B, Hq, num_splits), 256))
     _check(lib.paged_gqa_decode(pool.handle, q.data_ptr(), B, Hq, block_table.data_ptr(),
                                 block_table.shape[1], seq_lens.data_ptr(), float(scale),
                                 out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                int(num_splits), _stream_handle(stream)), "paged_gqa_decode")
+                                int(num_splits), _stream_on(pool, stream)), "paged_gqa_decode")
     return out
 
 
@@ -220,10 +222,10 @@ def paged_gqa_decode_ex(pool, q, block_table, seq_lens, scale, window=0, out=Non
     _check_decode_args(pool, q, block_table, seq_lens, 4)
     B, q_len, Hq, D = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_on(pool, stream, tuple(q.shape))
     if workspace is None:
-        nbytes = paged_gqa_workspace_size_ex(pool, B, q_len, Hq, num_splits)
-        workspace = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = _zeros_on(pool, stream, max(
+            paged_gqa_workspace_size_ex(pool, B, q_len, Hq, num_splits), 256))
     _check(lib.paged_gqa_decode_shaped(pool.handle, q.data_ptr(), B, q_len, Hq,
                                        block_table.data_ptr(), block_table.shape[1],
                                        seq_lens.data_ptr(), int(window), float(scale),
@@ -303,13 +305,13 @@ def paged_gqa_decode_host(pool, q, block_table, seq_lens, scale, window=0, out=N
         raise ValueError("out must be a contiguous CPU tensor shaped and typed like q")
     max_blocks = block_table.shape[1]
     if workspace is None:
-        nbytes = paged_gqa_workspace_size_host(pool, B, q_len, Hq, max_blocks, num_splits)
-        workspace = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=pool.k_pool.device)
+        workspace = _zeros_on(pool, stream, max(paged_gqa_workspace_size_host(
+            pool, B, q_len, Hq, max_blocks, num_splits), 256))
     _check(lib.paged_gqa_decode_host(pool.handle, q.data_ptr(), B, q_len, Hq,
                                      block_table.data_ptr(), max_blocks, seq_lens.data_ptr(),
                                      int(window), float(scale), out.data_ptr(),
                                      workspace.data_ptr(), workspace.numel(), int(num_splits),
-                                     _stream_handle(stream)), "paged_gqa_decode_host")
+                                     _stream_on(pool, stream)), "paged_gqa_decode_host")
     return out
 
 

@@ -115,3 +115,44 @@ def test_sequences_of_impossible_length(d):
     for row in range(200, 270):
         tol = 2.0 ** -8 * want[row].abs() + (2.0 ** -8 + 2.0 ** -12) * size[row]
         assert torch.all((outs[0][row].cpu().double() - want[row]).abs() <= tol)
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_decodes_on_a_given_stream_without_a_workspace(as_int):
+    """Decodes make their workspace and output on the stream that they are launched on: with
+    the current stream busy, and its memory dirty and soon handed out again, every result is
+    right."""
+    g = torch.Generator().manual_seed(5)
+    lens = torch.randint(500, 4000, (6,), generator=g).tolist()
+    b = Batch(lens, [1] * 6, hkv=2, d=64, seed=6)
+    q = b.rows(8, packed=False)
+    pool, dq, table, lens = b.pool(), q.cuda(), b.table.cuda(), b.len_t.cuda()
+    h_q, h_table, h_lens = q.contiguous(), b.table, b.len_t
+    n = max(pgd.paged_gqa_workspace_size_host(pool, 6, 1, 8, b.table.shape[1]), 1 << 20)
+    side = torch.cuda.Stream()
+    x = torch.zeros(1 << 26, device="cuda")
+    torch.cuda.synchronize()
+    outs, host, s = [], [], side.cuda_stream if as_int else side
+    for i in range(30):
+        for _ in range(2):
+            x.add_(1.0)
+        dirt = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+        del dirt
+        kw = dict(softcap=20.0) if i % 3 == 0 else {}
+        if i % 3 < 2:
+            outs.append((kw, pgd.paged_gqa_decode_ex(pool, dq.view(6, 1, 8, 64), table, lens, 0.1,
+                                                     stream=s, **kw)))
+        else:
+            outs.append((kw, pgd.paged_gqa_decode(pool, dq, table, lens, 0.1, stream=s)))
+        host.append(pgd.paged_gqa_decode_host(pool, h_q, h_table, h_lens, 0.1, stream=s))
+        dirt = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+        del dirt
+    torch.cuda.synchronize()
+    ok(pool)
+    for i, (kw, out) in enumerate(outs):
+        got = out.cpu().view(6, 8, 64)
+        if i < 3:
+            check_rows(b, got, q, 0.1, decode=True, **kw)
+        assert torch.equal(got, outs[i % 3 if kw else 1][1].cpu().view(6, 8, 64))
+        assert torch.equal(host[i], outs[1][1].cpu().view(6, 8, 64))
+    pool.close()
