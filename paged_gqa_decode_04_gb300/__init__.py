@@ -173,8 +173,20 @@ def _check_decode_args(pool, q, block_table, seq_lens, q_dims):
             seq_lens.shape[0] != q.shape[0]):
         raise ValueError("shape mismatch between q, tables and pool")
     for t in (q, block_table, seq_lens):
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError("inputs must be contiguous CUDA tensors")
+        if t.get_device() != pool.device.index or not t.is_contiguous():
+            raise ValueError("inputs must be contiguous CUDA tensors on the pool's device")
+
+
+def _check_out(pool, q, out, workspace):
+    """Types, sizes and placement of a decode's output and workspace."""
+    if out.dtype is not q.dtype:
+        raise TypeError("out must be %s like q" % q.dtype)
+    if out.numel() < q.numel():
+        raise ValueError("out is smaller than q")
+    for t in (out, workspace):
+        if t.get_device() != pool.device.index or not t.is_contiguous():
+            raise ValueError("out and workspace must be contiguous CUDA tensors on the pool's "
+                             "device")
 
 
 def paged_gqa_decode(pool, q, block_table, seq_lens, scale, out=None, workspace=None,
@@ -193,9 +205,11 @@ def paged_gqa_decode(pool, q, block_table, seq_lens, scale, out=None, workspace=
     if workspace is None:
         workspace = _zeros_on(pool, stream, max(
             paged_gqa_workspace_size(pool, B, Hq, num_splits), 256))
+    _check_out(pool, q, out, workspace)
     _check(lib.paged_gqa_decode(pool.handle, q.data_ptr(), B, Hq, block_table.data_ptr(),
                                 block_table.shape[1], seq_lens.data_ptr(), float(scale),
-                                out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                out.data_ptr(), workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(),
                                 int(num_splits), _stream_on(pool, stream)), "paged_gqa_decode")
     return out
 
@@ -226,11 +240,13 @@ def paged_gqa_decode_ex(pool, q, block_table, seq_lens, scale, window=0, out=Non
     if workspace is None:
         workspace = _zeros_on(pool, stream, max(
             paged_gqa_workspace_size_ex(pool, B, q_len, Hq, num_splits), 256))
+    _check_out(pool, q, out, workspace)
     _check(lib.paged_gqa_decode_shaped(pool.handle, q.data_ptr(), B, q_len, Hq,
                                        block_table.data_ptr(), block_table.shape[1],
                                        seq_lens.data_ptr(), int(window), float(scale),
                                        float(softcap), _slopes_ptr(pool, slopes, Hq),
-                                       out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                       out.data_ptr(), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(),
                                        int(num_splits), _stream_on(pool, stream)),
            "paged_gqa_decode_ex")
     return out
@@ -307,10 +323,13 @@ def paged_gqa_decode_host(pool, q, block_table, seq_lens, scale, window=0, out=N
     if workspace is None:
         workspace = _zeros_on(pool, stream, max(paged_gqa_workspace_size_host(
             pool, B, q_len, Hq, max_blocks, num_splits), 256))
+    if workspace.get_device() != pool.device.index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the pool's device")
     _check(lib.paged_gqa_decode_host(pool.handle, q.data_ptr(), B, q_len, Hq,
                                      block_table.data_ptr(), max_blocks, seq_lens.data_ptr(),
                                      int(window), float(scale), out.data_ptr(),
-                                     workspace.data_ptr(), workspace.numel(), int(num_splits),
+                                     workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), int(num_splits),
                                      _stream_on(pool, stream)), "paged_gqa_decode_host")
     return out
 

@@ -156,3 +156,38 @@ def test_decodes_on_a_given_stream_without_a_workspace(as_int):
         assert torch.equal(got, outs[i % 3 if kw else 1][1].cpu().view(6, 8, 64))
         assert torch.equal(host[i], outs[1][1].cpu().view(6, 8, 64))
     pool.close()
+
+
+def test_decodes_refuse_outputs_and_workspaces():
+    """Raised before anything is launched; a larger output and a workspace of another type are
+    fine."""
+    b = Batch([40, 30], [1, 1], hkv=2, seed=9)
+    pool, q = b.pool(), b.rows(4, packed=False)
+    dq, table, lens = q.cuda(), b.table.cuda(), b.len_t.cuda()
+    n = pgd.paged_gqa_workspace_size_host(pool, 2, 1, 4, table.shape[1])
+    out = torch.full((3, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+
+    def calls(**kw):
+        yield lambda: pgd.paged_gqa_decode(pool, dq, table, lens, 0.1, **kw)
+        yield lambda: pgd.paged_gqa_decode_ex(pool, dq.view(2, 1, 4, 128), table, lens, 0.1, **kw)
+
+    for kw, err in ((dict(out=out.cpu()), ValueError), (dict(out=out[:1]), ValueError),
+                    (dict(out=out.float()), TypeError), (dict(workspace=ws.cpu()), ValueError),
+                    (dict(workspace=torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2]),
+                     ValueError)):
+        for call in calls(**kw):
+            with pytest.raises(err):
+                call()
+    for bad in (ws.cpu(), torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            pgd.paged_gqa_decode_host(pool, q.contiguous(), b.table, b.len_t, 0.1, workspace=bad)
+    words = torch.zeros(-(-n // 4), dtype=torch.int32, device="cuda")
+    for call in calls(out=out, workspace=words):
+        call()
+        torch.cuda.synchronize()
+        ok(pool)
+        check_rows(b, out.cpu(), q, 0.1, decode=True)
+        assert torch.all(out[2] == 7)
+        out[:2] = 0
+    pool.close()
