@@ -371,9 +371,9 @@ int paged_gqa_attend(pgd_pool_t pool, const void *q, int64_t q_stride, int total
  *                quarter of the cap, not of the row's largest score, and rounds them to bfloat16
  *                (8-bit pages with scales per block: neither): cached values below 2^36 in
  *                magnitude
- *   slopes       [Hq] float32, device, 4-byte aligned, finite, or NULL.  Scores and bias are
- *                summed in float32, in units of log 2: a bias of 2^k natural units has steps
- *                of about 2^(k-23)
+ *   slopes       [Hq] float32, device, 4-byte aligned, finite, or NULL; beyond +-2^13 they count
+ *                as that.  Scores and bias are summed in float32, in units of log 2: a bias of
+ *                2^k natural units has steps of about 2^(k-23)
  *   visible      (attend) [total][2] int32, device, 8-byte aligned, or NULL: the row sees
  *                tokens [first, end) of its sequence alone, of those that causality and the
  *                window let it see.  Packed documents: where a row's document begins and ends;

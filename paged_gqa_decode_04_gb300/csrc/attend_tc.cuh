@@ -984,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int pos = 0;        // of the row's token
             if ((MOD & kBias) && at_row < rows) {
                 const int i = mine.token;
-                slope = __ldg(a.slopes + head * a.group + mine.rem) * 1.4426950408889634f;
+                slope = slope_of(a.slopes + head * a.group + mine.rem);
                 pos = s.len - s.n + i;
                 if (prefix)
                     pos = __ldg(a.r.lens + (s.row0 + i) / a.q_len) - a.q_len + i % a.q_len;

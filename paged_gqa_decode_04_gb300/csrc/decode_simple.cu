@@ -17,6 +17,7 @@
 #include <math.h>
 
 #include "partition.cuh"
+#include "softcap.cuh"
 
 namespace pgd {
 namespace {
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kSimpleThreads) decode_simple_kernel(DecodeArg
 
         for (int j = warp; j < G; j += kSimpleWarps) {
             const int h = kvh * G + j;
-            const float slope = a.slopes ? a.slopes[h] * 1.4426950408889634f : 0.f;
+            const float slope = a.slopes ? slope_of(a.slopes + h) : 0.f;
             float qf[DPL], o[DPL];
             const T* qrow = q + ((int64_t)b * a.hq + h) * D + lane * DPL;
 #pragma unroll

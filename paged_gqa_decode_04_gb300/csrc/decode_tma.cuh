@@ -71,7 +71,6 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 // this many tiles per CTA: tiny calls then split runs into fewer pieces.
 constexpr int kMinTilesPerCta = 2;
 constexpr int kSmemBudget = 227 * 1024;
-constexpr float kLog2e = 1.4426950408889634f;  // slopes are given in natural units
 
 // ----------------------------------------------------------------- PTX wrappers
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -697,8 +696,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if constexpr (C::EX) {
             if (a.slopes) {
                 const float* sl = a.slopes + (int64_t)q_kvh * G;
-                sl0 = row0_ok ? __ldg(sl + row0 % G) * kLog2e : 0.f;
-                sl1 = row1_ok ? __ldg(sl + row1 % G) * kLog2e : 0.f;
+                sl0 = row0_ok ? slope_of(sl + row0 % G) : 0.f;
+                sl1 = row1_ok ? slope_of(sl + row1 % G) : 0.f;
             }
         }
         if constexpr (C::FP8) {

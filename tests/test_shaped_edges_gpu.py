@@ -191,3 +191,47 @@ def test_decodes_refuse_outputs_and_workspaces():
         assert torch.all(out[2] == 7)
         out[:2] = 0
     pool.close()
+
+
+# Slopes whose bias is beyond float32 at the distances of a test, on both sides of the one from
+# which on they count alike, and an ordinary one.  Raw scores differ by far less than 2^13, so
+# that all but the last leave one token, the nearest or the farthest.
+STEEP = torch.tensor([3.4e38, -1e30, 2.0 ** 25, -2.0 ** 20, 9000.0, 1.0])
+
+
+@pytest.mark.parametrize("pages,scales,d", [("f32", "head", 128), ("f32", "head", 64),
+                                            ("bf16", "head", 64), ("bf16", "head", 128),
+                                            ("e4m3", "head", 128), ("e4m3", "block", 128),
+                                            ("int8", "head", 128), ("int8", "block", 128)])
+def test_decode_steep_slopes(pages, scales, d):
+    b = Batch([1, 300, 40, 1200], [1] * 4, hkv=2, d=d, pages=pages, scales=scales, seed=1)
+    q = b.rows(6, packed=False)
+    pool = b.pool()
+    for cap in (0.0, 20.0):
+        got = pgd.paged_gqa_decode_ex(pool, q.view(4, 1, 6, d).cuda(), b.table.cuda(),
+                                      b.len_t.cuda(), 0.1, softcap=cap, slopes=STEEP.cuda())
+        ok(pool)
+        got = got.cpu().view(4, 6, d)
+        if pages != "f32":
+            check_rows(b, got, q, 0.1, decode=True, softcap=cap, slopes=STEEP)
+            continue
+        want, _ = shaped.attend(q, b.k, b.v, None, None, b.cu, b.table, b.lens, 0.1, softcap=cap,
+                                slopes=STEEP)
+        for r, y in want.items():
+            assert (got[r].double() - y).abs().max() <= 1e-5
+    pool.close()
+
+
+@pytest.mark.parametrize("pages,scales", [("bf16", "head"), ("e4m3", "head"), ("e4m3", "block"),
+                                          ("int8", "head"), ("int8", "block")])
+def test_attend_steep_slopes(pages, scales):
+    b = Batch([300, 140], [130, 140], hkv=2, pages=pages, scales=scales, seed=2)
+    q = b.rows(6)
+    pool, dq, where = b.pool(), b.to(q), b.where()
+    for causal in (True, False):
+        for cap in (0.0, 20.0):
+            got = pgd.paged_gqa_attend(pool, dq, *where, 0.1, causal=causal, softcap=cap,
+                                       slopes=STEEP.cuda()).cpu()
+            ok(pool)
+            check_rows(b, got, q, 0.1, causal=causal, softcap=cap, slopes=STEEP)
+    pool.close()
