@@ -373,7 +373,8 @@ int paged_gqa_attend(pgd_pool_t pool, const void *q, int64_t q_stride, int total
  *                magnitude
  *   slopes       [Hq] float32, device, 4-byte aligned, finite, or NULL; beyond +-2^13 they count
  *                as that.  Scores and bias are summed in float32, in units of log 2: a bias of
- *                2^k natural units has steps of about 2^(k-23)
+ *                2^k natural units has steps of about 2^(k-23) (attend: the bias less that of
+ *                the token the row sees for which it is largest)
  *   visible      (attend) [total][2] int32, device, 8-byte aligned, or NULL: the row sees
  *                tokens [first, end) of its sequence alone, of those that causality and the
  *                window let it see.  Packed documents: where a row's document begins and ends;

@@ -982,12 +982,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float slope = 0.f;  // in base-2 units
             int pos = 0;        // of the row's token
+            // A row's bias is taken relative to that of the token that it sees for which it is
+            // largest, so that it is small where weights are not, and its rounding, 2^-24 of it,
+            // does not reach them, however far away all that the row sees lies.  (Relative to
+            // the row's own token all that lies 40000 tokens off at a slope of 2^13 had exponents
+            // off by 16, and f16 weights overflowed.)  That token is |shift| away: the nearest one,
+            // on its side, or for slopes below 0 the farthest, on either side (shift < 0).
+            int shift = 0;
             if ((MOD & kBias) && at_row < rows) {
                 const int i = mine.token;
                 slope = slope_of(a.slopes + head * a.group + mine.rem);
                 pos = s.len - s.n + i;
                 if (prefix)
                     pos = __ldg(a.r.lens + (s.row0 + i) / a.q_len) - a.q_len + i % a.q_len;
+                if (my_hi > my_lo)
+                    shift = slope < 0.f ? -max(abs(pos - my_lo), abs(pos - (my_hi - 1)))
+                                        : min(max(pos, my_lo), my_hi - 1) - pos;
             }
             const uint32_t lanes = uint32_t(warp % 4 * 32) << 16;
             const uint32_t ts = tmem + lanes + blk * kTile;
@@ -1044,7 +1054,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const int t0 = tile_at(j) * kTile;
-                const float far = float(t0 - pos);
+                // slope (|shift| - |p - t|) as -slope |t - (p + shift)|; with slopes below 0
+                // slope |t - (p -+ |shift|)| for tokens behind and ahead of the row's own, and as it
+                // stands in the tile that holds that: lines either way where `straight`
+                int moved = shift;
+                float fall = -slope, more = 0.f;
+                if (kBiased && !kLine && slope < 0.f) {
+                    const bool back = t0 + kTile - 1 <= pos, ahead = t0 >= pos;
+                    if (!back) moved = ahead ? -shift : 0;
+                    if (back || ahead)
+                        fall = slope;
+                    else
+                        more = -slope * float(shift);
+                }
+                const float far = float(t0 - (pos + moved));
                 uint32_t x[kHalf];
                 auto load = [&](int h) {
                     tmem_ld32(ts + h * kHalf, x);
@@ -1131,8 +1154,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (kBiased && kLine)
                             b = add2(steps[i], b);
                         else if (kBiased)
-                            b = pair(fmaf(-slope, fabsf(at + float(2 * i)), add),
-                                     fmaf(-slope, fabsf(at + float(2 * i + 1)), add));
+                            b = pair(fmaf(fall, fabsf(at + float(2 * i)), add),
+                                     fmaf(fall, fabsf(at + float(2 * i + 1)), add));
                         if constexpr (kCapped) {
                             const uint64_t y = mul2(r, kk), z = mul2(y, y);
                             uint64_t p = poly[kTerms - 1];
@@ -1168,7 +1191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int g = 0; g < kHalf / 8; ++g) {
                                     float y[8];
                                     uint64_t e[4];
-                                    exponents(h, g, 0.f, e);
+                                    exponents(h, g, more, e);
 #pragma unroll
                                     for (int i = 0; i < 4; ++i)
                                         unpair(e[i], y[2 * i], y[2 * i + 1]);
@@ -1200,6 +1223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 float off = m == -INFINITY ? 0.f : -m;
                 if (kF16 && !PB) off += kLift;
+                if (kBiased) off += more;
                 uint64_t sum[2] = {0, 0};
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
@@ -1268,7 +1292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float4* const sc = reinterpret_cast<const float4*>(
                     smem + L::kScales + (PB ? (j - T0) % L::kScaleTiles * L::kScaleBytes : 0));
                 if (PB && sc[kTile / 8].x != vgain) return false;
-                const float far = float(tile_at(j) * kTile - pos);
+                const float far = float(tile_at(j) * kTile - (pos + shift));
                 float off = m == -INFINITY ? 0.f : -m;
                 if (kF16 && !PB) off += kLift;
                 const float c = fmaf(slope, far, off);
@@ -1498,6 +1522,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m = -INFINITY;
                 l = 0.f;
             }
+            // to be joined with a decode's part, whose bias is the whole one
+            if ((MOD & kBias) && prefix) m = fmaf(-slope, fabsf(float(shift)), m);
         } else if (early) {
             // A block without a tile has no use for its queries, but results() writes to where
             // they are on their way to: rows whose copies other threads of the block started.

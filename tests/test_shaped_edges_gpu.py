@@ -7,7 +7,7 @@ import paged_gqa_decode_04_gb300 as pgd
 from oracle import shaped
 from page_ops_cases import Batch
 from paged_gqa_decode_04_gb300 import _lib
-from shaped_cases import alibi, check_rows
+from shaped_cases import alibi, check_rows, group_tables, shared_batch
 
 pytestmark = pytest.mark.gpu
 
@@ -234,4 +234,68 @@ def test_attend_steep_slopes(pages, scales):
                                        slopes=STEEP.cuda()).cpu()
             ok(pool)
             check_rows(b, got, q, 0.1, causal=causal, softcap=cap, slopes=STEEP)
+    pool.close()
+
+
+@pytest.mark.parametrize("pages,scales", [("bf16", "head"), ("e4m3", "head"), ("e4m3", "block"),
+                                          ("int8", "head")])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_bias_of_what_is_far_away(pages, scales, causal):
+    """Rows that see only tokens far behind, far ahead or on one side of themselves.  Biases reach
+    2^25 in units of log 2 there; what is left of them among the tokens a row sees is below 2^21
+    at the slopes where one token is left, and below 2^10 at the others."""
+    b = Batch([3000, 200], [3000, 200], hkv=1, pages=pages, scales=scales, seed=3)
+    vis = torch.zeros(b.total, 2, dtype=torch.int32)
+    vis[0::4] = torch.tensor([0, 100])
+    vis[1::4] = torch.tensor([2900, 3000])
+    vis[2::4] = torch.tensor([1400, 1500])
+    vis[3::64] = torch.tensor([1490, 1500])
+    slopes = torch.cat([STEEP, alibi(2)])
+    q = b.rows(8)
+    pool, dq, where = b.pool(), b.to(q), b.where()
+    got = pgd.paged_gqa_attend(pool, dq, *where, 0.1, causal=causal, slopes=slopes.cuda(),
+                               visible=vis.cuda()).cpu()
+    ok(pool)
+    pool.close()
+    check_rows(b, got, q, 0.1, causal=causal, slopes=slopes, visible=vis)
+
+
+@pytest.mark.parametrize("pages,scales", [("bf16", "head"), ("e4m3", "head"), ("e4m3", "block"),
+                                          ("int8", "head")])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_bias_of_what_is_very_far_away(pages, scales, causal):
+    """The same at the end of a long sequence, where whole biases reach 2^29 in units of log 2:
+    steps of 32, beyond what an f16 weight can hold."""
+    b = Batch([40000], [40], hkv=1, pages=pages, scales=scales, seed=5)
+    vis = torch.zeros(40, 2, dtype=torch.int32)
+    vis[0::2] = torch.tensor([0, 300])
+    vis[1::2] = torch.tensor([64, 1000])
+    slopes = torch.cat([STEEP, alibi(2)])
+    q = b.rows(8)
+    pool, dq, where = b.pool(), b.to(q), b.where()
+    got = pgd.paged_gqa_attend(pool, dq, *where, 0.1, causal=causal, slopes=slopes.cuda(),
+                               visible=vis.cuda()).cpu()
+    ok(pool)
+    pool.close()
+    check_rows(b, got, q, 0.1, causal=causal, slopes=slopes, visible=vis)
+
+
+@pytest.mark.parametrize("pages,scales", [("bf16", "head"), ("e4m3", "head"), ("int8", "block")])
+@pytest.mark.parametrize("q_len", [1, 3])
+def test_shared_prefix_with_steep_slopes(q_len, pages, scales):
+    """A prefix and own tokens whose biases differ by up to 2^24: joined by what they come to."""
+    groups, n = [(0, 3), (3, 5)], [1500, 77]
+    b = shared_batch([900, 3, 40, 5, 700], groups, n, q_len, hkv=2, pages=pages, scales=scales,
+                     seed=4)
+    slopes = torch.cat([STEEP, alibi(2)])
+    q = b.rows(8, packed=False)
+    pool = b.pool()
+    cu, shared = group_tables(groups, n)
+    for cap in (0.0, 20.0):
+        got = pgd.paged_gqa_decode_shared(pool, q.view(5, q_len, 8, 128).cuda(), cu, shared,
+                                          b.table.cuda(), b.len_t.cuda(), 0.1, softcap=cap,
+                                          slopes=slopes.cuda())
+        ok(pool)
+        check_rows(b, got.cpu().view(5 * q_len, 8, 128), q, 0.1, decode=True, softcap=cap,
+                   slopes=slopes)
     pool.close()
