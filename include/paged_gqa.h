@@ -367,10 +367,9 @@ int paged_gqa_attend(pgd_pool_t pool, const void *q, int64_t q_stride, int total
  * with p as in the plain call: Lb - n_b + i for query i of the n_b of a sequence (causal or
  * not), Lb - q_len + i in a decode.
  *   softcap      0 (none) or 2^-64 .. 2^64.  tanh is taken to 2^-20 of its size or better.  An
- *                attention with a cap up to 55 and no slopes keeps its weights relative to a
- *                quarter of the cap, not of the row's largest score, and rounds them to bfloat16
- *                (8-bit pages with scales per block: neither): cached values below 2^36 in
- *                magnitude
+ *                attention over bfloat16 pages with a cap up to 55 and no slopes keeps its weights
+ *                relative to a quarter of the cap, not to the row's largest score: cached values
+ *                below 2^36 in magnitude
  *   slopes       [Hq] float32, device, 4-byte aligned, finite, or NULL; beyond +-2^13 they count
  *                as that.  Scores and bias are summed in float32, in units of log 2: a bias of
  *                2^k natural units has steps of about 2^(k-23) (attend: the bias less that of

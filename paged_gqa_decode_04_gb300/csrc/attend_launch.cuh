@@ -75,10 +75,7 @@ cudaError_t launch_shaped(Args& a, const Pool& p, const PageMaps& maps, cudaStre
         return a.cap > 0.f ? launch<D, PAGE, PB, kShaped | kCap | kBias>(a, p, maps, s)
                            : launch<D, PAGE, PB, kShaped | kBias>(a, p, maps, s);
     if (a.cap == 0.f) return launch<D, PAGE, PB, kShaped>(a, p, maps, s);
-    // with scales per block the maximum is found all the same: its one pass more costs less than
-    // the widening to bfloat16 (prefix of 3 prompts, 32/8 heads: 417 against 426 us; with scales
-    // per head 128 requests behind 32768 tokens take 258 instead of 271)
-    if constexpr (!PB)
+    if constexpr (PAGE == PGD_BF16)
         if (a.cap <= kFixedMost) return launch<D, PAGE, PB, kShaped | kCap | kFixed>(a, p, maps, s);
     return launch<D, PAGE, PB, kShaped | kCap>(a, p, maps, s);
 }

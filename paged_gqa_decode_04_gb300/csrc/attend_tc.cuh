@@ -148,9 +148,10 @@ struct Args {
 // and shared prefixes; with kCap and kBias besides, scores capped and less slope * distance.
 // kFixed: capped, and weights relative to a quarter of the cap instead of the row's maximum, which
 // then need not be found (the same prompts, at that stage 480 -> 400 us).  For caps up to
-// kFixedMost base-2 units, and with bfloat16 operands over 8-bit pages too (in which codes are
-// exact): weights are between 2^-100 and 2^60, where bfloat16 and float32 are as precise as near
-// 1, and sums over 2^31 tokens stay finite for values below 2^36.
+// kFixedMost base-2 units and bfloat16 pages: weights are between 2^-100 and 2^60, where bfloat16
+// and float32 are as precise as near 1, and sums over 2^31 tokens stay finite for values below
+// 2^36.  f16, which weights over 8-bit pages are held in, does not reach that far, and bfloat16
+// there gained 4% (128 requests behind two prompts 271 -> 259 us) for three bits of each weight.
 constexpr int kShaped = 1, kCap = 2, kBias = 4, kFixed = 8;
 constexpr float kFixedMost = 80.f;
 
@@ -417,11 +418,6 @@ template <int PAGE>
 __device__ __forceinline__ uint32_t operand2(float lo, float hi) {
     return PAGE == PGD_BF16 ? bf16x2(lo, hi) : f16x2(lo, hi);
 }
-// Exact for codes: 8 bits or fewer.
-__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t two) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
-    return bf16x2(f.x, f.y);
-}
 // Four codes to two pairs of f16.
 template <int PAGE>
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
@@ -450,7 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap map_v) {
     using L = Layout<D, PAGE, PB>;
     constexpr bool kQ8 = L::kQ8;
-    constexpr bool kF16 = kQ8 && !(MOD & kFixed);  // the products' operands: f16, else bfloat16
+    static_assert(!kQ8 || !(MOD & kFixed), "weights relative to a fixed reference are bfloat16");
+    constexpr bool kF16 = kQ8;  // the products' operands: f16, else bfloat16
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
@@ -1569,10 +1566,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     widen4<PAGE>(x[i].y, y[2], y[3]);
                     widen4<PAGE>(x[i].z, y[4], y[5]);
                     widen4<PAGE>(x[i].w, y[6], y[7]);
-                    if (!kF16) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = f16x2_to_bf16x2(y[e]);
-                    }
                     const int t = tj * kTile + r;
                     if (edge && (t < lo || t >= hi)) {  // V rows no query sees
 #pragma unroll

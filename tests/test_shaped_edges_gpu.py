@@ -7,7 +7,7 @@ import paged_gqa_decode_04_gb300 as pgd
 from oracle import shaped
 from page_ops_cases import Batch
 from paged_gqa_decode_04_gb300 import _lib
-from shaped_cases import alibi, check_rows, group_tables, shared_batch
+from shaped_cases import alibi, check_rows, group_tables, shared_batch, tail
 
 pytestmark = pytest.mark.gpu
 
@@ -299,3 +299,37 @@ def test_shared_prefix_with_steep_slopes(q_len, pages, scales):
         check_rows(b, got.cpu().view(5 * q_len, 8, 128), q, 0.1, decode=True, softcap=cap,
                    slopes=slopes)
     pool.close()
+
+
+def check_rows_f16(b, got, q, scale, low, **kw):
+    """The definition's rows, to the output's rounding, 2^-8, and weights of f16, 2^-11; 2^-12 for
+    the rest and `low` a token for f16 below its normal numbers, as in check_rows."""
+    want, size = shaped.attend(q, b.k, b.v, b.k_scale, b.v_scale, b.cu, b.table, b.lens, scale,
+                               **kw)
+    for row, y in want.items():
+        tol = 2.0 ** -8 * y.abs() + (2.0 ** -11 + 2.0 ** -12) * size[row] + low * max(b.lens)
+        err = (got[row].double() - y).abs()
+        assert torch.all(err <= tol), (row, float((err - tol).max()))
+
+
+@pytest.mark.parametrize("cap", [2.0, 30.0, 50.0, 60.0])
+@pytest.mark.parametrize("pages,scales", [("e4m3", "head"), ("int8", "head"), ("e4m3", "block")])
+def test_capped_weights_over_8_bit_pages_keep_f16(pages, scales, cap):
+    """As without a cap: weights of 11 bits in the attention and in a shared prefix."""
+    b = Batch([300, 160], [100, 160], hkv=2, pages=pages, scales=scales, seed=7)
+    q = b.rows(6) * 3
+    pool = b.pool()
+    got = pgd.paged_gqa_attend(pool, b.to(q), *b.where(), 0.1, softcap=cap).cpu()
+    ok(pool)
+    pool.close()
+    check_rows_f16(b, got, q, 0.1, tail(b, False), softcap=cap)
+    groups, n = [(0, 4)], [512]
+    b = shared_batch([1, 30, 100, 7], groups, n, hkv=2, pages=pages, scales=scales, seed=8)
+    q = b.rows(6, packed=False) * 3
+    pool = b.pool()
+    cu, shared = group_tables(groups, n)
+    got = pgd.paged_gqa_decode_shared(pool, q.cuda(), cu, shared, b.table.cuda(), b.len_t.cuda(),
+                                      0.1, softcap=cap).cpu()
+    ok(pool)
+    pool.close()
+    check_rows_f16(b, got, q, 0.1, tail(b, True), softcap=cap)
