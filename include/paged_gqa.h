@@ -158,7 +158,9 @@ int paged_kv_pool_destroy(pgd_pool_t pool);
  * table and one counter word per split run.  It must be zero-filled before
  * its first use; every call that completes leaves it ready for the next one
  * (each run's count back at zero; a flag bit beside it alternates), so a
- * workspace can be reused call after call.  After a call that latched
+ * workspace can be reused call after call, by calls of fewer sequences than
+ * it was sized for too (of the same Hq, Hkv, D, q_len and num_splits: zero it
+ * between calls that differ in those).  After a call that latched
  * PGD_ERR_TIMEOUT, zero it again.
  */
 int paged_gqa_workspace_size(pgd_pool_t pool, int B, int Hq, int num_splits, size_t *bytes);
@@ -276,10 +278,9 @@ size_t paged_gqa_noalloc_scratch_bytes(void);
  * split runs are merged inside the decode kernel (plan merge 0 where
  * paged_gqa_plan reports 2), so that only one kernel writes over the link.
  *   workspace    device buffer of at least paged_gqa_workspace_size_host
- *                bytes, 256-byte aligned; its first
- *                paged_gqa_workspace_size_ex bytes are the decode workspace
- *                (zero-filled before first use, reusable as described there),
- *                the rest is staging room for q, block_table, seq_lens and out
+ *                bytes, 256-byte aligned: a decode workspace
+ *                (zero-filled before first use, reusable as described there)
+ *                and staging room for q, block_table, seq_lens and out
  * Arguments, shapes, results and errors otherwise as paged_gqa_decode_ex.
  * Returns PGD_ERR_CUDA if a staging copy cannot be enqueued.
  */

@@ -423,6 +423,7 @@ int decode_ex_impl(pgd_pool_t pool, const void* q, int B, int q_len, int Hq,
     }
     if (B == 0) return PGD_OK;
     if (out_on_host && plan.merge_variant == 2) plan.merge_variant = 0;
+    place_at_end(&wl, workspace_bytes);
 
     DeviceGuard g(p.device);
     if (!g.ok) return PGD_ERR_CUDA;
@@ -538,8 +539,11 @@ int paged_gqa_decode_host(pgd_pool_t pool, const void* h_q, int B, int q_len, in
                                    num_splits, stream);
     if (!h_q || !h_out || !h_block_table || !h_seq_lens || !workspace) return PGD_ERR_ARG;
     const Pool& p = pool->p;
-    const HostLayout hl = host_layout(p, dec, B, q_len, Hq, max_blocks);
+    HostLayout hl = host_layout(p, dec, B, q_len, Hq, max_blocks);
     if (!aligned(workspace, 256) || workspace_bytes < hl.total) return PGD_ERR_WORKSPACE;
+    // the staging room at the end, like all but the counters (place_at_end)
+    const size_t by = workspace_bytes / 256 * 256 - hl.total;
+    for (size_t* off : {&dec, &hl.q_off, &hl.bt_off, &hl.sl_off, &hl.out_off}) *off += by;
 
     DeviceGuard g(p.device);
     if (!g.ok) return PGD_ERR_CUDA;

@@ -130,6 +130,16 @@ struct WorkspaceLayout {
 // `rows` = query rows per KV head: q_len * G.
 WorkspaceLayout workspace_layout(int B, int hkv, int rows, int hg, int d, int parts);
 
+// All but the counters at the end of a workspace of `bytes` (w->total or more).  A call's counters
+// have to be zero when it starts, so calls of fewer sequences must leave nothing where those of
+// more lie: counters grow from the start with B, the rest, which grows with B too, ends at the end.
+inline void place_at_end(WorkspaceLayout* w, size_t bytes) {
+    const size_t by = bytes / 256 * 256 - w->total;
+    w->tile_base_off += by;
+    w->part_lse_off += by;
+    w->part_o_off += by;
+}
+
 // Every argument check of a decode call (paged_gqa_decode_ex's contract), in
 // the order the entry points apply them; fills the plan and, for B > 0, the
 // workspace layout.  PGD_OK, or the status the call returns before anything

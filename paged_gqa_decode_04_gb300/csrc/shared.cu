@@ -79,8 +79,14 @@ extern "C" int paged_gqa_decode_shared(pgd_pool_t pool, const void* q, int B, in
         if (!cu_groups || !shared_lens) return PGD_ERR_ARG;
         if (!is_aligned(cu_groups, 4) || !is_aligned(shared_lens, 4)) return PGD_ERR_ALIGN;
     }
-    const SharedLayout sl = shared_layout(p, wl.total, B, q_len, Hq, num_groups);
+    SharedLayout sl = shared_layout(p, wl.total, B, q_len, Hq, num_groups);
     if (workspace_bytes < sl.total) return PGD_ERR_WORKSPACE;
+    // at the end, so that a decode of more sequences finds its counters as it left them
+    const size_t by = workspace_bytes / 256 * 256 - sl.total;
+    place_at_end(&wl, wl.total + by);
+    for (size_t* off : {&sl.starts_off, &sl.row_lse_off, &sl.row_o_off, &sl.pre_lse_off,
+                        &sl.pre_o_off})
+        *off += by;
     const int group = Hq / p.hkv, per = group * q_len;
     const int64_t pieces = max_pieces(B, num_groups, per, attend::kRowShift, 1);
     if ((int64_t)B * q_len * Hq > INT32_MAX / 2) return PGD_ERR_SHAPE;

@@ -333,3 +333,62 @@ def test_capped_weights_over_8_bit_pages_keep_f16(pages, scales, cap):
     ok(pool)
     pool.close()
     check_rows_f16(b, got, q, 0.1, tail(b, True), softcap=cap)
+
+
+SIZES = [3, 40, 2, 64, 17, 64, 1, 33, 64]
+
+
+@pytest.mark.parametrize("pages,scales,d,heads", [("bf16", "head", 64, (2, 8)),
+                                                  ("bf16", "head", 128, (2, 8)),
+                                                  ("bf16", "head", 128, (1, 20)),
+                                                  ("bf16", "head", 128, (8, 64)),
+                                                  ("e4m3", "block", 128, (8, 64)),
+                                                  ("f32", "head", 128, (2, 8))])
+def test_one_workspace_for_batches_of_any_size(pages, scales, d, heads):
+    """A workspace sized for the largest batch, used by smaller and larger ones in turn, by plain
+    and shaped decodes and by the one with host buffers: the bits of a fresh workspace."""
+    hkv, hq = heads
+    g = torch.Generator().manual_seed(d + hq)
+    lens = torch.randint(100, 3000, (64,), generator=g).tolist()
+    b = Batch(lens, [1] * 64, hkv=hkv, d=d, pages=pages, scales=scales, seed=3)
+    q = b.rows(hq, packed=False).contiguous()
+    pool = b.pool()
+    dq, table, lens = q.cuda(), b.table.cuda(), b.len_t.cuda()
+    ws = pgd.alloc_workspace(pool, 64, hq)
+    n = pgd.paged_gqa_workspace_size_host(pool, 64, 1, hq, table.shape[1])
+    wh = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    for B in SIZES:
+        for cap in (0.0, 15.0):
+            args = (pool, dq[:B].view(B, 1, hq, d), table[:B], lens[:B], 0.1)
+            out = torch.full((B, 1, hq, d), 7.0, dtype=b.act, device="cuda")
+            pgd.paged_gqa_decode_ex(*args, softcap=cap, out=out, workspace=ws)
+            assert torch.equal(out, pgd.paged_gqa_decode_ex(*args, softcap=cap)), (B, cap)
+        got = pgd.paged_gqa_decode_host(pool, q[:B], b.table[:B], b.len_t[:B], 0.1, workspace=wh)
+        want = pgd.paged_gqa_decode_host(pool, q[:B], b.table[:B], b.len_t[:B], 0.1)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), B
+    ok(pool)
+    pool.close()
+
+
+def test_one_workspace_for_shared_and_whole_decodes():
+    """A shared decode's workspace serves decodes of its batch or fewer sequences besides."""
+    g = torch.Generator().manual_seed(1)
+    own = torch.randint(100, 900, (64,), generator=g).tolist()
+    b = shared_batch(own, [(0, 64)], [700], hkv=2, d=64, seed=4)
+    q = b.rows(8, packed=False)
+    pool = b.pool()
+    dq, table, lens = q.cuda(), b.table.cuda(), b.len_t.cuda()
+    n = torch.tensor([700], dtype=torch.int32, device="cuda")
+    ws = pgd.alloc_workspace_shared(pool, 64, 1, 8, 1)
+    for B in SIZES:
+        cu = torch.tensor([0, B], dtype=torch.int32, device="cuda")
+        args = (pool, dq[:B], cu, n, table[:B], lens[:B], 0.1)
+        x = pgd.paged_gqa_decode_shared(*args, workspace=ws)
+        assert torch.equal(x, pgd.paged_gqa_decode_shared(*args)), B
+        for size in (B, 64):
+            args = (pool, dq[:size].view(size, 1, 8, 64), table[:size], lens[:size], 0.1)
+            y = pgd.paged_gqa_decode_ex(*args, slopes=alibi(8).cuda(), workspace=ws)
+            assert torch.equal(y, pgd.paged_gqa_decode_ex(*args, slopes=alibi(8).cuda())), size
+    ok(pool)
+    pool.close()
