@@ -427,7 +427,8 @@ int paged_gqa_decode_shared(pgd_pool_t pool, const void *q, int B, int q_len, in
                             float scale, float softcap, const float *slopes, void *out,
                             void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace bytes for paged_gqa_decode_shared with num_groups groups. */
+/* Workspace bytes for paged_gqa_decode_shared with num_groups groups, enough for fewer groups (one
+ * or more) and fewer sequences too. */
 int paged_gqa_workspace_size_shared(pgd_pool_t pool, int B, int q_len, int Hq, int num_groups,
                                     size_t *bytes);
 

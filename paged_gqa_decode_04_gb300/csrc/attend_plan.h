@@ -59,13 +59,24 @@ inline int prefix_parts(int tokens, int splits) {
     return pairs < splits ? pairs : splits;
 }
 
+constexpr int kMostSplits = 64;
+
 // CTAs that a piece of 256 query rows of one KV head is given for its group's prefix: as many
 // as the GPU holds at once, for `rows` rows a KV head of `groups` groups.
 inline int prefix_splits(int64_t rows, int groups, int hkv, int num_sms) {
     int64_t pieces = (rows + (1 << kRowShift) - 1) >> kRowShift;
     if (pieces < groups) pieces = groups;
     const int64_t splits = num_sms / (pieces * hkv);
-    return splits < 1 ? 1 : splits > 64 ? 64 : int(splits);
+    return splits < 1 ? 1 : splits > kMostSplits ? kMostSplits : int(splits);
+}
+
+// The most results of query heads, rows times prefix_splits, that a batch of at most `heads` query
+// heads (rows of all KV heads) leaves, however many groups it has: a piece's 256 rows have no more
+// than their share of the GPU.  Grows with the batch, so that a workspace serves smaller ones.
+inline int64_t most_prefix_rows(int64_t heads, int num_sms) {
+    const int64_t most = int64_t(num_sms) << kRowShift;
+    const int64_t all = heads * kMostSplits;
+    return heads > most ? heads : all < most ? all : most;
 }
 
 }  // namespace attend

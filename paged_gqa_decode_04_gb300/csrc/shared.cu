@@ -35,8 +35,9 @@ SharedLayout shared_layout(const Pool& p, size_t decode_bytes, int B, int q_len,
     w.row_lse_off = w.starts_off + round_up((size_t)B * sizeof(int32_t), 256);
     w.row_o_off = w.row_lse_off + round_up(rows * sizeof(float), 256);
     w.pre_lse_off = w.row_o_off + round_up(rows * p.d * sizeof(float), 256);
-    w.pre_o_off = w.pre_lse_off + round_up(w.splits * rows * sizeof(float), 256);
-    w.total = w.pre_o_off + round_up(w.splits * rows * p.d * sizeof(float), 256);
+    const size_t most = groups > 0 ? attend::most_prefix_rows(rows, p.num_sms) : 0;
+    w.pre_o_off = w.pre_lse_off + round_up(most * sizeof(float), 256);
+    w.total = w.pre_o_off + round_up(most * p.d * sizeof(float), 256);
     return w;
 }
 

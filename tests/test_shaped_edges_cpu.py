@@ -1,4 +1,7 @@
-"""What the decodes' binding refuses before the library is called."""
+"""What the decodes' binding refuses before the library is called, and the room that shared prefixes
+need."""
+import os
+import subprocess
 import types
 
 import pytest
@@ -33,3 +36,37 @@ def test_decodes_refuse_tables_elsewhere():
     i32 = dict(dtype=torch.int32)
     with pytest.raises(ValueError, match="pool's device"):
         pgd._check_decode_args(pool, q, torch.zeros(2, 3, **i32), torch.zeros(2, **i32), 3)
+
+
+def test_results_of_prefixes_fit_what_the_largest_batch_is_given(tmp_path):
+    """most_prefix_rows holds rows times prefix_splits of every batch up to its size, of any number
+    of groups, and grows with the batch."""
+    src = tmp_path / "m.cpp"
+    src.write_text("""
+#include <cstdio>
+#include <initializer_list>
+#include "attend_plan.h"
+using namespace pgd::attend;
+int main() {
+    for (int sms : {148, 152})
+        for (int hkv : {1, 2, 5, 8, 16})
+            for (int per : {1, 3, 4, 8, 20, 64}) {          // rows of a sequence and KV head
+                long long before = 0;
+                for (int B = 1; B < 700; B += B < 80 ? 1 : 13) {
+                    const long long heads = (long long)B * per * hkv;
+                    const long long most = most_prefix_rows(heads, sms);
+                    if (most < before) return printf("falls %d %d %d\\n", hkv, per, B), 1;
+                    before = most;
+                    for (int g = 1; g <= B; ++g)
+                        if (heads * prefix_splits((long long)B * per, g, hkv, sms) > most)
+                            return printf("small %d %d %d %d\\n", hkv, per, B, g), 1;
+                }
+            }
+    printf("fits\\n");
+}
+""")
+    inc = os.path.join(os.path.dirname(os.path.abspath(pgd.__file__)), "csrc")
+    exe = tmp_path / "m"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I" + inc, str(src), "-o", str(exe)], check=True)
+    res = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert res.returncode == 0 and res.stdout == "fits\n", res.stdout

@@ -392,3 +392,26 @@ def test_one_workspace_for_shared_and_whole_decodes():
             assert torch.equal(y, pgd.paged_gqa_decode_ex(*args, slopes=alibi(8).cuda())), size
     ok(pool)
     pool.close()
+
+
+def test_a_shared_workspace_serves_fewer_groups_and_sequences():
+    """Made for 64 sequences in 16 groups, used for 1 to 16 groups of 8 to 64."""
+    own = [1 + 7 * i % 50 for i in range(64)]
+    b = shared_batch(own, [(0, 64)], [300], hkv=8, seed=9)
+    q = b.rows(64, packed=False)
+    pool = b.pool()
+    dq, table, lens = q.cuda(), b.table.cuda(), b.len_t.cuda()
+    ws = pgd.alloc_workspace_shared(pool, 64, 1, 64, 16)
+    for B, groups in ((64, 16), (64, 1), (32, 2), (32, 1), (8, 8), (8, 1), (64, 3)):
+        cu = torch.tensor([B * g // groups for g in range(groups + 1)], dtype=torch.int32)
+        n = torch.full((groups,), 300, dtype=torch.int32, device="cuda")
+        args = (pool, dq[:B], cu.cuda(), n, table[:B], lens[:B], 0.1)
+        x = pgd.paged_gqa_decode_shared(*args, workspace=ws)
+        ok(pool)
+        assert torch.equal(x, pgd.paged_gqa_decode_shared(*args))
+        if B == 64:
+            check_rows(b, x.cpu(), q, 0.1, decode=True)
+    sizes = [pgd.paged_gqa_workspace_size_shared(pool, B, 1, 64, g)
+             for B in (1, 2, 8, 33, 64, 200, 1000) for g in (1, 5, 70)]
+    assert sizes == sorted(sizes)
+    pool.close()
