@@ -370,7 +370,8 @@ int paged_gqa_attend(pgd_pool_t pool, const void *q, int64_t q_stride, int total
  *   softcap      0 (none) or 2^-64 .. 2^64.  tanh is taken to 2^-20 of its size or better.  An
  *                attention over bfloat16 pages with a cap up to 55 and no slopes keeps its weights
  *                relative to a quarter of the cap, not to the row's largest score: cached values
- *                below 2^36 in magnitude
+ *                are below 2^36 in magnitude, and where all scores of a row are near -softcap
+ *                they count to within 2^-26 (weights are 2^-100 there)
  *   slopes       [Hq] float32, device, 4-byte aligned, finite, or NULL; beyond +-2^13 they count
  *                as that.  Scores and bias are summed in float32, in units of log 2: a bias of
  *                2^k natural units has steps of about 2^(k-23) (attend: the bias less that of
@@ -414,9 +415,11 @@ int paged_gqa_decode_shaped(pgd_pool_t pool, const void *q, int B, int q_len, in
  *   slopes       as in paged_gqa_decode_shaped; 0 and NULL for plain scores
  *   workspace    paged_gqa_workspace_size_shared bytes (at least), 256-byte aligned,
  *                zero-filled before first use; calls that may overlap need distinct ones
- * The result is that of paged_gqa_decode_ex beyond float32 rounding.  Groups that do not ascend
- * within the batch or a negative shared length latch PGD_ERR_SEQ_LEN, and every sequence is
- * then read whole.  A block id out of range in a shared prefix makes the rows of its whole
+ * The result is that of paged_gqa_decode_ex but for the weights' rounding to the 16 bits of the
+ * products, in each relative to other references: both are within 2^-8 (f16, over 8-bit pages:
+ * 2^-11) of the weighted mean of |v|, and the output's rounding, of the exact one.  Groups that
+ * do not ascend within the batch or a negative shared length latch PGD_ERR_SEQ_LEN, and every
+ * sequence is then read whole.  A block id out of range in a shared prefix makes the rows of its whole
  * group NaN.  bfloat16 and 8-bit pools (PGD_ERR_UNSUPPORTED for float32); over 8-bit pages the
  * limits of paged_gqa_attend hold for the prefix, and with a cap those of
  * paged_gqa_attend_shaped.  Three kernel launches.

@@ -883,7 +883,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int u = 0; u < kR; ++u, at.next()) {
                         if (r0 + u * step + line >= rows) continue;
-                        // a row that sees a token has a sum of 1 or more; NaN where a part failed
+                        // A row that sees a token has a sum of 1 or more relative to a running
+                        // maximum, and of 2^-100 to 2^91 relative to kFixed's reference: both in
+                        // __fdividef's range (1 over more than 2^126 is 0), which kFixedMost is
+                        // tied to.  NaN where a part failed.
                         const float inv = sum[u] == 0.f ? 0.f : __fdividef(1.f, sum[u]);
                         if (prefix) {  // this CTA's part of the row
                             const int64_t r = (int64_t)share * a.r.total * a.hq + vector();

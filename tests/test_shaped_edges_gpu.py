@@ -415,3 +415,25 @@ def test_a_shared_workspace_serves_fewer_groups_and_sequences():
              for B in (1, 2, 8, 33, 64, 200, 1000) for g in (1, 5, 70)]
     assert sizes == sorted(sizes)
     pool.close()
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -18, 2.0 ** -24, 2.0 ** -30, 2.0 ** 30])
+def test_values_where_all_scores_are_at_the_lower_end_of_the_cap(size):
+    """Weights near 2^-100 of a fixed reference: values of any size to the bound's steps and 2^-26,
+    2^-126 over the weight."""
+    b = Batch([700, 130], [140, 130], hkv=1, d=64, seed=13)
+    b.k[:] = torch.where(b.k.isnan(), b.k, torch.ones((), dtype=b.k.dtype))
+    b.v *= size
+    q = -torch.ones(b.total, 2, 64, dtype=torch.bfloat16)
+    pool, where = b.pool(), b.where()
+    for cap in (55.0, 30.0):
+        for causal in (True, False):
+            got = pgd.paged_gqa_attend(pool, q.cuda(), *where, 40.0, causal=causal,
+                                       softcap=cap).cpu()
+            ok(pool)
+            want, most = shaped.attend(q, b.k, b.v, None, None, b.cu, b.table, b.lens, 40.0,
+                                       causal=causal, softcap=cap)
+            for row, y in want.items():
+                tol = 2.0 ** -8 * y.abs() + (2.0 ** -8 + 2.0 ** -12) * most[row] + 2.0 ** -26
+                assert torch.all((got[row].double() - y).abs() <= tol), (row, cap)
+    pool.close()
