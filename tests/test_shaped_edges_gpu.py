@@ -437,3 +437,63 @@ def test_values_where_all_scores_are_at_the_lower_end_of_the_cap(size):
                 tol = 2.0 ** -8 * y.abs() + (2.0 ** -8 + 2.0 ** -12) * most[row] + 2.0 ** -26
                 assert torch.all((got[row].double() - y).abs() <= tol), (row, cap)
     pool.close()
+
+
+@pytest.mark.parametrize("pages,scales,d", [("bf16", "head", 64), ("bf16", "head", 128),
+                                            ("e4m3", "head", 128), ("int8", "block", 128)])
+def test_plain_c_entry_points(pages, scales, d):
+    """paged_gqa_attend and paged_gqa_decode_ex of the C interface, which the binding does not
+    call, on real data: right, and the bits of the shaped ones with nothing shaped."""
+    lib = _lib.load()
+    b = Batch([300, 40, 0, 129], [100, 3, 0, 129], hkv=2, d=d, pages=pages, scales=scales, seed=6)
+    q = b.rows(6)
+    pool, dq = b.pool(), b.to(q)
+    cu, table, lens = b.where()
+    for causal, window in ((1, 0), (1, 33), (0, 0)):
+        got, same = [torch.full((b.total, 6, d), 7.0, dtype=b.act, device="cuda")
+                     for _ in range(2)]
+        first = (pool.handle, dq.data_ptr(), dq.stride(0), b.total, 6, cu.data_ptr(), 4,
+                 table.data_ptr(), table.shape[1], lens.data_ptr(), causal, window, 0.1)
+        assert lib.paged_gqa_attend(*first, got.data_ptr(), None) == 0
+        assert lib.paged_gqa_attend_shaped(*first, 0.0, None, None, same.data_ptr(), None) == 0
+        torch.cuda.synchronize()
+        ok(pool)
+        check_rows(b, got.cpu(), q, 0.1, causal=bool(causal), window=window)
+        assert torch.equal(got, same)
+    for q_len, window in ((1, 0), (3, 0), (2, 50)):
+        b.cu = torch.arange(5, dtype=torch.int32) * q_len
+        q = torch.randn((4 * q_len, 6, d), generator=b.g).to(b.act)
+        dq = q.cuda()
+        n = pgd.paged_gqa_workspace_size_ex(pool, 4, q_len, 6)
+        ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        got, same = [torch.full((4 * q_len, 6, d), 7.0, dtype=b.act, device="cuda")
+                     for _ in range(2)]
+        torch.cuda.synchronize()
+        first = (pool.handle, dq.data_ptr(), 4, q_len, 6, table.data_ptr(), table.shape[1],
+                 lens.data_ptr(), window, 0.1)
+        last = (ws.data_ptr(), n, 0, None)
+        assert lib.paged_gqa_decode_ex(*first, got.data_ptr(), *last) == 0
+        assert lib.paged_gqa_decode_shaped(*first, 0.0, None, same.data_ptr(), *last) == 0
+        torch.cuda.synchronize()
+        ok(pool)
+        check_rows(b, got.cpu(), q, 0.1, decode=True, window=window)
+        assert torch.equal(got, same)
+    pool.close()
+
+
+def test_sequences_that_are_all_prefix():
+    """One query a sequence, and every cached token shared: nothing is left for the decode, in
+    some sequences or in any."""
+    for own in ([0, 0, 0], [0, 5, 0]):
+        for n in (256, 512, 320):
+            b = shared_batch(own, [(0, 3)], [n], hkv=2, bs=64, seed=n)
+            q = b.rows(8, packed=False)
+            pool = b.pool()
+            cu, shared = group_tables([(0, 3)], [n])
+            for kw in ({}, dict(softcap=20.0), dict(slopes=alibi(8))):
+                dev = {k: v.cuda() if torch.is_tensor(v) else v for k, v in kw.items()}
+                got = pgd.paged_gqa_decode_shared(pool, q.cuda(), cu, shared, b.table.cuda(),
+                                                  b.len_t.cuda(), 0.1, **dev)
+                ok(pool)
+                check_rows(b, got.cpu(), q, 0.1, decode=True, **kw)
+            pool.close()
