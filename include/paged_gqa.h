@@ -419,8 +419,8 @@ int paged_gqa_decode_shaped(pgd_pool_t pool, const void *q, int B, int q_len, in
  * products, in each relative to other references: both are within 2^-8 (f16, over 8-bit pages:
  * 2^-11) of the weighted mean of |v|, and the output's rounding, of the exact one.  Groups that
  * do not ascend within the batch or a negative shared length latch PGD_ERR_SEQ_LEN, and every
- * sequence is then read whole.  A block id out of range in a shared prefix makes the rows of its whole
- * group NaN.  bfloat16 and 8-bit pools (PGD_ERR_UNSUPPORTED for float32); over 8-bit pages the
+ * sequence is then read whole.  A block id out of range in a shared prefix makes the rows of its
+ * whole group NaN.  bfloat16 and 8-bit pools (PGD_ERR_UNSUPPORTED for float32); over 8-bit pages the
  * limits of paged_gqa_attend hold for the prefix, and with a cap those of
  * paged_gqa_attend_shaped.  Three kernel launches.
  */

@@ -70,7 +70,7 @@
 // Their tiles are shaped_tile and settled_tile; tiles come from the last on where there is a bias;
 // results leave from the softmax warps.  Measured against the plain kernels on the same rows
 // (32/8 heads, 4 prompts of 2006 to 3900 tokens, scores up to +-20): 362 us under a cap of 50, 343
-// without; 2048 of 8192 tokens, 64/8 heads: 400 with a bias, 340 without.  A CTA's cycles on
+// without; 2048 of 8192 tokens, 64/8 heads: 407 with a bias, 338 without.  A CTA's cycles on
 // documents of 1050 tokens packed into one of 16384 (6.7 tiles a piece, 44100): 3600 to find its
 // piece and send for the queries, 3200 for ranges, TMEM and the first barrier, 1000 and 3900 until
 // queries and first keys are there, 6400 for the first tile, 3100 for each other, 700 for the last
@@ -1055,8 +1055,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int t0 = tile_at(j) * kTile;
                 // slope (|shift| - |p - t|) as -slope |t - (p + shift)|; with slopes below 0
-                // slope |t - (p -+ |shift|)| for tokens behind and ahead of the row's own, and as it
-                // stands in the tile that holds that: lines either way where `straight`
+                // slope |t - (p -+ |shift|)| for tokens behind and ahead of the row's own, and as
+                // it stands in the tile that holds that: lines either way where `straight`
                 int moved = shift;
                 float fall = -slope, more = 0.f;
                 if (kBiased && !kLine && slope < 0.f) {
@@ -1283,8 +1283,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // first half's weights are computed against the reference so far while the largest
             // score is looked for.  That and the bias at the nearer end bound what the tile
             // brings; where it might be too much (false) nothing was handed over.  (2048 of 8192
-            // tokens, 64/8 heads: 400 us, 459 with shaped_tile alone; packed documents without a
-            // bias gain nothing, 314 against 306.)
+            // tokens, 64/8 heads: 407 us, 775 with shaped_tile alone; packed documents without a
+            // bias gained nothing, 314 against 306.)
             auto settled_tile = [&](int j) {
                 uint32_t x[kTile], w[kTile / 4];
                 uint64_t sum[2] = {0, 0};

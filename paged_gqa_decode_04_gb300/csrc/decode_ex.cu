@@ -165,9 +165,11 @@ cudaError_t launch_join_d(const DecodeArgs& a, cudaStream_t s) {
 
 cudaError_t launch_join(const DecodeArgs& a, cudaStream_t s) {
     if (a.B == 0) return cudaSuccess;
-    // more than two rounds of loads a row and few rows: its parts to four times the threads
-    // (3 drafted tokens of 16 sequences, 32 parts: 51 -> 47 us; 64 sequences of 32 heads, 19
-    // parts: 78 -> 79, so not there)
+    // More than two rounds of loads a row and few rows: its parts to four times the threads.  It
+    // turns between 1280 and 1536 rows (us of a whole call in a graph, one and four times the
+    // threads: behind 8192 tokens, 20 query heads of one KV head, 160 rows 50 and 46, 960 57 and
+    // 52, 1280 54 and 50, 2560 54 and 56; 32/8 heads behind 16384, 1024 rows 67 and 63, 1536 69
+    // both; a capped step of one sequence of 32768, 32 rows, 75 and 48).
     const int pieces = a.num_parts / (a.B * a.units) + 1;
     const bool many = (a.starts ? a.prefix_splits : 0) + pieces > 2 * kJoinBatch &&
                       (int64_t)a.B * a.q_len * a.hq <= 1024;

@@ -13,11 +13,10 @@
 // same notes say of FlashAttention's online softmax.
 //
 // merge_kernel: one warp per row of a sequence (one CTA for all rows of one: 339 us for a
-// sequence of 3000 tokens, 32/8 heads of 128, of which 270 were this merge's); used after the CUDA-core kernel, whose
-// units are single KV heads (a run is one (sequence, KV head) pair).  Runs that were not split
-// are left alone (the decode kernel wrote them), sequences of length 0 get
-// zeros, and sequences whose length is out of range get NaN and latch
-// PGD_ERR_SEQ_LEN.
+// sequence of 3000 tokens, 32/8 heads of 128, of which 270 were this merge's); used after the
+// CUDA-core kernel, whose units are single KV heads (a run is one (sequence, KV head) pair).  Runs
+// that were not split are left alone (the decode kernel wrote them), sequences of length 0 get
+// zeros, and sequences whose length is out of range get NaN and latch PGD_ERR_SEQ_LEN.
 #include <cuda_bf16.h>
 #include <math.h>
 

@@ -1,5 +1,6 @@
-"""Attention with shaped scores, decode and shared prefixes where they can go wrong: blocks of rows
-without a tile, steep and far biases, workspaces of many shapes, given streams, the C entry points."""
+"""Attention with shaped scores, decode and shared prefixes where they can go wrong: blocks of
+rows without a tile, steep and far biases, small values under a cap, workspaces of many shapes,
+given streams, the C entry points."""
 import pytest
 import torch
 
