@@ -173,7 +173,7 @@ def _check_decode_args(pool, q, block_table, seq_lens, q_dims):
             seq_lens.shape[0] != q.shape[0]):
         raise ValueError("shape mismatch between q, tables and pool")
     for t in (q, block_table, seq_lens):
-        if t.get_device() != pool.device.index or not t.is_contiguous():
+        if not t.is_cuda or t.get_device() != pool.device.index or not t.is_contiguous():
             raise ValueError("inputs must be contiguous CUDA tensors on the pool's device")
 
 
