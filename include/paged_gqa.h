@@ -369,9 +369,10 @@ int paged_gqa_attend(pgd_pool_t pool, const void *q, int64_t q_stride, int total
  * not), Lb - q_len + i in a decode.
  *   softcap      0 (none) or 2^-64 .. 2^64.  tanh is taken to 2^-20 of its size or better.  An
  *                attention over bfloat16 pages with a cap up to 55 and no slopes keeps its weights
- *                relative to a quarter of the cap, not to the row's largest score: cached values
- *                are below 2^36 in magnitude, and where all scores of a row are near -softcap
- *                they count to within 2^-26 (weights are 2^-100 there)
+ *                relative to a quarter of the cap, not to the row's largest score, unless all
+ *                that a row sees lies in one stretch of 128 tokens: cached values are below 2^36
+ *                in magnitude, and where all scores of such a row are near -softcap they count to
+ *                within 2^-26 (weights are 2^-100 there)
  *   slopes       [Hq] float32, device, 4-byte aligned, finite, or NULL; beyond +-2^13 they count
  *                as that.  Scores and bias are summed in float32, in units of log 2: a bias of
  *                2^k natural units has steps of about 2^(k-23) (attend: the bias less that of

@@ -69,7 +69,7 @@
 //     s = scale <q, k>;  s <- c tanh(s / c);  s <- s - slope |p - t|;  first <= t < end.
 // Their tiles are shaped_tile and settled_tile; tiles come from the last on where there is a bias;
 // results leave from the softmax warps.  Measured against the plain kernels on the same rows
-// (32/8 heads, 4 prompts of 2006 to 3900 tokens, scores up to +-20): 362 us under a cap of 50, 343
+// (32/8 heads, 4 prompts of 2006 to 3900 tokens, scores up to +-20): 372 us under a cap of 50, 343
 // without; 2048 of 8192 tokens, 64/8 heads: 407 with a bias, 338 without.  A CTA's cycles on
 // documents of 1050 tokens packed into one of 16384 (6.7 tiles a piece, 44100): 3600 to find its
 // piece and send for the queries, 3200 for ranges, TMEM and the first barrier, 1000 and 3900 until
@@ -152,6 +152,10 @@ struct Args {
 // and float32 are as precise as near 1, and sums over 2^31 tokens stay finite for values below
 // 2^36.  f16, which weights over 8-bit pages are held in, does not reach that far, and bfloat16
 // there gained 4% (128 requests behind two prompts 271 -> 259 us) for three bits of each weight.
+// Such a row's largest weight is rounded as all others are, which counts where they are few: a row
+// that sees tokens of one tile alone, one that not all rows see whole, has its own largest score
+// as the reference (one token: its value to the bit, off by 0.0015 otherwise; 363 -> 372 us.  The
+// sum of the rounded weights instead, 377 us, is off by up to twice a weight's rounding).
 constexpr int kShaped = 1, kCap = 2, kBias = 4, kFixed = 8;
 constexpr float kFixedMost = 80.f;
 
@@ -1042,7 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr bool kEdge = decltype(edge)::value;
                 constexpr bool kLine = decltype(straight)::value;
                 constexpr bool kCapped = (MOD & kCap) != 0, kBiased = (MOD & kBias) != 0;
-                constexpr bool kFix = (MOD & kFixed) != 0;
+                constexpr bool kFix = (MOD & kFixed) != 0 && !kEdge;
                 constexpr int kHalf = kTile / 2;
                 const float4* const sc = reinterpret_cast<const float4*>(
                     smem + L::kScales + (PB ? (j - T0) % L::kScaleTiles * L::kScaleBytes : 0));
@@ -1209,7 +1213,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!kBiased && !PB) top *= scale;  // (-infinity stays that)
                     }
                     const bool over = top > m + kGrow;
-                    if (__any_sync(0xffffffffu, over)) {
+                    if (MOD & kFixed) {
+                        if (my_hi > my_lo && my_lo >= t0 && my_hi <= t0 + kTile)
+                            m = top;  // all that the row sees is here
+                        else if (m == -INFINITY)
+                            m = 0.25f * a.cap;
+                    } else if (__any_sync(0xffffffffu, over)) {
                         float keep = 1.f;
                         if (over) {
                             keep = m == -INFINITY ? 0.f : ex2(m - top);
@@ -1218,7 +1227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (j > first) rescale(keep);
                     }
-                } else {
+                } else if (m == -INFINITY) {
                     m = 0.25f * a.cap;
                 }
                 float off = m == -INFINITY ? 0.f : -m;

@@ -498,3 +498,33 @@ def test_sequences_that_are_all_prefix():
                 ok(pool)
                 check_rows(b, got.cpu(), q, 0.1, decode=True, **kw)
             pool.close()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kw", [{}, dict(softcap=2.0), dict(softcap=50.0), dict(softcap=60.0),
+                                dict(slopes=True), dict(softcap=50.0, slopes=True)])
+def test_a_row_that_sees_one_token_is_its_value(kw, d):
+    """To the bit, over bfloat16 pages: the one weight is 1, to which a sum off by less than 2^-13
+    rounds it, and what such a sum divides is off by far less than the half step, 2^-9, that would
+    leave the value."""
+    kw = dict(kw, slopes=alibi(6).cuda()) if "slopes" in kw else kw
+    b = Batch([300, 1, 140], [300, 1, 140], hkv=2, d=d, seed=14)
+    q = b.rows(6) * 3
+    pool, dq, (cu, table, lens) = b.pool(), b.to(q), b.where()
+    tokens = [(s, t) for s, n in enumerate(b.lens) for t in range(n)]
+    values = torch.stack([b.v[int(b.table[s][t // 16]), t % 16] for s, t in tokens])
+    values = values.repeat_interleave(3, dim=1)
+    at = torch.tensor([[t, t + 1] for _, t in tokens], dtype=torch.int32, device="cuda")
+    for causal in (True, False):
+        got = pgd.paged_gqa_attend(pool, dq, cu, table, lens, d ** -0.5, causal=causal,
+                                   visible=at, **kw)
+        assert torch.equal(got.cpu(), values)
+    got = pgd.paged_gqa_attend(pool, dq, cu, table, lens, d ** -0.5, **kw).cpu()
+    first = [0, 300, 301]
+    assert torch.equal(got[first], values[first])
+    ones = torch.ones(3, dtype=torch.int32, device="cuda")
+    dq = q[first].contiguous().cuda()
+    got = pgd.paged_gqa_decode_ex(pool, dq.view(3, 1, 6, d), table, ones, d ** -0.5, **kw)
+    assert torch.equal(got.cpu().view(3, 6, d), values[first])
+    ok(pool)
+    pool.close()
