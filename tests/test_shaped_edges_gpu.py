@@ -528,3 +528,42 @@ def test_a_row_that_sees_one_token_is_its_value(kw, d):
     assert torch.equal(got.cpu().view(3, 6, d), values[first])
     ok(pool)
     pool.close()
+
+
+def test_captured_batches_of_several_sizes_share_a_workspace():
+    """Graphs of a whole and of a shared decode for 3, 64 and 17 sequences, captured over one
+    workspace each and replayed in turn: the bits of calls with workspaces of their own."""
+    g = torch.Generator().manual_seed(2)
+    own = torch.randint(50, 900, (64,), generator=g).tolist()
+    b = shared_batch(own, [(0, 64)], [600], hkv=2, d=64, seed=5)
+    q = b.rows(8, packed=False)
+    pool = b.pool()
+    dq, table, lens = q.cuda(), b.table.cuda(), b.len_t.cuda()
+    n = torch.tensor([600], dtype=torch.int32, device="cuda")
+    wd = pgd.alloc_workspace(pool, 64, 8)
+    wsh = pgd.alloc_workspace_shared(pool, 64, 1, 8, 1)
+    side, graphs = torch.cuda.Stream(), []
+    for B in (3, 64, 17):
+        cu = torch.tensor([0, B], dtype=torch.int32, device="cuda")
+        whole = (pool, dq[:B].view(B, 1, 8, 64), table[:B], lens[:B], 0.1)
+        shared = (pool, dq[:B], cu, n, table[:B], lens[:B], 0.1)
+        want = [pgd.paged_gqa_decode_ex(*whole), pgd.paged_gqa_decode_ex(*whole, softcap=9.0),
+                pgd.paged_gqa_decode_shared(*shared, softcap=9.0)]
+        outs = [torch.zeros_like(x) for x in want]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            pgd.paged_gqa_decode_ex(*whole, out=outs[0], workspace=wd)
+            pgd.paged_gqa_decode_ex(*whole, softcap=9.0, out=outs[1], workspace=wd)
+            pgd.paged_gqa_decode_shared(*shared, softcap=9.0, out=outs[2], workspace=wsh)
+        graphs.append((graph, outs, want, cu))
+    for i in (0, 1, 2, 1, 0, 0, 2, 1):
+        graph, outs, want, _ = graphs[i]
+        for x in outs:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(outs, want):
+            assert torch.equal(x, y)
+    ok(pool)
+    pool.close()
